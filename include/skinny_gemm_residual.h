@@ -80,7 +80,7 @@
 extern "C" {
 #endif
 
-#define SGR_ABI_VERSION 9
+#define SGR_ABI_VERSION 10
 
 typedef enum {
   SGR_OK = 0,

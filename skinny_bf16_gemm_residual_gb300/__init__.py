@@ -6,10 +6,15 @@ and its low-bit weight variant (FP8 E4M3 codes Wq with a per-column scale):
 
     Y[M,N] = bf16( scale[N] * A[M,K] . e4m3(Wq[N,K])^T  +  R[M,N] )
 
+and the operators between two such projections of a decode step (see
+``attention``): head norms with rotation, the append to a paged E4M3 cache,
+and attention over it.
+
 The work runs in hand-written CUDA kernels behind the C ABI declared in
-include/skinny_gemm_residual.h; this package is a ctypes binding with the
-same function names (see ``binding``), the build step (``build``) and the
-seeded synthetic input generators (``inputs``).  The library is loaded on
+include/skinny_gemm_residual.h and include/sgr_attention.h; this package is a
+ctypes binding with the same function names (see ``binding`` and
+``attention``), the build step (``build``) and the seeded synthetic input
+generators (``inputs``).  The library is loaded on
 first use; there is no CPU fallback.
 """
 from .binding import (  # noqa: F401
@@ -62,4 +67,13 @@ from .binding import (  # noqa: F401
     sgr_validate_w4_ptr,
     sgr_selftest_wait_timeout,
     sgr_selftest_streamk_abort,
+)
+from .attention import (  # noqa: F401
+    KvBatch,
+    KvCache,
+    RopeNorm,
+    kv_attention_workspace,
+    sgr_kv_append,
+    sgr_kv_attention,
+    sgr_qk_norm_rope,
 )

@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in include/skinny_gemm_residual.h.
+"""ctypes binding of the C ABI in include/skinny_gemm_residual.h and, in raw
+form, include/sgr_attention.h (its tensor-level calls are in ``attention``).
 
 Argument marshalling only: every step of the operation runs in the CUDA
 library.  Functions carry the C names.  Tensor arguments are torch CUDA
@@ -14,7 +15,7 @@ import threading
 
 from . import build as _build
 
-ABI_VERSION = 9  # must equal SGR_ABI_VERSION of the loaded library
+ABI_VERSION = 10  # must equal SGR_ABI_VERSION of the loaded library
 
 SGR_OK = 0
 SGR_ERR_NULL = 1
@@ -43,6 +44,30 @@ class sgr_group(ctypes.Structure):
                 ("ldy", ctypes.c_int64), ("M", ctypes.c_int), ("reserved", ctypes.c_int)]
 
 
+class sgr_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class sgr_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class sgr_kv_batch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("batch", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("tokens", ctypes.c_int), ("max_new", ctypes.c_int)]
+
+
+class sgr_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("table_rows", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
 class SgrError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -67,7 +92,7 @@ class sgr_config(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 
-# Entry points declared in include/skinny_gemm_residual.h.
+# Entry points declared in include/skinny_gemm_residual.h and include/sgr_attention.h.
 EXPORTS = (
     "skinny_gemm_residual",
     "skinny_gemm_residual_ex",
@@ -88,6 +113,13 @@ EXPORTS = (
     "sgr_validate_w4",
     "sgr_selftest_wait_timeout",
     "sgr_selftest_streamk_abort",
+    "sgr_qk_norm_rope",
+    "sgr_kv_append",
+    "sgr_kv_attention",
+    "sgr_kv_attention_workspace",
+    "sgr_validate_qk_norm_rope",
+    "sgr_validate_kv_append",
+    "sgr_validate_kv_attention",
 )
 
 
@@ -134,6 +166,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.sgr_validate_w4.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, I, I, I]
         lib.sgr_selftest_wait_timeout.argtypes = [U, ctypes.POINTER(ctypes.c_uint)]
         lib.sgr_selftest_streamk_abort.argtypes = [vp, vp, vp, vp, I, I, I, I, ctypes.POINTER(ctypes.c_uint)]
+        # Structures go as addresses (byref() or a structure's own address).
+        lib.sgr_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp, U, vp]
+        lib.sgr_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, U, vp]
+        lib.sgr_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I, vp, i64, U, vp]
+        lib.sgr_kv_attention_workspace.argtypes = [I, vp, vp, I, ctypes.POINTER(i64)]
+        lib.sgr_validate_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp]
+        lib.sgr_validate_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+        lib.sgr_validate_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I]
         for name in EXPORTS:
             if name != "sgr_status_string":
                 getattr(lib, name).restype = ctypes.c_int

@@ -1,9 +1,10 @@
 """Build step for the CUDA library (in-tree, sm_103a only).
 
-``build_library()`` compiles ``csrc/sgr_api.cu`` (which includes the kernels)
-with nvcc into ``_build/libskinny_gemm_residual.so`` next to this file and
-returns its path.  Rebuilds when any source or the public header is newer
-than the library.
+``build_library()`` compiles ``csrc/sgr_api.cu`` (the projections) and
+``csrc/sgr_kv.cu`` (the attention operators), each with the kernels that it
+includes, with nvcc side by side, links them into
+``_build/libskinny_gemm_residual.so`` next to this file and returns its path.
+Rebuilds when any source or public header is newer than the library.
 """
 from __future__ import annotations
 
@@ -21,8 +22,8 @@ LIB_NAME = "libskinny_gemm_residual.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
-NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-              "--expt-relaxed-constexpr"]
+NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
+UNITS = ("sgr_api.cu", "sgr_kv.cu")
 
 
 def _nvcc() -> str:
@@ -45,6 +46,17 @@ def is_stale(path: str = LIB_PATH) -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _run(commands: list[list[str]], verbose: bool) -> None:
+    """Run the commands side by side; raise for the first that fails."""
+    running = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for cmd in commands]
+    outputs = [p.communicate()[0] for p in running]
+    for cmd, p, out in zip(commands, running, outputs):
+        if p.returncode != 0:
+            raise RuntimeError(f"nvcc failed ({p.returncode}):\n{' '.join(cmd)}\n{out}")
+        if verbose:
+            print(out)
+
+
 def build_library(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
                   out_path: str = LIB_PATH) -> str:
     """Compile the library if needed; return the .so path."""
@@ -52,15 +64,17 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
         return out_path
     os.makedirs(os.path.dirname(out_path), exist_ok=True)
     tmp = out_path + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH_FLAGS, *NVCC_FLAGS, *(extra_flags or []), f"-I{INCLUDE}",
-           os.path.join(CSRC, "sgr_api.cu"), "-o", tmp]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stderr}")
-    if verbose:
-        print(res.stderr)
+    common = [_nvcc(), *(["-Xptxas=-v"] if verbose else []), *ARCH_FLAGS]
+    objects = [f"{tmp}.{unit}.o" for unit in UNITS]
+    compiles = [[*common, *NVCC_FLAGS, *(extra_flags or []), f"-I{INCLUDE}", "-c", os.path.join(CSRC, unit), "-o", obj]
+                for unit, obj in zip(UNITS, objects)]
+    try:
+        _run(compiles, verbose)
+        _run([[*common, "-shared", *objects, "-o", tmp]], False)
+    finally:
+        for obj in objects:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(tmp, out_path)
     return out_path
 

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "skinny_gemm_residual.h"
+#include "sgr_internal.h"
 #include "sgr_simt.cuh"
 #include "sgr_tc.cuh"
 #include "sgr_rows.cuh"
@@ -21,7 +22,7 @@
 
 namespace {
 
-constexpr int kMaxDevices = 64;
+using sgr::kMaxDevices;
 constexpr int kMaxDynSmem = 232448;  // 227 KB, the per-CTA opt-in limit on sm_100-class GPUs
 constexpr long long kMaxN = 1 << 24;
 constexpr long long kMaxK = 1 << 20;
@@ -255,6 +256,7 @@ int init_device(int dev) {
     if (ok == SGR_OK && sgr::pair_init_device(dev) != cudaSuccess) ok = SGR_ERR_DEVICE;
     if (ok == SGR_OK && sgr::w8_init_device() != cudaSuccess) ok = SGR_ERR_DEVICE;
     if (ok == SGR_OK && sgr::w8s_init_device() != cudaSuccess) ok = SGR_ERR_DEVICE;
+    if (ok == SGR_OK && sgr::kv_init_device(dev) != SGR_OK) ok = SGR_ERR_DEVICE;
     if (ok != SGR_OK) cudaGetLastError();
     st.sms = sms;
     st.err = errp;
@@ -1156,6 +1158,8 @@ int run_grouped(const sgr_group* groups, int num_groups, int N, int K, const sgr
 }
 
 }  // namespace
+
+int sgr::device_error_word(int dev, unsigned** word) { return error_word(dev, word); }
 
 extern "C" {
 

@@ -1,0 +1,453 @@
+// sgr_kv.cu -- C ABI of the attention operators (include/sgr_attention.h):
+// argument checks, device set-up and kernel launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+#include <utility>
+
+#include "sgr_attention.h"
+#include "sgr_internal.h"
+#include "sgr_kv_append.cuh"
+#include "sgr_kv_attn.cuh"
+
+namespace {
+
+using sgr::kMaxDevices;
+
+constexpr long long kMaxStride = 1LL << 36;  // as the row strides of skinny_gemm_residual.h
+constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxHeads = 1 << 12;
+
+// ------------------------------------------------------------ argument checks
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+struct Extent {
+  uintptr_t lo, hi;  // [lo, hi) bytes
+};
+
+bool overlap(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
+
+Extent heads_extent(const sgr_heads& x, long long tokens, int dim) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(x.data);
+  if (tokens <= 0 || x.heads <= 0) return {b, b};
+  return {b, b + 2 * static_cast<uintptr_t>((tokens - 1) * x.token_stride + (x.heads - 1) * x.head_stride + dim)};
+}
+
+// Whether two sets of head rows share elements.  Slices of one packed buffer
+// (same token stride, each row's heads within it) are told apart by their
+// place in the row; anything else by its extent.
+bool heads_overlap(const sgr_heads& a, const sgr_heads& b, long long tokens, int dim) {
+  if (!overlap(heads_extent(a, tokens, dim), heads_extent(b, tokens, dim))) return false;
+  const long long ts = a.token_stride;
+  const long long wa = (a.heads - 1) * a.head_stride + dim, wb = (b.heads - 1) * b.head_stride + dim;
+  if (ts != b.token_stride || wa > ts || wb > ts) return true;
+  const long long bytes = (long long)(reinterpret_cast<intptr_t>(b.data) - reinterpret_cast<intptr_t>(a.data));
+  const long long d = ((bytes % (2 * ts) + 2 * ts) % (2 * ts)) / 2;  // place of b's heads in a's rows
+  return d < wa || d + wb > ts;
+}
+
+bool same_rows(const sgr_heads& a, const sgr_heads& b) {
+  return a.data == b.data && a.token_stride == b.token_stride && a.head_stride == b.head_stride && a.heads == b.heads;
+}
+
+int check_heads(const sgr_heads* x, int heads, int dim, bool output) {
+  if (!x) return SGR_ERR_NULL;
+  if (x->reserved != 0) return SGR_ERR_UNSUPPORTED;
+  if (x->heads < 1 || x->heads != heads) return SGR_ERR_SHAPE;
+  if (heads > kMaxHeads) return SGR_ERR_UNSUPPORTED;
+  if (!x->data) return SGR_ERR_NULL;
+  if (x->token_stride < 0 || x->head_stride < 0) return SGR_ERR_SHAPE;
+  if (x->token_stride > kMaxStride || x->head_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  if (!aligned(x->data, 16) || x->token_stride % 8 || x->head_stride % 8) return SGR_ERR_ALIGN;
+  // Rows that are written must not overlap one another: heads within a token
+  // or tokens within a head.
+  const long long ts = x->token_stride, hs = x->head_stride;
+  if (hs < dim && heads > 1) return SGR_ERR_SHAPE;
+  if (output && ts < dim) return SGR_ERR_SHAPE;
+  return SGR_OK;
+}
+
+// Outputs: neither tokens within heads nor heads within tokens may collide.
+int check_rows(const sgr_heads& x, long long tokens, int dim) {
+  if (tokens <= 1) return SGR_OK;
+  const long long ts = x.token_stride, hs = x.head_stride;
+  if (x.heads == 1) return ts >= dim ? SGR_OK : SGR_ERR_SHAPE;
+  const bool heads_inside = ts >= (x.heads - 1) * hs + dim, tokens_inside = hs >= (tokens - 1) * ts + dim;
+  return heads_inside || tokens_inside ? SGR_OK : SGR_ERR_SHAPE;
+}
+
+int check_norm_rope(const sgr_norm_rope* nr, int dim) {
+  if (!nr) return SGR_ERR_NULL;
+  if ((nr->q_weight && !aligned(nr->q_weight, 16)) || (nr->k_weight && !aligned(nr->k_weight, 16)))
+    return SGR_ERR_ALIGN;
+  if ((nr->q_weight || nr->k_weight) && !(nr->eps >= 0.f && std::isfinite(nr->eps))) return SGR_ERR_SHAPE;
+  if (nr->table) {
+    if (!aligned(nr->table, 16)) return SGR_ERR_ALIGN;
+    if (nr->table_rows < 1 || nr->rot_dim < 16 || nr->rot_dim % 16 || nr->rot_dim > dim) return SGR_ERR_SHAPE;
+  }
+  return SGR_OK;
+}
+
+int check_dim(int dim) {
+  if (dim < 1) return SGR_ERR_SHAPE;
+  return dim == 64 || dim == 128 ? SGR_OK : SGR_ERR_UNSUPPORTED;
+}
+
+int validate_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* qo, const sgr_heads* ko,
+                  const int* positions, int tokens, int dim, const sgr_norm_rope* nr) {
+  int rc;
+  if (tokens < 0) return SGR_ERR_SHAPE;
+  if ((rc = check_dim(dim)) != SGR_OK) return rc;
+  if (tokens > kMaxTokens) return SGR_ERR_UNSUPPORTED;
+  if (!q || !qo || (k == nullptr) != (ko == nullptr)) return SGR_ERR_NULL;
+  if (tokens == 0) return SGR_OK;
+  if (!positions) return SGR_ERR_NULL;
+  if (!aligned(positions, 4)) return SGR_ERR_ALIGN;
+  if ((rc = check_norm_rope(nr, dim)) != SGR_OK) return rc;
+  const sgr_heads* in[2] = {q, k};
+  const sgr_heads* out[2] = {qo, ko};
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    if ((rc = check_heads(in[i], in[i]->heads, dim, false)) != SGR_OK) return rc;
+    if ((rc = check_heads(out[i], in[i]->heads, dim, true)) != SGR_OK) return rc;
+    if ((rc = check_rows(*out[i], tokens, dim)) != SGR_OK) return rc;
+  }
+  for (int i = 0; i < (k ? 2 : 1); ++i)
+    for (int j = 0; j < (k ? 2 : 1); ++j) {
+      if (!(i == j && same_rows(*in[i], *out[j])) && heads_overlap(*in[i], *out[j], tokens, dim)) return SGR_ERR_ALIAS;
+      if (i < j && heads_overlap(*out[i], *out[j], tokens, dim)) return SGR_ERR_ALIAS;
+    }
+  return SGR_OK;
+}
+
+int check_cache(const sgr_kv_cache* c) {
+  if (!c) return SGR_ERR_NULL;
+  int rc;
+  if ((rc = check_dim(c->head_dim)) != SGR_OK) return rc;
+  if (c->num_pages < 0 || c->heads < 1 || c->page_size < 1) return SGR_ERR_SHAPE;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return SGR_ERR_UNSUPPORTED;
+  if (c->heads > kMaxHeads) return SGR_ERR_UNSUPPORTED;
+  if (c->num_pages == 0) return SGR_OK;  // a cache without pages: block tables name none
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return SGR_ERR_NULL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return SGR_ERR_ALIGN;
+  struct Dim {
+    long long stride, count;
+  } d[3] = {{c->token_stride, c->page_size}, {c->head_stride, c->heads}, {c->page_stride, c->num_pages}};
+  for (const Dim& x : d) {
+    if (x.count > 1 && x.stride < 0) return SGR_ERR_SHAPE;
+    if (x.stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+    if (x.count > 1 && x.stride % 16) return SGR_ERR_ALIGN;
+  }
+  // Positions must not overlap: from the smallest stride up, each at least
+  // the span of what lies inside it.
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (d[j].stride > d[j + 1].stride) std::swap(d[j], d[j + 1]);
+  long long span = c->head_dim;
+  for (const Dim& x : d)
+    if (x.count > 1) {
+      if (x.stride < span) return SGR_ERR_SHAPE;
+      span += (x.count - 1) * x.stride;
+    }
+  if (c->scale_stride < c->heads && c->num_pages > 1) return SGR_ERR_SHAPE;
+  if (c->scale_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  return SGR_OK;
+}
+
+long long cache_bytes(const sgr_kv_cache& c) {
+  return (c.num_pages - 1) * c.page_stride + (c.heads - 1) * c.head_stride + (c.page_size - 1) * c.token_stride +
+         c.head_dim;
+}
+
+int check_batch(const sgr_kv_batch* b) {
+  if (!b) return SGR_ERR_NULL;
+  if (b->batch < 0 || b->tokens < 0 || b->max_new < 0 || b->max_pages < 0) return SGR_ERR_SHAPE;
+  if (b->batch > kMaxTokens || b->tokens > kMaxTokens || b->max_pages > (1 << 24)) return SGR_ERR_UNSUPPORTED;
+  if (b->batch == 0 || b->tokens == 0) return SGR_OK;
+  if (!b->q_start && b->tokens != b->batch) return SGR_ERR_SHAPE;
+  if (b->max_new < 1 || b->table_stride < b->max_pages) return SGR_ERR_SHAPE;
+  if (!b->seq_len || (b->max_pages > 0 && !b->block_table)) return SGR_ERR_NULL;
+  if (!aligned(b->seq_len, 4) || !aligned(b->block_table, 4) || !aligned(b->q_start, 4)) return SGR_ERR_ALIGN;
+  if (b->table_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  return SGR_OK;
+}
+
+bool empty(const sgr_kv_batch& b) { return b.batch == 0 || b.tokens == 0; }
+
+// Whether rows of heads and the cache (codes or scales) share memory.
+bool touches_cache(const sgr_heads& x, const sgr_kv_cache& c, long long tokens) {
+  if (c.num_pages == 0) return false;
+  const Extent e = heads_extent(x, tokens, c.head_dim);
+  for (const void* p : {(const void*)c.k, (const void*)c.v}) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (overlap(e, {lo, lo + (uintptr_t)cache_bytes(c)})) return true;
+  }
+  for (const void* p : {(const void*)c.k_scale, (const void*)c.v_scale}) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (overlap(e, {lo, lo + 4 * (uintptr_t)((c.num_pages - 1) * c.scale_stride + c.heads)})) return true;
+  }
+  return false;
+}
+
+int validate_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* k,
+                    const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr) {
+  int rc;
+  if ((rc = check_cache(c)) != SGR_OK || (rc = check_batch(b)) != SGR_OK) return rc;
+  if ((q == nullptr) != (qo == nullptr)) return SGR_ERR_NULL;
+  if (empty(*b)) return SGR_OK;
+  const int dim = c->head_dim;
+  if ((rc = check_norm_rope(nr, dim)) != SGR_OK) return rc;
+  if ((rc = check_heads(k, c->heads, dim, false)) != SGR_OK) return rc;
+  if ((rc = check_heads(v, c->heads, dim, false)) != SGR_OK) return rc;
+  if (touches_cache(*k, *c, b->tokens) || touches_cache(*v, *c, b->tokens)) return SGR_ERR_ALIAS;
+  if (q) {
+    if ((rc = check_heads(q, q->heads, dim, false)) != SGR_OK) return rc;
+    if ((rc = check_heads(qo, q->heads, dim, true)) != SGR_OK) return rc;
+    if ((rc = check_rows(*qo, b->tokens, dim)) != SGR_OK) return rc;
+    if (!same_rows(*q, *qo) && heads_overlap(*q, *qo, b->tokens, dim)) return SGR_ERR_ALIAS;
+    if (heads_overlap(*k, *qo, b->tokens, dim) || heads_overlap(*v, *qo, b->tokens, dim)) return SGR_ERR_ALIAS;
+    if (touches_cache(*q, *c, b->tokens) || touches_cache(*qo, *c, b->tokens)) return SGR_ERR_ALIAS;
+  }
+  return SGR_OK;
+}
+
+int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out,
+                       float scale, int window) {
+  int rc;
+  if ((rc = check_cache(c)) != SGR_OK || (rc = check_batch(b)) != SGR_OK) return rc;
+  if (!std::isfinite(scale) || window < 0) return SGR_ERR_SHAPE;
+  if (empty(*b)) return SGR_OK;
+  if (!q || !out) return SGR_ERR_NULL;
+  if ((rc = check_heads(q, q->heads, c->head_dim, false)) != SGR_OK) return rc;
+  if (q->heads % c->heads) return SGR_ERR_SHAPE;
+  if ((rc = check_heads(out, q->heads, c->head_dim, true)) != SGR_OK) return rc;
+  if ((rc = check_rows(*out, b->tokens, c->head_dim)) != SGR_OK) return rc;
+  if (heads_overlap(*q, *out, b->tokens, c->head_dim)) return SGR_ERR_ALIAS;
+  if (touches_cache(*out, *c, b->tokens)) return SGR_ERR_ALIAS;
+  return SGR_OK;
+}
+
+// ------------------------------------------------------------ device set-up
+struct KvDevice {
+  std::once_flag once;
+  int status = SGR_ERR_DEVICE;
+  int sms = 0;
+  unsigned* err = nullptr;
+};
+KvDevice g_kv[kMaxDevices];
+
+int current_kv_device(KvDevice** out) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SGR_ERR_DEVICE;
+  }
+  const int rc = sgr::kv_init_device(dev);
+  if (rc == SGR_OK) *out = &g_kv[dev];
+  return rc;
+}
+
+// ------------------------------------------------------------ launches
+sgr::KvHeads heads_of(const sgr_heads* x) {
+  if (!x) return {nullptr, 0, 0, 0};
+  return {static_cast<__nv_bfloat16*>(x->data), x->token_stride, x->head_stride, x->heads};
+}
+
+sgr::NormRope norm_rope_of(const sgr_norm_rope& n) {
+  return {static_cast<const __nv_bfloat16*>(n.q_weight), static_cast<const __nv_bfloat16*>(n.k_weight), n.table, n.eps,
+          n.table_rows, n.table ? n.rot_dim : 0, n.interleaved};
+}
+
+sgr::KvBatch batch_of(const sgr_kv_batch& b) {
+  return {b.block_table, b.seq_len, b.q_start, b.table_stride, b.batch, b.max_pages, b.tokens};
+}
+
+sgr::KvCacheRef cache_of(const sgr_kv_cache& c) {
+  const int shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  return {static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.k_scale, c.v_scale, c.page_stride, c.head_stride,
+          c.token_stride, c.scale_stride, c.num_pages, shift, c.heads};
+}
+
+template <class Params>
+int launch(void (*fn)(const Params), dim3 grid, int threads, size_t smem, const Params& p, unsigned flags,
+           void* stream) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = (flags & SGR_FLAG_NO_PDL) ? 0 : 1;
+  if (cudaLaunchKernelEx(&lc, fn, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SGR_ERR_LAUNCH;
+  }
+  return SGR_OK;
+}
+
+// Heads that one block of 4 warps takes of a row: one pass of its warps while
+// that does not fill the GPU (few rows: latency), up to four passes beyond
+// (the row's cosines, sines and weights are then read once for more heads).
+int rope_heads_per_block(int sms, long long rows, int heads, int dim, int threads) {
+  const int pass = threads / 32 * (32 / (dim / 8));
+  int passes = 1;
+  while (passes < 4 && rows * ((heads + pass * passes - 1) / (pass * passes)) > 16LL * sms) passes *= 2;
+  return pass * passes;
+}
+
+int run_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* qo, const sgr_heads* ko, const int* positions,
+             int tokens, int dim, const sgr_norm_rope* nr, unsigned flags, void* stream) {
+  int rc = validate_rope(q, k, qo, ko, positions, tokens, dim, nr);
+  if (rc != SGR_OK || tokens == 0) return rc;
+  KvDevice* dev;
+  if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  sgr::RopeParams p;
+  p.q = heads_of(q);
+  p.k = heads_of(k);
+  p.qo = heads_of(qo);
+  p.ko = heads_of(ko);
+  p.positions = positions;
+  p.nr = norm_rope_of(*nr);
+  p.err = dev->err;
+  const int heads = p.q.heads + p.k.heads;
+  p.heads_per_block = rope_heads_per_block(dev->sms, tokens, heads, dim, sgr::kRopeThreads);
+  const dim3 grid(tokens, (heads + p.heads_per_block - 1) / p.heads_per_block);
+  return launch(dim == 64 ? sgr::qk_norm_rope_kernel<64> : sgr::qk_norm_rope_kernel<128>, grid, sgr::kRopeThreads, 0, p,
+                flags, stream);
+}
+
+using AppendFn = void (*)(const sgr::AppendParams);
+
+// The kernel whose threads hold a whole page of new tokens, or `most` of them.
+AppendFn append_fn(int dim, int page_size, int most) {
+  const int tok = sgr::kAppendThreads / (dim / 8);
+  const int n = most < page_size ? most : page_size;
+  const int pass = n <= tok ? 1 : n <= 2 * tok ? 2 : n <= 4 * tok ? 4 : 8;
+  if (dim == 64)
+    return pass == 1 ? sgr::kv_append_kernel<64, 1> : pass == 2 ? sgr::kv_append_kernel<64, 2> : sgr::kv_append_kernel<64, 4>;
+  return pass == 1   ? sgr::kv_append_kernel<128, 1>
+         : pass == 2 ? sgr::kv_append_kernel<128, 2>
+         : pass == 4 ? sgr::kv_append_kernel<128, 4>
+                     : sgr::kv_append_kernel<128, 8>;
+}
+
+int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* k,
+               const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr, unsigned flags, void* stream) {
+  int rc = validate_append(c, b, q, k, v, qo, nr);
+  if (rc != SGR_OK || empty(*b)) return rc;
+  KvDevice* dev;
+  if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  sgr::AppendParams p;
+  p.q = heads_of(q);
+  p.k = heads_of(k);
+  p.v = heads_of(v);
+  p.qo = heads_of(qo);
+  p.cache = cache_of(*c);
+  p.batch = batch_of(*b);
+  p.nr = norm_rope_of(*nr);
+  p.err = dev->err;
+  // Pages written to: at most one per row; a sequence of n rows reaches at
+  // most (n - 1) / page_size + 2 of them.
+  long long slots = (long long)b->tokens / c->page_size + 2LL * b->batch;
+  if (slots > b->tokens) slots = b->tokens;
+  p.heads_per_block = q ? rope_heads_per_block(dev->sms, b->tokens, q->heads, c->head_dim, sgr::kAppendThreads) : 1;
+  p.q_chunks = q ? (q->heads + p.heads_per_block - 1) / p.heads_per_block : 0;
+  const long long q_blocks = (long long)b->tokens * p.q_chunks, blocks = q_blocks + slots * c->heads * 2;
+  if (blocks > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
+  p.q_blocks = (int)q_blocks;
+  return launch(append_fn(c->head_dim, c->page_size, b->tokens), dim3((unsigned)blocks), sgr::kAppendThreads, 0, p,
+                flags, stream);
+}
+
+int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out, float scale,
+                  int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
+  int rc = validate_attention(c, b, q, out, scale, window);
+  if (rc != SGR_OK || empty(*b)) return rc;
+  (void)workspace;
+  (void)workspace_bytes;
+  KvDevice* dev;
+  if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  sgr::AttnParams p;
+  p.q = heads_of(q);
+  p.out = heads_of(out);
+  p.cache = cache_of(*c);
+  p.batch = batch_of(*b);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.window = window;
+  p.err = dev->err;
+  const dim3 grid(b->tokens, q->heads);
+  return launch(c->head_dim == 64 ? sgr::kv_attn_kernel<64> : sgr::kv_attn_kernel<128>, grid, sgr::kAttnThreads, 0, p,
+                flags, stream);
+}
+
+}  // namespace
+
+namespace sgr {
+
+int kv_init_device(int dev) {
+  if (dev < 0 || dev >= kMaxDevices) return SGR_ERR_DEVICE;
+  KvDevice& d = g_kv[dev];
+  std::call_once(d.once, [&] {
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || d.sms <= 0) {
+      cudaGetLastError();
+      return;
+    }
+    d.status = device_error_word(dev, &d.err);
+  });
+  return d.status;
+}
+
+}  // namespace sgr
+
+extern "C" {
+
+int sgr_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* q_out, const sgr_heads* k_out,
+                     const int* positions, int tokens, int head_dim, const sgr_norm_rope* nr, unsigned flags,
+                     void* stream) {
+  return run_rope(q, k, q_out, k_out, positions, tokens, head_dim, nr, flags, stream);
+}
+
+int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* k,
+                  const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, unsigned flags, void* stream) {
+  return run_append(cache, batch, q, k, v, q_out, nr, flags, stream);
+}
+
+int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* out,
+                     float scale, int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
+  return run_attention(cache, batch, q, out, scale, window, workspace, workspace_bytes, flags, stream);
+}
+
+int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
+                               int64_t* bytes) {
+  if (!bytes) return SGR_ERR_NULL;
+  (void)device;
+  int rc;
+  if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
+  if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
+  *bytes = 0;
+  return SGR_OK;
+}
+
+int sgr_validate_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* q_out, const sgr_heads* k_out,
+                              const int* positions, int tokens, int head_dim, const sgr_norm_rope* nr) {
+  return validate_rope(q, k, q_out, k_out, positions, tokens, head_dim, nr);
+}
+
+int sgr_validate_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                           const sgr_heads* k, const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr) {
+  return validate_append(cache, batch, q, k, v, q_out, nr);
+}
+
+int sgr_validate_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                              const sgr_heads* out, float scale, int window) {
+  return validate_attention(cache, batch, q, out, scale, window);
+}
+
+}  // extern "C"

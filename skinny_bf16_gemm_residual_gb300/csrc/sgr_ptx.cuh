@@ -40,6 +40,7 @@ enum : unsigned {
   kErrWaitFixup = 4,     // split-K fixup gave up waiting for its inputs
   kErrDrain = 5,         // a CTA gave up draining its own copies before exit
   kErrTmemAlloc = 6,     // tensor-memory allocation returned no columns
+  kErrIndex = 7,         // a page, length, position or row offset in device data is out of range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
