@@ -1,7 +1,9 @@
 // sgr_kv.cu -- C ABI of the attention operators (include/sgr_attention.h):
 // argument checks, device set-up and kernel launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -272,9 +274,8 @@ sgr::KvCacheRef cache_of(const sgr_kv_cache& c) {
           c.token_stride, c.scale_stride, c.num_pages, shift, c.heads};
 }
 
-template <class Params>
-int launch(void (*fn)(const Params), dim3 grid, int threads, size_t smem, const Params& p, unsigned flags,
-           void* stream) {
+template <class Fn, class... Params>
+int launch(Fn fn, dim3 grid, int threads, size_t smem, unsigned flags, void* stream, const Params&... p) {
   cudaLaunchConfig_t lc = {};
   lc.gridDim = grid;
   lc.blockDim = dim3(threads, 1, 1);
@@ -285,7 +286,7 @@ int launch(void (*fn)(const Params), dim3 grid, int threads, size_t smem, const 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = (flags & SGR_FLAG_NO_PDL) ? 0 : 1;
-  if (cudaLaunchKernelEx(&lc, fn, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&lc, fn, p...) != cudaSuccess) {
     cudaGetLastError();
     return SGR_ERR_LAUNCH;
   }
@@ -319,8 +320,8 @@ int run_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* qo, const 
   const int heads = p.q.heads + p.k.heads;
   p.heads_per_block = rope_heads_per_block(dev->sms, tokens, heads, dim, sgr::kRopeThreads);
   const dim3 grid(tokens, (heads + p.heads_per_block - 1) / p.heads_per_block);
-  return launch(dim == 64 ? sgr::qk_norm_rope_kernel<64> : sgr::qk_norm_rope_kernel<128>, grid, sgr::kRopeThreads, 0, p,
-                flags, stream);
+  return launch(dim == 64 ? sgr::qk_norm_rope_kernel<64> : sgr::qk_norm_rope_kernel<128>, grid, sgr::kRopeThreads, 0,
+                flags, stream, p);
 }
 
 using AppendFn = void (*)(const sgr::AppendParams);
@@ -362,29 +363,101 @@ int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q,
   const long long q_blocks = (long long)b->tokens * p.q_chunks, blocks = q_blocks + slots * c->heads * 2;
   if (blocks > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
   p.q_blocks = (int)q_blocks;
-  return launch(append_fn(c->head_dim, c->page_size, b->tokens), dim3((unsigned)blocks), sgr::kAppendThreads, 0, p,
-                flags, stream);
+  return launch(append_fn(c->head_dim, c->page_size, b->tokens), dim3((unsigned)blocks), sgr::kAppendThreads, 0,
+                flags, stream, p);
+}
+
+// ------------------------------------------------------------ attention
+using AttnFn = void (*)(const CUtensorMap, const CUtensorMap, const sgr::AttnParams);
+using JoinFn = void (*)(const sgr::AttnParams, int);
+
+struct AttnKernel {
+  AttnFn fn;
+  JoinFn join;
+  int smem;
+};
+
+template <int D, int NT>
+AttnKernel attn_kernel_of() {
+  return {sgr::kv_attn_kernel<D, NT>, sgr::kv_attn_join_kernel<D, NT>, sgr::attn_smem_bytes<D, NT>()};
+}
+
+AttnKernel attn_kernel(int dim, int nt) {
+  if (dim == 64) return nt == 8 ? attn_kernel_of<64, 8>() : nt == 16 ? attn_kernel_of<64, 16>() : attn_kernel_of<64, 32>();
+  return nt == 8 ? attn_kernel_of<128, 8>() : nt == 16 ? attn_kernel_of<128, 16>() : attn_kernel_of<128, 32>();
+}
+
+struct AttnPlan {
+  int nt;           // rows of a row tile
+  int grid;
+  bool split;       // whether a row tile may span CTAs
+  bool reuse;       // whether a sequence may have several row tiles
+  int64_t bytes;    // workspace
+};
+
+// Row tiles as small as the rows of a sequence allow: the small operands and
+// accumulators are 2 nt columns wide, and so is the softmax work a tile.
+AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
+  AttnPlan a;
+  const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
+  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
+  const long long units = c.heads * row_tiles * (tiles > 1 ? tiles : 1);
+  a.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
+  a.split = tiles > 1;
+  a.reuse = rows > a.nt;
+  a.bytes = 2LL * a.grid * (a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
+  return a;
+}
+
+// Cache codes as a 4-D tensor (element, position in the page, head, page).
+bool make_cache_tmap(CUtensorMap* m, const void* codes, const sgr_kv_cache& c) {
+  sgr::detail::EncodeTiledFn fn = sgr::detail::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dim = (cuuint64_t)c.head_dim;
+  cuuint64_t dims[4] = {dim, (cuuint64_t)c.page_size, (cuuint64_t)c.heads, (cuuint64_t)(c.num_pages ? c.num_pages : 1)};
+  // (a stride that nothing is reached by may hold anything)
+  cuuint64_t strides[3] = {(cuuint64_t)c.token_stride, c.heads > 1 ? (cuuint64_t)c.head_stride : dim,
+                           c.num_pages > 1 ? (cuuint64_t)c.page_stride : dim};
+  cuuint32_t box[4] = {(cuuint32_t)dim, (cuuint32_t)c.page_size, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out, float scale,
                   int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
   int rc = validate_attention(c, b, q, out, scale, window);
   if (rc != SGR_OK || empty(*b)) return rc;
-  (void)workspace;
-  (void)workspace_bytes;
+  if (!workspace) return SGR_ERR_NULL;
+  if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads);
+  if (workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
+  CUtensorMap tk, tv;
+  // (a cache without pages: the maps are never used)
+  if (!make_cache_tmap(&tk, c->num_pages ? c->k : workspace, *c) || !make_cache_tmap(&tv, c->num_pages ? c->v : workspace, *c))
+    return SGR_ERR_LAUNCH;
   sgr::AttnParams p;
   p.q = heads_of(q);
   p.out = heads_of(out);
   p.cache = cache_of(*c);
   p.batch = batch_of(*b);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.window = window;
+  p.window = window > 0 ? window : INT_MAX;
+  p.group = q->heads / c->heads;
+  p.reuse = a.reuse ? 1 : 0;
   p.err = dev->err;
-  const dim3 grid(b->tokens, q->heads);
-  return launch(c->head_dim == 64 ? sgr::kv_attn_kernel<64> : sgr::kv_attn_kernel<128>, grid, sgr::kAttnThreads, 0, p,
-                flags, stream);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2LL * a.grid * a.nt * c->head_dim);
+  p.pieces = reinterpret_cast<sgr::AttnPiece*>(p.part_ml + 2LL * a.grid * a.nt);
+  const AttnKernel k = attn_kernel(c->head_dim, a.nt);
+  rc = launch(k.fn, dim3(a.grid), sgr::kAttnThreads, k.smem, flags, stream, tk, tv, p);
+  if (rc != SGR_OK || !a.split) return rc;
+  return launch(k.join, dim3(a.grid, a.nt), sgr::kJoinThreads, 0, flags, stream, p, a.grid);
 }
 
 }  // namespace
@@ -399,7 +472,20 @@ int kv_init_device(int dev) {
       cudaGetLastError();
       return;
     }
-    d.status = device_error_word(dev, &d.err);
+    int prev = -1;
+    if (cudaGetDevice(&prev) != cudaSuccess || (prev != dev && cudaSetDevice(dev) != cudaSuccess)) {
+      cudaGetLastError();
+      return;
+    }
+    bool ok = true;
+    for (int dim : {64, 128})
+      for (int nt : {8, 16, 32})
+        ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(attn_kernel(dim, nt).fn)) == cudaSuccess;
+    if (prev != dev) cudaSetDevice(prev);
+    if (ok)
+      d.status = device_error_word(dev, &d.err);
+    else
+      cudaGetLastError();
   });
   return d.status;
 }
@@ -427,11 +513,11 @@ int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const
 int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
                                int64_t* bytes) {
   if (!bytes) return SGR_ERR_NULL;
-  (void)device;
   int rc;
   if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
   if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
-  *bytes = 0;
+  if ((rc = sgr::kv_init_device(device)) != SGR_OK) return rc;
+  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads).bytes;
   return SGR_OK;
 }
 

@@ -114,6 +114,41 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
+// Wait that also returns (false) as soon as another role of the CTA aborted.
+__device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity,
+                                                   volatile int* abort_flag) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_test_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > SGR_WAIT_LIMIT_NS) return false;
+  }
+}
+
+// The same for waits that may last microseconds (a consumer ahead of its
+// producer, an epilogue waiting for the whole main loop, a CTA launched early
+// by programmatic dependent launch): after a short spin the thread sleeps
+// between polls (32 ns doubling to 256 ns), so that it does not take issue
+// slots from the warps that do the work on the same SM sub-partition.
+__device__ __forceinline__ bool mbar_wait_sleepy_or_abort(uint32_t bar, uint32_t parity,
+                                                          volatile int* abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  unsigned ns = 32;
+  while (true) {
+    __nanosleep(ns);
+    if (mbar_test_wait(bar, parity)) return true;
+    if (ns < 256) ns <<= 1;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > SGR_WAIT_LIMIT_NS) return false;
+  }
+}
+
 // ------------------------------------------------------------ cache policies
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
@@ -146,6 +181,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int3
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+
+// 4-D tensor copy (TMA) global -> shared.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -225,6 +270,27 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   return d;
 }
 
+// Shared-memory matrix descriptor of rows of kRow (64 or 128) bytes stored
+// with the swizzle of that width, 8-row groups 8 kRow apart.  K-major: a row
+// is an operand row.  M-major: a row holds kRow consecutive m of one k, and
+// operands wider than kRow continue `lead` bytes on.
+template <int kRow>
+__device__ __forceinline__ uint64_t smem_desc_rows(uint32_t saddr, uint32_t lead = 16) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((lead & 0x3FFFFu) >> 4) << 16;
+  d |= (uint64_t)(8 * kRow >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)(kRow == 128 ? 2 : 4) << 61;
+  return d;
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in such a tile.
+template <int kRow>
+__device__ __forceinline__ uint32_t swizzled(int row, int chunk) {
+  return (uint32_t)(row * kRow + ((chunk ^ (kRow == 128 ? row & 7 : (row >> 1) & 3)) << 4));
+}
+
 // Instruction descriptor for kind::f16 with BF16 A and B, FP32 accumulator,
 // both operands K-major, no negation or sparsity: D format (bits 4-5) = 1,
 // A format (7-9) = 1, B format (10-12) = 1, N >> 3 (17-22), M >> 4 (24-28).
@@ -241,6 +307,25 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// D (+)= A[smem] . B[smem]^T with E4M3 A and B, FP32 D, issued by one thread.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format 0), FP32
+// D (bits 4-5 = 1), both K-major: N >> 3 at bits 17-22, M >> 4 at 24-28.
+// (An M-major A operand -- element (m, k) of consecutive m next to one another
+// -- sets bit 15.)
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 // D[tmem] (+)= A[tmem] . B[smem]^T: the A operand (M = 128 rows x K = 16)

@@ -39,6 +39,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "sgr_internal.h"
 #include "sgr_ptx.cuh"
 #include "skinny_gemm_residual.h"
 
@@ -92,41 +93,6 @@ __device__ __forceinline__ long long tc_unit_begin(long long U, int G, int c) {
 // The CTA whose unit range contains unit u.
 __device__ __forceinline__ int tc_cta_of(long long U, int G, long long u) {
   return (int)(((u + 1) * G - 1) / U);
-}
-
-// Wait that also returns (false) as soon as another role of the CTA aborted.
-__device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity,
-                                                   volatile int* abort_flag) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > SGR_WAIT_LIMIT_NS) return false;
-  }
-}
-
-// The same for waits that may last microseconds (a consumer ahead of its
-// producer, an epilogue waiting for the whole main loop, a CTA launched early
-// by programmatic dependent launch): after a short spin the thread sleeps
-// between polls (32 ns doubling to 256 ns), so that it does not take issue
-// slots from the warps that do the work on the same SM sub-partition.
-__device__ __forceinline__ bool mbar_wait_sleepy_or_abort(uint32_t bar, uint32_t parity,
-                                                          volatile int* abort_flag) {
-#pragma unroll 1
-  for (int i = 0; i < 8; ++i)
-    if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  unsigned ns = 32;
-  while (true) {
-    __nanosleep(ns);
-    if (mbar_test_wait(bar, parity)) return true;
-    if (ns < 256) ns <<= 1;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > SGR_WAIT_LIMIT_NS) return false;
-  }
 }
 
 // 16 accumulator columns summed over the chains, chain 0 first (fixed order).
@@ -435,26 +401,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 // ------------------------------------------------------------------ host side
 namespace detail {
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-inline EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      return (EncodeTiledFn) nullptr;
-    }
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
-}
 
 // 2-D BF16 row-major [rows, cols] with row stride ld (elements); box
 // box_cols x box_rows with the 128-byte swizzle; out-of-bounds reads as zero.

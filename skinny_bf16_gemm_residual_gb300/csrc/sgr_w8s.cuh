@@ -178,23 +178,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
 // 2^e as a float for e in [-126, 127].
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// D (+)= A[smem] . B[smem]^T with E4M3 A and B, FP32 D, issued by one thread.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format 0), FP32
-// D (bits 4-5 = 1), both K-major: N >> 3 at bits 17-22, M >> 4 at 24-28.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
-  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
-}
-
 // kInRegs = w8s_in_regs(M, K): the instance with the register form of the
 // converters and the epilogue's warm-up pass; the other instance has the
 // per-stage form and no warm-up.  Each carries only its own code (the first
