@@ -22,6 +22,7 @@ using sgr::kMaxDevices;
 constexpr long long kMaxStride = 1LL << 36;  // as the row strides of skinny_gemm_residual.h
 constexpr int kMaxTokens = 1 << 20;
 constexpr int kMaxHeads = 1 << 12;
+constexpr int kMaxGroup = 1 << 10;  // query heads a key/value head: rows of a sequence stay below 2^30
 
 // ------------------------------------------------------------ argument checks
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -227,6 +228,7 @@ int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_h
   if ((rc = check_heads(q, q->heads, c->head_dim, false)) != SGR_OK) return rc;
   if (q->heads % c->heads) return SGR_ERR_SHAPE;
   if ((rc = check_heads(out, q->heads, c->head_dim, true)) != SGR_OK) return rc;
+  if (q->heads / c->heads > kMaxGroup) return SGR_ERR_UNSUPPORTED;
   if ((rc = check_rows(*out, b->tokens, c->head_dim)) != SGR_OK) return rc;
   if (heads_overlap(*q, *out, b->tokens, c->head_dim)) return SGR_ERR_ALIAS;
   if (touches_cache(*out, *c, b->tokens)) return SGR_ERR_ALIAS;
@@ -369,17 +371,18 @@ int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q,
 
 // ------------------------------------------------------------ attention
 using AttnFn = void (*)(const CUtensorMap, const CUtensorMap, const sgr::AttnParams);
-using JoinFn = void (*)(const sgr::AttnParams, int);
+using JoinFn = void (*)(const sgr::AttnParams);
 
 struct AttnKernel {
   AttnFn fn;
   JoinFn join;
-  int smem;
+  int smem, threads;
 };
 
 template <int D, int NT>
 AttnKernel attn_kernel_of() {
-  return {sgr::kv_attn_kernel<D, NT>, sgr::kv_attn_join_kernel<D, NT>, sgr::attn_smem_bytes<D, NT>()};
+  return {sgr::kv_attn_kernel<D, NT>, sgr::kv_attn_join_kernel<D, NT>, sgr::attn_smem_bytes<D, NT>(),
+          sgr::AttnShape<D, NT>::kThreads};
 }
 
 AttnKernel attn_kernel(int dim, int nt) {
@@ -407,7 +410,7 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   a.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
   a.split = tiles > 1;
   a.reuse = rows > a.nt;
-  a.bytes = 2LL * a.grid * (a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
+  a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
   return a;
 }
 
@@ -455,9 +458,9 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2LL * a.grid * a.nt * c->head_dim);
   p.pieces = reinterpret_cast<sgr::AttnPiece*>(p.part_ml + 2LL * a.grid * a.nt);
   const AttnKernel k = attn_kernel(c->head_dim, a.nt);
-  rc = launch(k.fn, dim3(a.grid), sgr::kAttnThreads, k.smem, flags, stream, tk, tv, p);
+  rc = launch(k.fn, dim3(a.grid), k.threads, k.smem, flags, stream, tk, tv, p);
   if (rc != SGR_OK || !a.split) return rc;
-  return launch(k.join, dim3(a.grid, a.nt), sgr::kJoinThreads, 0, flags, stream, p, a.grid);
+  return launch(k.join, dim3(a.grid, a.nt / 8), sgr::kJoinThreads, 0, flags, stream, p);
 }
 
 }  // namespace

@@ -37,10 +37,10 @@
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile.
 //
-// Roles (256 threads, two CTAs an SM): warps 0-3 softmax (thread = token,
-// then = element d), warp 4 walks the work, loads pages by TMA and hands out
-// segments, warp 5 issues the MMAs, warps 6-7 bring the next segment's
-// queries into the operand.
+// Roles (two CTAs an SM): 4 or 8 softmax warps (thread = token, then = element
+// d; with 8, two groups of 4 take half of the columns each), one warp that
+// walks the work, loads pages by TMA and hands out segments, one that issues
+// the MMAs, two that bring the next segments' queries into the operand.
 #pragma once
 
 #include <cuda.h>
@@ -50,7 +50,6 @@
 
 namespace sgr {
 
-constexpr int kAttnThreads = 256;
 constexpr int kAttnTile = 128;  // tokens
 constexpr int kAttnQueue = 8;   // segments handed out ahead
 
@@ -66,11 +65,12 @@ struct AttnSeg {
   int pad;
 };
 
-// A partial sum's owner, for the kernel that joins them.
+// Owner of the partial sums of a row tile that begins in a CTA and ends in
+// CTA `last` (0: none).
 struct AttnPiece {
-  int valid, last;
+  int last;
   int h, row0, r0, nrows;
-  int pad[2];
+  int pad[3];
 };
 
 struct AttnParams {
@@ -82,54 +82,62 @@ struct AttnParams {
   int group;         // query heads a key/value head
   int reuse;         // row tiles of a sequence share the cache's bytes
   unsigned* err;
-  float* part_o;  // [2 grid][NT][D]
-  float2* part_ml;  // [2 grid][NT]  maximum, sum
-  AttnPiece* pieces;  // [2 grid]
+  float* part_o;      // [2 grid][NT][D]
+  float2* part_ml;    // [2 grid][NT]  maximum, sum
+  AttnPiece* pieces;  // [grid]
 };
 
 template <int D, int NT>
 struct AttnShape {
+  static constexpr int kGroups = NT == 8 ? 1 : 2;  // of 4 softmax warps
+  static constexpr int kC = NT / kGroups;          // columns a softmax thread
+  static constexpr int kSoftmax = 4 * kGroups;     // warps
+  static constexpr int kThreads = 32 * (kSoftmax + 4);
   static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
-  // As deep as two CTAs an SM allow.
-  static constexpr int kStages = D == 128 ? (NT <= 16 ? 3 : 2) : (NT <= 16 ? 6 : 4);
+  // As many stages and query buffers as two CTAs an SM allow.
+  static constexpr int kStages = D == 128 ? (NT <= 16 ? 3 : 2) : (NT == 8 ? 6 : NT == 16 ? 5 : 4);
+  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : 4;
   static constexpr int kPBytes = kCols * kAttnTile;
   static constexpr int kQBytes = kCols * D;
-  static constexpr int kTmemCols = 4 * kCols < 32 ? 32 : 4 * kCols;  // S and O, two each
+  static constexpr int kTmemCols = 4 * kCols;  // S and O, two each
 };
 
-template <int NT>
+template <int D, int NT>
 struct AttnCtl {
-  uint64_t kfull[6], vfull[6], empty[6];
-  uint64_t sfull[2], sempty[2], ofull[2], oempty[2], qfull[2], qempty[2], pfull, drain;
+  using Sh = AttnShape<D, NT>;
+  static constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC;
+  uint64_t kfull[S], vfull[S], empty[S];
+  uint64_t sfull[2], sempty[2], ofull[2], oempty[2], qfull[Q], qempty[Q], pfull, drain;
   uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
   uint32_t tmem;
   int abort;
-  int go[2];
-  int start_b;
+  int go[2][2];
   unsigned nan_tokens[4];
-  long long start_off, units;
-  long long scan[kAttnThreads / 32];
+  // where this CTA's share begins: sequence (-1: none), head, row tile, units of it to skip
+  int start_b, start_h, start_j, start_skip;
+  KvSeq start_seq;
+  long long scan[Sh::kThreads / 32];
   AttnSeg seg[kAttnQueue];
-  float kscale[6][8], vexp[6][8];  // of a stage's pages
-  int flags[6];                    // 1: some token is not live, 2: rows see different tokens
-  alignas(16) float qf[2][NT];     // score factor of a row
-  int qpos[2][NT];                 // last position that a row sees
-  long long qout[2][NT];           // its place in the output
-  alignas(16) float wmax[2][4][NT], wsum[4][NT];
-  alignas(16) float m[4][NT], alpha[4][2][NT], beta[4][2][NT];  // each softmax warp's own copy
+  float kscale[S][8], vexp[S][8];  // of a stage's pages
+  int flags[S];                    // 1: some token is not live, 2: rows see different tokens
+  long long qout[Q][NT];           // a row's place in the output
+  alignas(16) float qf[Q][NT];     // its score factor
+  int qpos[Q][NT];                 // the last position that it sees
+  alignas(16) float wmax[2][Sh::kSoftmax][C], wsum[Sh::kSoftmax][C];
+  alignas(16) float m[Sh::kSoftmax][C], alpha[Sh::kSoftmax][2][C], beta[Sh::kSoftmax][2][C];  // a warp's own copies
 };
 
 template <int D, int NT>
 constexpr int attn_ctl_bytes() {
-  return (int)((sizeof(AttnCtl<NT>) + 1023) / 1024 * 1024);
+  return (int)((sizeof(AttnCtl<D, NT>) + 1023) / 1024 * 1024);
 }
 
 template <int D, int NT>
 constexpr int attn_smem_bytes() {
   using S = AttnShape<D, NT>;
-  return 1024 + attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + 2 * S::kQBytes;
+  return 1024 + attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + S::kQBufs * S::kQBytes;
 }
 
 // Row tile j of a sequence: its rows, the positions they see, its units (a
@@ -160,6 +168,16 @@ __device__ __forceinline__ long long attn_seq_units(const KvSeq& s, int group, i
   return u;
 }
 
+// Equal shares: CTA c of `active` takes units [share_begin(c), share_begin(c + 1)).
+struct AttnShare {
+  long long per, rest;  // the first `rest` CTAs take one more than `per`
+  __device__ __forceinline__ long long begin(long long c) const { return c * per + min(c, rest); }
+  __device__ __forceinline__ int cta_of(long long u) const {
+    const long long x = rest * (per + 1);
+    return (int)(u < x ? u / (per + 1) : rest + (u - x) / per);
+  }
+};
+
 // 2^d for whole d <= 0 (0 from -127 down), on the integer unit.
 __device__ __forceinline__ float exp2_whole(float d) {
   return __int_as_float((__float_as_int(fmaxf(d, -127.f) + 12582912.f) << 23) + 0x3f800000);
@@ -175,6 +193,25 @@ __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Sums of C columns over the warp's lanes: lane l returns column l / (32 / C).
+template <int C>
+__device__ __forceinline__ float warp_column_sums(float (&x)[C]) {
+  const int lane = threadIdx.x & 31;
+  int d = 16;
+#pragma unroll
+  for (int n = C / 2; n > 0; n >>= 1, d >>= 1) {
+    const bool upper = (lane & d) != 0;
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      const float give = upper ? x[k] : x[k + n], keep = upper ? x[k + n] : x[k];
+      x[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+    }
+  }
+#pragma unroll
+  for (; d > 0; d >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
+  return x[0];
 }
 
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
@@ -206,34 +243,32 @@ __device__ __forceinline__ uint32_t split2(float a, float b) {
   return r;
 }
 
-template <int NT>
-__device__ __forceinline__ void tmem_ld_sum(uint32_t taddr, float (&x)[NT]) {
-  // columns [0, NT) (hi) plus columns [NT, 2 NT) (lo) / 32
-  if constexpr (NT == 8) {
-    float v[16];
-    tmem_ld16(taddr, v);
+// x[q] = hi[q] + lo[q] / 32 of C accumulator columns at `hi`, the lo ones
+// `apart` columns on.
+template <int C>
+__device__ __forceinline__ void tmem_ld_sum(uint32_t hi, uint32_t apart, float (&x)[C]) {
+  if constexpr (C == 8) {
+    float v[8], w[8];
+    tmem_ld8x2(hi, hi + apart, v, w);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = fmaf(v[8 + q], kLoScale, v[q]);
+    for (int q = 0; q < 8; ++q) x[q] = fmaf(w[q], kLoScale, v[q]);
   } else {
+    float v[16];
+    tmem_ld16(hi, x);
+    tmem_ld16(hi + apart, v);
 #pragma unroll
-    for (int c = 0; c < NT; c += 16) {
-      float v[16], w[16];
-      tmem_ld16(taddr + c, v);
-      tmem_ld16(taddr + NT + c, w);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) x[c + q] = fmaf(w[q], kLoScale, v[q]);
-    }
+    for (int q = 0; q < 16; ++q) x[q] = fmaf(v[q], kLoScale, x[q]);
   }
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, 2)
+__global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Sh = AttnShape<D, NT>;
-  constexpr int S = Sh::kStages, kCols = Sh::kCols;
+  constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC, kCols = Sh::kCols, kSoftmax = Sh::kSoftmax;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  AttnCtl<NT>& c = *reinterpret_cast<AttnCtl<NT>*>(smem_raw + (base - raw));
+  AttnCtl<D, NT>& c = *reinterpret_cast<AttnCtl<D, NT>*>(smem_raw + (base - raw));
   const uint32_t ring = base + attn_ctl_bytes<D, NT>();
   const uint32_t pbuf = ring + S * Sh::kStageBytes, qbuf = pbuf + Sh::kPBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -247,23 +282,25 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&c.sfull[i]), 1);
-      mbar_init(smem_u32(&c.sempty[i]), 4);
+      mbar_init(smem_u32(&c.sempty[i]), kSoftmax);
       mbar_init(smem_u32(&c.ofull[i]), 1);
-      mbar_init(smem_u32(&c.oempty[i]), 4);
-      mbar_init(smem_u32(&c.qfull[i]), 2);
-      mbar_init(smem_u32(&c.qempty[i]), 5);  // the last MMA that reads it, the softmax warps
+      mbar_init(smem_u32(&c.oempty[i]), kSoftmax);
     }
-    mbar_init(smem_u32(&c.pfull), 4);
+    for (int i = 0; i < Q; ++i) {
+      mbar_init(smem_u32(&c.qfull[i]), 2);
+      mbar_init(smem_u32(&c.qempty[i]), 1 + kSoftmax);  // the last MMA that reads it, the softmax warps
+    }
+    mbar_init(smem_u32(&c.pfull), kSoftmax);
     mbar_init(smem_u32(&c.drain), 1);
     for (int i = 0; i < kAttnQueue; ++i) {
       mbar_init(smem_u32(&c.segfull[i]), 1);
-      mbar_init(smem_u32(&c.segempty[i]), 7);  // MMA, 4 softmax and 2 query warps
+      mbar_init(smem_u32(&c.segempty[i]), kSoftmax + 3);  // and the MMA and query warps
     }
     c.abort = 0;
     c.start_b = -1;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kSoftmax + 1) {
     tmem_alloc(smem_u32(&c.tmem), Sh::kTmemCols);
     tmem_relinquish();
   }
@@ -280,82 +317,95 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
   pdl_wait();
 
   // ------------------------------------------------ this CTA's share of the work
+  // Each thread counts the units of its (consecutive) sequences; the one that
+  // holds the share's first unit says where it lies.
   const int ps = p.cache.page_shift, hk = p.cache.heads;
-  long long mine = 0;
-  for (int b = tid; b < p.batch.batch; b += kAttnThreads)
-    mine += attn_seq_units<NT>(kv_seq(p.batch, ps, b, p.err), p.group, p.window);
+  const int per_thread = (p.batch.batch + Sh::kThreads - 1) / Sh::kThreads;
+  const int b_first = tid * per_thread, b_last = min(b_first + per_thread, p.batch.batch);
+  KvSeq own{0, 0, 0};
+  long long units = 0, mine = 0;
+  for (int b = b_first; b < b_last; ++b) {
+    own = kv_seq(p.batch, ps, b, p.err);
+    units = attn_seq_units<NT>(own, p.group, p.window);  // (of the last one: all there is to know with one a thread)
+    mine += units * hk;
+  }
+  long long upto = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) c.scan[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) c.scan[warp] = upto;
   __syncthreads();
-  long long total = 0;
+  long long total = 0, before = upto - mine;
 #pragma unroll
-  for (int w = 0; w < kAttnThreads / 32; ++w) total += c.scan[w];
-  total *= hk;
+  for (int w = 0; w < Sh::kThreads / 32; ++w) {
+    before += w < warp ? c.scan[w] : 0;
+    total += c.scan[w];
+  }
   // (with fewer units than CTAs the last ones have none, the others one each)
-  const long long active = min(total, (long long)gridDim.x);
-  const bool busy = blockIdx.x < active;
-  const long long u0 = busy ? total * blockIdx.x / active : 0, u1 = busy ? total * (blockIdx.x + 1) / active : 0;
-  {
-    long long before = 0;  // units of the sequences before this round's
-    for (int b0 = 0; b0 < p.batch.batch && u1 > u0; b0 += kAttnThreads) {
-      const int b = b0 + tid;
-      long long u = 0;
-      if (b < p.batch.batch) u = hk * attn_seq_units<NT>(kv_seq(p.batch, ps, b, nullptr), p.group, p.window);
-      long long sum = u;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
+  const int active = (int)min(total, (long long)gridDim.x);
+  AttnShare share{0, 0};
+  if (active > 0) {
+    if (total >> 31)
+      share.per = total / active;
+    else
+      share.per = (unsigned)total / (unsigned)active;
+    share.rest = total - share.per * active;
+  }
+  const bool busy = (int)blockIdx.x < active;
+  const long long u0 = busy ? share.begin(blockIdx.x) : 0, u1 = busy ? share.begin(blockIdx.x + 1) : 0;
+  if (busy && u0 >= before && u0 < before + mine) {
+    int b = b_last - 1;
+    if (per_thread > 1) {
+      for (b = b_first;; ++b) {
+        own = kv_seq(p.batch, ps, b, nullptr);
+        units = attn_seq_units<NT>(own, p.group, p.window);
+        if (u0 < before + units * hk) break;
+        before += units * hk;
       }
-      __syncthreads();
-      if (lane == 31) c.scan[warp] = sum;
-      __syncthreads();
-      long long at = before + sum - u;
-#pragma unroll
-      for (int w = 0; w < kAttnThreads / 32; ++w) {
-        at += w < warp ? c.scan[w] : 0;
-        before += c.scan[w];
-      }
-      if (u0 >= at && u0 < at + u) {
-        c.start_b = b;
-        c.start_off = u0 - at;
-      }
-      if (before > u0) break;
     }
+    long long off = u0 - before;
+    int h = 0, j = 0;
+    for (; off >= units; off -= units) ++h;
+    AttnItem it = attn_item<NT>(own, p.group, p.window, 0);
+    while (off >= it.units()) {
+      off -= it.units();
+      it = attn_item<NT>(own, p.group, p.window, ++j);
+    }
+    c.start_b = b;
+    c.start_h = h;
+    c.start_j = j;
+    c.start_skip = (int)off;
+    c.start_seq = own;
   }
   __syncthreads();
 
-  if (warp == 4) {
+  if (warp == kSoftmax) {
     // ------------------------------------------------------- walk and TMA loads
     const uint64_t policy = p.reuse ? policy_evict_last() : policy_evict_first();
-    int b = c.start_b, h = 0, j = 0, skip = 0, sq = 0, pieces = 0;
-    long long left = b >= 0 ? u1 - u0 : 0;
-    KvSeq s{0, 0, 0};
+    int b = c.start_b, h = c.start_h, j = c.start_j, skip = c.start_skip, sq = 0;
+    long long u = u0;  // next unit
+    KvSeq s = c.start_seq;
     AttnItem it{};
     bool ok = true;
-    if (left > 0) {
-      s = kv_seq(p.batch, ps, b, nullptr);
-      const long long per = attn_seq_units<NT>(s, p.group, p.window);
-      long long off = c.start_off;
-      h = (int)(off / per);
-      off -= h * per;
-      it = attn_item<NT>(s, p.group, p.window, 0);
-      while (off >= it.units()) {
-        off -= it.units();
-        it = attn_item<NT>(s, p.group, p.window, ++j);
-      }
-      skip = (int)off;
-    }
+    AttnPiece piece{};  // of the row tile that goes on in the next CTA
+    if (b >= 0)
+      it = attn_item<NT>(s, p.group, p.window, j);
+    else
+      u = u1;
     int t = 0, t_end = 0;  // tiles of the segment handed out last
-    auto hand_out = [&](const AttnSeg& g) {
-      const int qi = sq % kAttnQueue;
-      if (ok && !mbar_wait_or_abort(smem_u32(&c.segempty[qi]), ((sq / kAttnQueue) & 1) ^ 1, abort_flag)) {
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
         if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
         *abort_flag = 1;
         ok = false;
       }
       ok = __all_sync(0xffffffffu, ok);
+    };
+    auto hand_out = [&](const AttnSeg& g) {
+      const int qi = sq % kAttnQueue;
+      wait(&c.segempty[qi], ((sq / kAttnQueue) & 1) ^ 1);
       if (!ok) return;
       if (lane == 0) {
         c.seg[qi] = g;
@@ -363,18 +413,18 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       }
       ++sq;
     };
-    // The next tile of this CTA's share; hands out the segments it enters.
     struct Tile {
-      int tile, h, flags, page;  // page: this lane's, -1 = none
+      int h, flags;
+      int page;  // this lane's table entry, -1 = none
       float ks, vs;
     };
     AttnItem cur{};
     int cur_h = 0, cur_b = 0, cur_p0 = 0, cur_p1 = 0;
+    // The next tile of this CTA's share; hands out the segments it enters.
     auto next_tile = [&](Tile& x) -> bool {
       while (t == t_end) {
-        if (left <= 0 || !ok) return false;
-        const int nt = (s.n * p.group + NT - 1) / NT;
-        if (j >= nt || s.n == 0) {
+        if (u >= u1 || !ok) return false;
+        if (it.nrows <= 0) {  // past the last row tile of the head
           j = 0;
           if (s.n == 0 || ++h == hk) {
             h = 0;
@@ -385,8 +435,8 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
           }
           it = attn_item<NT>(s, p.group, p.window, 0);
         }
-        const int units = it.units(), take = (int)min(left, (long long)(units - skip));
-        left -= take;
+        const int units = it.units(), take = (int)min(u1 - u, (long long)(units - skip));
+        u += take;
         if (it.tb <= it.ta) {  // rows that see nothing: zeros
           for (int e = lane; e < it.nrows * (D / 8); e += 32) {
             const int r = it.r0 + e / (D / 8);
@@ -410,13 +460,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         g.thi = it.thi;
         g.slot = 2 * (int)blockIdx.x + (skip == 0 ? 1 : 0);
         g.pad = 0;
-        if (lane == 0 && (g.kind & (kSegStart | kSegEnd)) != (kSegStart | kSegEnd)) {
-          AttnPiece pc = {1, (g.kind & kSegEnd) ? 1 : 0, h, s.row0, it.r0, it.nrows, {0, 0}};
-          p.pieces[g.slot] = pc;
-        }
-        if ((g.kind & (kSegStart | kSegEnd)) != (kSegStart | kSegEnd)) pieces |= 1 << (g.slot & 1);
         hand_out(g);
         if (!ok) return false;
+        if (g.kind == kSegStart) piece = {share.cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
         t = g.ta;
         t_end = g.tb;
         cur = it;
@@ -428,18 +474,25 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         if (g.kind & kSegEnd) it = attn_item<NT>(s, p.group, p.window, ++j);
       }
       const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
-      x.tile = t++;
+      ++t;
       x.h = cur_h;
       x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
       if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
       // This lane's page of the tile, where some row sees a position of it.
       const int block = (x0 >> ps) + lane, at = block << ps;
       x.page = -1;
-      if (lane < (kAttnTile >> ps) && at < cur.thi && at + (1 << ps) > cur.tlo)
-        x.page = kv_page(p.batch, p.cache.num_pages, cur_b, block, p.err);
+      if (lane < (kAttnTile >> ps) && at < cur.thi && at + (1 << ps) > cur.tlo) {
+        x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
+        x.flags |= 4;
+      }
       return true;
     };
+    // Checks the entry and asks for the page's scales.
     auto load_scales = [&](Tile& x) {
+      if ((x.flags & 4) && (x.page < 0 || x.page >= p.cache.num_pages)) {
+        report_error(p.err, kErrIndex);
+        x.page = -1;
+      }
       x.ks = x.vs = 0.f;
       if (x.page >= 0) {
         const long long at = (long long)x.page * p.cache.scale_stride + x.h;
@@ -447,35 +500,22 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         x.vs = p.cache.v_scale[at];
       }
     };
-    // Two tiles ahead of the copies: table entries, then (dependent) scales.
+    // Two tiles ahead of the copies: table entries, then (dependent) scales,
+    // which reach the stage while its copies are under way.
     Tile a{}, n1{}, n2{};
     bool has_a = next_tile(a), has_1 = has_a && next_tile(n1);
     if (has_a) load_scales(a);
-    int i = 0;
+    int i = 0, slot = 0;
+    uint32_t par = 0;
+    const int per_tile = kAttnTile >> ps;
+    const uint32_t page_bytes = (uint32_t)D << ps;
     while (has_a && ok) {
-      const bool has_2 = has_1 && next_tile(n2);
-      if (has_1) load_scales(n1);
-      const int slot = i % S;
-      if (i >= S && !mbar_wait_or_abort(smem_u32(&c.empty[slot]), ((i / S) & 1) ^ 1, abort_flag)) {
-        if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
-        *abort_flag = 1;
-        ok = false;
-      }
-      ok = __all_sync(0xffffffffu, ok);
+      if (i >= S) wait(&c.empty[slot], par ^ 1u);
       if (!ok) break;
-      const int per_tile = kAttnTile >> ps;
       const unsigned live = __ballot_sync(0xffffffffu, a.page >= 0);
-      if (lane < per_tile) {
-        c.kscale[slot][lane] = a.ks;
-        // (an exponent of -inf marks a page that is not there)
-        c.vexp[slot][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
-      }
-      if (lane == 0) c.flags[slot] = a.flags | (__popc(live) < per_tile ? 1 : 0);
-      __syncwarp();
       const uint32_t kb = smem_u32(&c.kfull[slot]), vb = smem_u32(&c.vfull[slot]);
-      const uint32_t page_bytes = (uint32_t)D << ps;
       if (lane == 0) {
-        mbar_arrive_expect_tx(kb, (uint32_t)__popc(live) * page_bytes);
+        mbar_expect_tx(kb, (uint32_t)__popc(live) * page_bytes);
         mbar_arrive_expect_tx(vb, (uint32_t)__popc(live) * page_bytes);
       }
       __syncwarp();
@@ -484,7 +524,21 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         tma_load_4d(dst + Sh::kTileBytes, &tmK, 0, 0, a.h, a.page, kb, policy);
         tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, vb, policy);
       }
+      const bool has_2 = has_1 && next_tile(n2);
+      if (has_1) load_scales(n1);
+      if (lane < per_tile) {
+        c.kscale[slot][lane] = a.ks;
+        // (an exponent of -inf marks a page that is not there)
+        c.vexp[slot][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
+      }
+      if (lane == 0) c.flags[slot] = (a.flags & 3) | (__popc(live) < per_tile ? 1 : 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kb);
       ++i;
+      if (++slot == S) {
+        slot = 0;
+        par ^= 1u;
+      }
       a = n1;
       n1 = n2;
       has_a = has_1;
@@ -493,90 +547,110 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
     AttnSeg stop{};
     stop.kind = kSegStop;
     hand_out(stop);
-    if (lane < 2 && !(pieces >> lane & 1)) p.pieces[2 * blockIdx.x + lane].valid = 0;
+    if (lane == 0) p.pieces[blockIdx.x] = piece;
     // Every copy that this warp issued lands before the CTA may exit.
     bool landed = true;
     for (int k = i > S ? i - S : 0; k < i && landed; ++k)
       landed = mbar_wait(smem_u32(&c.kfull[k % S]), (k / S) & 1) && mbar_wait(smem_u32(&c.vfull[k % S]), (k / S) & 1);
     if (!landed) report_error(p.err, kErrDrain);
-  } else if (warp == 5) {
+  } else if (warp == kSoftmax + 1) {
     // ------------------------------------------------------------- MMA issuer
+    // Issues whichever of the two products can go: V^T P^T of the oldest tile
+    // whose weights are written, or K Q^T of the next one.  Neither waits for
+    // the other's inputs.
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_e4m3_f32(kAttnTile, kCols), idesc_o = idesc_s | (1u << 15);
       const uint32_t acc_o = tmem + 2 * kCols;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
-          if (!*abort_flag) report_error(p.err, kErrWaitFull);
-          *abort_flag = 1;
-          ok = false;
-        }
-      };
-      // O of tile k = V^T P^T, once its weights are written.
-      auto value_product = [&](int k) {
-        const int slot = k % S;
-        wait(&c.vfull[slot], (k / S) & 1);
-        wait(&c.pfull, k & 1);
-        wait(&c.oempty[k & 1], ((k >> 1) & 1) ^ 1);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t v = ring + (uint32_t)slot * Sh::kStageBytes;
-        // D = 64: the upper half of the 128 rows reads the K tile behind V;
-        // its rows of the accumulator are not used.
-        const uint64_t vd = smem_desc_rows<D>(v, Sh::kTileBytes), pd = smem_desc_rows<128>(pbuf);
-#pragma unroll
-        for (int kk = 0; kk < kAttnTile / 32; ++kk)
-          mma_e4m3(acc_o + (k & 1) * kCols, vd + (uint64_t)(kk * (32 * D >> 4)), pd + (uint64_t)(kk * 2), idesc_o, kk > 0);
-        mma_commit(smem_u32(&c.ofull[k & 1]));
-        mma_commit(smem_u32(&c.empty[slot]));
-      };
-      int i = 0, sq = 0, filled = 0;
-      while (ok) {
-        const int qi = sq % kAttnQueue;
-        wait(&c.segfull[qi], (sq / kAttnQueue) & 1);
-        if (!ok) break;
-        const int kind = c.seg[qi].kind, ta = c.seg[qi].ta, tb = c.seg[qi].tb;
-        mbar_arrive(smem_u32(&c.segempty[qi]));
-        ++sq;
-        if (kind & kSegStop) break;
-        wait(&c.qfull[filled & 1], (filled >> 1) & 1);
-        const uint64_t qd = smem_desc_rows<D>(qbuf + (filled & 1) * Sh::kQBytes);
-        for (int t = ta; t < tb && ok; ++t, ++i) {
-          const int slot = i % S;
-          wait(&c.kfull[slot], (i / S) & 1);
-          wait(&c.sempty[i & 1], ((i >> 1) & 1) ^ 1);
-          if (!ok) break;
+      int sq = 0, filled = -1, t = 0, t_end = 0;  // segments read, query buffer in use, its tiles
+      int i = 0, islot = 0, k = 0, kslot = 0;     // tiles scored, tiles weighted
+      uint32_t ipar = 0, kpar = 0;
+      bool fresh = false, stop = false, ok = true;
+      uint64_t since = 0;
+      unsigned idle = 0;
+      while (ok && (!stop || k < i)) {
+        if (k < i && mbar_test_wait(smem_u32(&c.pfull), k & 1) && mbar_test_wait(smem_u32(&c.vfull[kslot]), kpar) &&
+            mbar_test_wait(smem_u32(&c.oempty[k & 1]), ((k >> 1) & 1) ^ 1)) {
           tc_fence_after();
-          const uint64_t kd = smem_desc_rows<D>(ring + (uint32_t)slot * Sh::kStageBytes + Sh::kTileBytes);
+          // D = 64: the upper half of the 128 rows reads the K tile behind V;
+          // its rows of the accumulator are not used.
+          const uint64_t vd = smem_desc_rows<D>(ring + (uint32_t)kslot * Sh::kStageBytes, Sh::kTileBytes);
+          const uint64_t pd = smem_desc_rows<128>(pbuf);
+#pragma unroll
+          for (int kk = 0; kk < kAttnTile / 32; ++kk)
+            mma_e4m3(acc_o + (k & 1) * kCols, vd + (uint64_t)(kk * (32 * D >> 4)), pd + (uint64_t)(kk * 2), idesc_o, kk > 0);
+          mma_commit(smem_u32(&c.ofull[k & 1]));
+          mma_commit(smem_u32(&c.empty[kslot]));
+          ++k;
+          if (++kslot == S) {
+            kslot = 0;
+            kpar ^= 1u;
+          }
+          idle = 0;
+          continue;
+        }
+        if (!stop && t == t_end) {
+          const int qi = sq % kAttnQueue;
+          if (mbar_test_wait(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1)) {
+            stop = (c.seg[qi].kind & kSegStop) != 0;
+            t = c.seg[qi].ta;
+            t_end = c.seg[qi].tb;
+            mbar_arrive(smem_u32(&c.segempty[qi]));
+            ++sq;
+            ++filled;
+            fresh = true;
+            idle = 0;
+            continue;
+          }
+        } else if (!stop && (!fresh || mbar_test_wait(smem_u32(&c.qfull[filled % Q]), (filled / Q) & 1)) &&
+                   mbar_test_wait(smem_u32(&c.kfull[islot]), ipar) &&
+                   mbar_test_wait(smem_u32(&c.sempty[i & 1]), ((i >> 1) & 1) ^ 1)) {
+          fresh = false;
+          tc_fence_after();
+          const uint64_t kd = smem_desc_rows<D>(ring + (uint32_t)islot * Sh::kStageBytes + Sh::kTileBytes);
+          const uint64_t qd = smem_desc_rows<D>(qbuf + (uint32_t)(filled % Q) * Sh::kQBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
             mma_e4m3(tmem + (i & 1) * kCols, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc_s, kk > 0);
           mma_commit(smem_u32(&c.sfull[i & 1]));
-          if (t == tb - 1) mma_commit(smem_u32(&c.qempty[filled & 1]));
-          if (i > 0) value_product(i - 1);
+          if (++t == t_end) mma_commit(smem_u32(&c.qempty[filled % Q]));
+          ++i;
+          if (++islot == S) {
+            islot = 0;
+            ipar ^= 1u;
+          }
+          idle = 0;
+          continue;
         }
-        ++filled;
+        // Nothing to issue: bounded, as every wait.
+        if (idle == 0) since = globaltimer_ns();
+        if ((++idle & 63u) == 0) {
+          if (*abort_flag) ok = false;
+          if (globaltimer_ns() - since > SGR_WAIT_LIMIT_NS) {
+            report_error(p.err, kErrWaitFull);
+            *abort_flag = 1;
+            ok = false;
+          }
+        }
       }
-      if (ok && i > 0) value_product(i - 1);
       mma_commit(smem_u32(&c.drain));
       if (!mbar_wait(smem_u32(&c.drain), 0)) report_error(p.err, kErrDrain);
     }
-  } else if (warp >= 6) {
+  } else if (warp >= kSoftmax + 2) {
     // ----------------------------------------------------------- query operand
-    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kPass = NT / kRows > 0 ? NT / kRows : 1;
-    const int qt = tid - 192, l = qt % kLanes;
-    int sq = 0, filled = 0;
+    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kPass = NT / kRows;
+    const int qt = tid - 32 * (kSoftmax + 2), l = qt % kLanes;
+    int sq = 0, buf = 0;
+    uint32_t par = 0;
     while (true) {
       const int qi = sq % kAttnQueue;
       bool ok = true;
-      if (lane == 0) ok = mbar_wait_sleepy_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
+      if (lane == 0) ok = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       const AttnSeg g = c.seg[qi];
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
       ++sq;
       if (g.kind & kSegStop) break;
-      const int buf = filled & 1;
       uint4 v[kPass];
       long long out_at[kPass];
       int pos[kPass];
@@ -587,13 +661,13 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
         pos[i] = -1;  // a row that is none sees nothing
         out_at[i] = 0;
         if (q < g.nrows) {
-          const int tok = r / p.group, head = g.h * p.group + r % p.group;
+          const int tok = r / p.group, head = g.h * p.group + r - tok * p.group;
           pos[i] = g.first + tok;
           out_at[i] = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
           v[i] = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         }
       }
-      if (lane == 0) ok = mbar_wait_sleepy_or_abort(smem_u32(&c.qempty[buf]), ((filled >> 1) & 1) ^ 1, abort_flag);
+      if (lane == 0) ok = mbar_wait_or_abort(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
@@ -618,27 +692,28 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (x[e] - h[e]) * 32.f;  // exact
         const uint2 lo = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
-        if (q < NT) {
-          const uint32_t qb = qbuf + (uint32_t)(buf * Sh::kQBytes) + (uint32_t)((l & 1) * 8);
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(hi.x), "r"(hi.y) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(NT + q, l >> 1)), "r"(lo.x), "r"(lo.y) : "memory");
-          if (l == 0) {
-            // a row with an infinity or NaN gets NaN
-            c.qf[buf][q] = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k) * p.scale_log2;
-            c.qpos[buf][q] = pos[i];
-            c.qout[buf][q] = out_at[i];
-          }
+        const uint32_t qb = qbuf + (uint32_t)(buf * Sh::kQBytes) + (uint32_t)((l & 1) * 8);
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(hi.x), "r"(hi.y) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(NT + q, l >> 1)), "r"(lo.x), "r"(lo.y) : "memory");
+        if (l == 0) {
+          // a row with an infinity or NaN gets NaN
+          c.qf[buf][q] = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k) * p.scale_log2;
+          c.qpos[buf][q] = pos[i];
+          c.qout[buf][q] = out_at[i];
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.qfull[buf]));
-      ++filled;
+      if (++buf == Q) {
+        buf = 0;
+        par ^= 1u;
+      }
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    // After a wait that ran out (abort) the waits fall through, so that all
-    // four warps keep meeting at their barrier until the segments end.
+    // After a wait that ran out (abort) the waits fall through, so that the
+    // warps keep meeting at their barriers until the segments end.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (!mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
         if (!*abort_flag) report_error(p.err, kErrWaitMma);
@@ -646,31 +721,44 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       }
       __syncwarp();
     };
-    const uint32_t lane_base = (uint32_t)warp << 21;  // tensor-memory lane 32 warp
-    float o[NT], l[NT];
-    float run = 0.f;  // running maximum of row `lane`
+    const int group = warp >> 2, tok = tid & 127, q0 = group * C;  // columns q0 .. q0 + C - 1
+    auto meet = [&] {  // the group's 4 warps
+      __syncwarp();
+      if (Sh::kGroups == 1 || group == 0)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      else
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+    };
+    const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)q0;  // tensor-memory lanes of this warp
+    float o[C], l[C];
+    float run = 0.f;  // running maximum of column q0 + lane
     unsigned nan_rows = 0;
-    int i = 0, sq = 0, filled = 0;
+    int i = 0, slot = 0, sq = 0, buf = 0;
+    uint32_t par = 0, qpar = 0;
+    bool scaled_before = false;  // whether the tile before needs its factors
     // O of tile k, read back and accumulated.
-    auto accumulate = [&](int k) {
+    auto accumulate = [&](int k, bool scaled) {
       wait(&c.ofull[k & 1], (k >> 1) & 1);
       tc_fence_after();
-      float x[NT];
-      tmem_ld_sum<NT>(tmem + lane_base + 2 * kCols + (k & 1) * kCols, x);
+      float x[C];
+      tmem_ld_sum<C>(lane_base + 2 * kCols + (k & 1) * kCols, NT, x);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.oempty[k & 1]));
+      if (scaled) {
 #pragma unroll
-      for (int q = 0; q < NT; ++q) o[q] = fmaf(x[q], c.beta[warp][k & 1][q], o[q] * c.alpha[warp][k & 1][q]);
+        for (int q = 0; q < C; ++q) o[q] = fmaf(x[q], c.beta[warp][k & 1][q], o[q] * c.alpha[warp][k & 1][q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < C; ++q) o[q] += x[q];
+      }
     };
     while (true) {
       const int qi = sq % kAttnQueue;
-      if (tid == 0)
-        c.go[sq & 1] = mbar_wait_sleepy_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
-      __syncwarp();
-      named_bar_sync(1, 128);
-      if (!c.go[sq & 1]) {
-        if (tid == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
+      if (tok == 0) c.go[group][sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
+      meet();
+      if (!c.go[group][sq & 1]) {
+        if (tok == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
         *abort_flag = 1;
         break;
       }
@@ -679,228 +767,234 @@ __global__ void __launch_bounds__(kAttnThreads, 2)
       if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
       ++sq;
       if (g.kind & kSegStop) break;
-      const int buf = filled & 1;
-      wait(&c.qfull[buf], (filled >> 1) & 1);
+      wait(&c.qfull[buf], qpar);
 #pragma unroll
-      for (int q = 0; q < NT; ++q) o[q] = l[q] = 0.f;
+      for (int q = 0; q < C; ++q) o[q] = l[q] = 0.f;
       run = -3.0e38f;
       nan_rows = 0;
-      for (int t = g.ta; t < g.tb; ++t, ++i) {
-        const int slot = i % S, sb = i & 1;
+      for (int t = g.ta; t < g.tb; ++t) {
+        const int sb = i & 1;
         wait(&c.sfull[sb], (i >> 1) & 1);
-        wait(&c.kfull[slot], (i / S) & 1);  // (orders this thread's reads of the page scales)
+        wait(&c.kfull[slot], par);  // (orders this thread's reads of the page scales)
         tc_fence_after();
-        float x[NT];
-        tmem_ld_sum<NT>(tmem + lane_base + sb * kCols, x);
+        float x[C];
+        tmem_ld_sum<C>(lane_base + sb * kCols, NT, x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.sempty[sb]));
-        const int pi = tid >> ps, flags = c.flags[slot], pos = t * kAttnTile + tid;
+        const int pi = tok >> ps, flags = c.flags[slot], pos = t * kAttnTile + tok;
         const float ks = c.kscale[slot][pi], ve = c.vexp[slot][pi];
         const bool live = !(flags & 1) || (pos >= g.tlo && pos < g.thi && ve > -INFINITY);
 #pragma unroll
-        for (int q = 0; q < NT; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q], ve);
+        for (int q = 0; q < C; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q0 + q], ve);
         if (flags & 2) {
 #pragma unroll
-          for (int q = 0; q < NT; ++q) {
-            const int last = c.qpos[buf][q];
+          for (int q = 0; q < C; ++q) {
+            const int last = c.qpos[buf][q0 + q];
             if (!(live && pos <= last && pos > last - p.window)) x[q] = -INFINITY;
           }
         } else if (!live) {
 #pragma unroll
-          for (int q = 0; q < NT; ++q) x[q] = -INFINITY;
+          for (int q = 0; q < C; ++q) x[q] = -INFINITY;
         }
-        // The tile's maximum of each row, rounded up; lane q keeps row q's.
+        // The tile's maximum of each column, rounded up; lane q keeps column
+        // q's.  Weights are taken relative to the running maximum where the
+        // tile's lies at most 2^4 below it (then nothing is rescaled), else to
+        // the tile's own.
         float top = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
+        for (int q = 0; q < C; ++q) {
           const float w = warp_max(x[q]);
           if (lane == q) top = w;
         }
-        if (lane < NT) c.wmax[sb][warp][lane] = top;
-        __syncwarp();
-        named_bar_sync(1, 128);
-        if (lane < NT) {
-          top = fmaxf(fmaxf(c.wmax[sb][0][lane], c.wmax[sb][1][lane]), fmaxf(c.wmax[sb][2][lane], c.wmax[sb][3][lane]));
-          const float m = fmaxf(ceilf(top), -3.0e38f), now = fmaxf(run, m);
-          c.m[warp][lane] = m;
-          c.alpha[warp][sb][lane] = exp2_whole(run - now);
-          c.beta[warp][sb][lane] = exp2_whole(m - now);
+        if (lane < C) c.wmax[sb][warp][lane] = top;
+        meet();
+        bool scaled = false;
+        if (lane < C) {
+          const int w0 = warp & ~3;
+          top = fmaxf(fmaxf(c.wmax[sb][w0][lane], c.wmax[sb][w0 + 1][lane]), fmaxf(c.wmax[sb][w0 + 2][lane], c.wmax[sb][w0 + 3][lane]));
+          const float m = fmaxf(ceilf(top), -3.0e38f), now = fmaxf(run, m), ref = now - m <= 4.f ? now : m;
+          const float al = exp2_whole(run - now), be = exp2_whole(ref - now);
+          c.m[warp][lane] = ref - 8.f;  // weights come as 256 p
+          c.alpha[warp][sb][lane] = al;
+          c.beta[warp][sb][lane] = be;
+          scaled = al != 1.f || be != 1.f;
           run = now;
         }
-        __syncwarp();
+        scaled = __any_sync(0xffffffffu, scaled);
         const float iv = live ? kv_exp2i(-(int)ve) : 0.f;  // the value scale does not count in the sum of weights
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          x[q] = ex2(x[q] - c.m[warp][q]);
-          l[q] = fmaf(x[q] * iv, c.beta[warp][sb][q], l[q] * c.alpha[warp][sb][q]);
+        for (int q = 0; q < C; ++q) x[q] = ex2(x[q] - c.m[warp][q]);
+        if (scaled) {
+#pragma unroll
+          for (int q = 0; q < C; ++q) l[q] = fmaf(x[q] * iv, c.beta[warp][sb][q], l[q] * c.alpha[warp][sb][q]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < C; ++q) l[q] = fmaf(x[q], iv, l[q]);
         }
         const bool joined = t > g.ta;
         if (joined) wait(&c.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);  // the weights before are read
         if (flags) {
-          wait(&c.vfull[slot], (i / S) & 1);
+          wait(&c.vfull[slot], par);
           const uint32_t vt = ring + (uint32_t)slot * Sh::kStageBytes;
           // Values of tokens that no row sees must not reach the product
           // (0 x NaN): their codes become zeros.
-          if (!live) {
+          if (!live && group == 0) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)(tid * D + k * 16)), "r"(0u) : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)(tok * D + k * 16)), "r"(0u) : "memory");
           }
           if (flags & 2) {
             // A NaN value that some rows see and others do not: those that do
-            // get their NaN below, and the code becomes zero.
+            // get their NaN here, and the code becomes zero.
             bool nan = false;
-            if (live) {
+            if (live && group == 0) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k) {
-                const uint4 u = lds128(vt + (uint32_t)(tid * D + k * 16));
+                const uint4 u = lds128(vt + (uint32_t)(tok * D + k * 16));
                 const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) nan |= (((w4[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
               }
             }
             const unsigned any = __ballot_sync(0xffffffffu, nan);
-            if (lane == 0) c.nan_tokens[warp] = any;
+            if (lane == 0 && group == 0) c.nan_tokens[warp] = any;
             __syncwarp();
-            named_bar_sync(1, 128);
+            asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");
             if ((c.nan_tokens[0] | c.nan_tokens[1] | c.nan_tokens[2] | c.nan_tokens[3]) != 0) {
               for (int k = 0; k < kAttnTile; ++k) {
-                if (!(c.nan_tokens[k >> 5] >> (k & 31) & 1) || tid >= D) continue;
-                const uint32_t at = vt + swizzled<D>(k, tid >> 4) + (tid & 15);
-                if ((lds8(at) & 0x7F) != 0x7F) continue;
-                for (int q = 0; q < NT; ++q) {
-                  const int last = c.qpos[buf][q], kp = t * kAttnTile + k;
+                if (!(c.nan_tokens[k >> 5] >> (k & 31) & 1) || tok >= D) continue;
+                if ((lds8(vt + swizzled<D>(k, tok >> 4) + (tok & 15)) & 0x7F) != 0x7F) continue;
+                for (int q = 0; q < C; ++q) {
+                  const int last = c.qpos[buf][q0 + q], kp = t * kAttnTile + k;
                   if (kp <= last && kp > last - p.window) nan_rows |= 1u << q;
                 }
-                sts8(at, 0);
               }
               __syncwarp();
-              named_bar_sync(1, 128);  // nan_tokens is read
+              asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");  // all have seen the codes
+              if (nan) {
+                for (int k = 0; k < D; ++k)
+                  if ((lds8(vt + (uint32_t)(tok * D + k)) & 0x7F) == 0x7F) sts8(vt + (uint32_t)(tok * D + k), 0);
+              }
             }
+            __syncwarp();
           }
         }
-        const uint32_t col = (uint32_t)(tid & 15), chunk = tid >> 4;
+        const uint32_t col = (uint32_t)(tok & 15), chunk = tok >> 4;
 #pragma unroll
-        for (int q = 0; q < NT; q += 2) {
-          const uint32_t u = split2(x[q] * 256.f, x[q + 1] * 256.f);
-          sts8(pbuf + swizzled<128>(q, chunk) + col, u);
-          sts8(pbuf + swizzled<128>(q + 1, chunk) + col, u >> 8);
-          sts8(pbuf + swizzled<128>(NT + q, chunk) + col, u >> 16);
-          sts8(pbuf + swizzled<128>(NT + q + 1, chunk) + col, u >> 24);
+        for (int q = 0; q < C; q += 2) {
+          const uint32_t u = split2(x[q], x[q + 1]);
+          // (q0 is a multiple of 8: it does not change the swizzle)
+          sts8(pbuf + q0 * 128 + swizzled<128>(q, chunk) + col, u);
+          sts8(pbuf + q0 * 128 + swizzled<128>(q + 1, chunk) + col, u >> 8);
+          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q, chunk) + col, u >> 16);
+          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q + 1, chunk) + col, u >> 24);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.pfull));
-        if (joined) accumulate(i - 1);
+        if (joined) accumulate(i - 1, scaled_before);
+        scaled_before = scaled;
+        ++i;
+        if (++slot == S) {
+          slot = 0;
+          par ^= 1u;
+        }
       }
-      accumulate(i - 1);
+      accumulate(i - 1, scaled_before);
       // ------------------------------------------------------- the segment's end
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        float w = l[q];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-        if (lane == 0) c.wsum[warp][q] = w;
+      const float part = warp_column_sums<C>(l);
+      if (lane % (32 / C) == 0) c.wsum[warp][lane / (32 / C)] = part;
+      meet();
+      const bool whole = (g.kind & (kSegStart | kSegEnd)) == (kSegStart | kSegEnd);
+      if (lane < C) {
+        const int w0 = warp & ~3;
+        const float sum = c.wsum[w0][lane] + c.wsum[w0 + 1][lane] + c.wsum[w0 + 2][lane] + c.wsum[w0 + 3][lane];
+        c.m[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole && (warp & 3) == 0 && q0 + lane < g.nrows)
+          p.part_ml[(long long)g.slot * NT + q0 + lane] = make_float2(run, sum);
       }
       __syncwarp();
-      named_bar_sync(1, 128);
-      const float nan_f = __int_as_float(0x7fffffff);
-      const bool whole = (g.kind & (kSegStart | kSegEnd)) == (kSegStart | kSegEnd);
-      if (tid < D) {
+      if (tok < D) {
 #pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          if (q < g.nrows) {
-            float v = nan_rows >> q & 1 ? nan_f : o[q] * (1.f / 256.f);
-            if (whole) {
-              const float sum = c.wsum[0][q] + c.wsum[1][q] + c.wsum[2][q] + c.wsum[3][q];
-              p.out.p[c.qout[buf][q] + tid] = __float2bfloat16(sum == 0.f ? 0.f : v / sum);
-            } else {
-              p.part_o[((long long)g.slot * NT + q) * D + tid] = v;
-            }
+        for (int q = 0; q < C; ++q) {
+          const float v = nan_rows >> q & 1 ? __int_as_float(0x7fffffff) : o[q];
+          if (q0 + q < g.nrows) {
+            if (whole)
+              p.out.p[c.qout[buf][q0 + q] + tok] = __float2bfloat16(v * c.m[warp][q]);
+            else
+              p.part_o[((long long)g.slot * NT + q0 + q) * D + tok] = v;
           }
         }
       }
-      if (!whole && warp == 0 && lane < g.nrows)
-        p.part_ml[(long long)g.slot * NT + lane] =
-            make_float2(run, c.wsum[0][lane] + c.wsum[1][lane] + c.wsum[2][lane] + c.wsum[3][lane]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.qempty[buf]));
-      ++filled;
+      if (++buf == Q) {
+        buf = 0;
+        qpar ^= 1u;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kSoftmax + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Sh::kTmemCols);
   }
 }
 
-// Joins the partial sums of row tiles that span CTAs: block (c, q) takes row
-// q of the row tile that begins in CTA c and ends in a later one, if any.
-// The pieces are those of CTAs c, c+1, ... up to the one marked last.
+// Joins the partial sums of row tiles that span CTAs: block c takes the row
+// tile that begins in CTA c and ends in a later one, if any, a warp a row; its
+// pieces are those of CTAs c, c + 1, ..., last.
 constexpr int kJoinThreads = 256;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnParams p, int grid) {
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes;
-  __shared__ int end;
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float4 part[kGroups][kLanes];
-  __shared__ float part_l[kGroups];
+__global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnParams p) {
+  constexpr int kE = D / 32;  // elements a lane
   pdl_launch_dependents();
   pdl_wait();
-  const int c0 = blockIdx.x, q = blockIdx.y, tid = threadIdx.x;
-  const AttnPiece own = p.pieces[2 * c0 + 1];
-  if (!own.valid || q >= own.nrows) return;
-  if (tid == 0) end = grid;
-  __syncthreads();
-  for (int b = c0 + 1; b < grid; b += kJoinThreads) {
-    const int k = b + tid;
-    if (k < grid && p.pieces[2 * k].valid && p.pieces[2 * k].last) atomicMin(&end, k);
-    __syncthreads();
-    if (end < grid) break;
-    __syncthreads();
-  }
-  __syncthreads();
-  const int n = min(end, grid - 1) - c0 + 1;
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = blockIdx.y * (kJoinThreads / 32) + warp;
+  const AttnPiece own = p.pieces[c0];
+  if (own.last <= c0 || q >= own.nrows) return;
+  const int n = own.last - c0 + 1;
   auto slot = [&](int k) { return (long long)(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * NT + q; };
-  float m = -3.0e38f;
-  for (int k = tid; k < n; k += kJoinThreads) m = fmaxf(m, p.part_ml[slot(k)].x);
+  float m = -3.0e38f, sum = 0.f, o[kE];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((tid & 31) == 0) red[tid >> 5] = m;
-  __syncthreads();
+  for (int e = 0; e < kE; ++e) o[e] = 0.f;
+  for (int k0 = 0; k0 < n; k0 += 32) {  // lane k: factor of piece k0 + k
+    float2 ml = make_float2(-3.0e38f, 0.f);
+    if (k0 + lane < n) ml = p.part_ml[slot(k0 + lane)];
+    const float now = fmaxf(m, warp_max(ml.x)), f = exp2_whole(ml.x - now), old = exp2_whole(m - now);
+    float w = ml.y * f;
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, red[w]);
-  const int gr = tid / kLanes, l = tid % kLanes;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int k = gr; k < n; k += kGroups) {
-    const float2 ml = p.part_ml[slot(k)];
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(k) * D + 4 * l);
-    const float f = exp2_whole(ml.x - m);
-    sum = fmaf(ml.y, f, sum);
-    o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
-  }
-  part[gr][l] = o;
-  if (l == 0) part_l[gr] = sum;
-  __syncthreads();
-  if (tid < kLanes) {
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 v = part[k][l];
-      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
+    sum = sum * old + w;
+    m = now;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] *= old;
+    const int kn = min(32, n - k0);
+#pragma unroll 8
+    for (int k = 0; k < kn; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float* v = p.part_o + slot(k0 + k) * D + lane * kE;
+      if constexpr (kE == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(v);
+        o[0] = fmaf(u.x, fk, o[0]), o[1] = fmaf(u.y, fk, o[1]), o[2] = fmaf(u.z, fk, o[2]), o[3] = fmaf(u.w, fk, o[3]);
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(v);
+        o[0] = fmaf(u.x, fk, o[0]), o[1] = fmaf(u.y, fk, o[1]);
+      }
     }
-    sum = 0.f;
-    for (int k = 0; k < kGroups; ++k) sum += part_l[k];
-    const float f = sum == 0.f ? 0.f : 1.f / sum;
-    const int r = own.r0 + q;
-    __nv_bfloat16* out = p.out.p + (long long)(own.row0 + r / p.group) * p.out.ts +
-                         (long long)(own.h * p.group + r % p.group) * p.out.hs + 4 * l;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
   }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const int r = own.r0 + q;
+  __nv_bfloat16* out = p.out.p + (long long)(own.row0 + r / p.group) * p.out.ts +
+                       (long long)(own.h * p.group + r % p.group) * p.out.hs + lane * kE;
+  if constexpr (kE == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[0] * f, o[1] * f);
 }
 
 }  // namespace sgr
