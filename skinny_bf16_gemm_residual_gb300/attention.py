@@ -17,9 +17,15 @@ they are.  Calls run on the tensors' device, on its current stream unless
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from .binding import (SGR_OK, SgrError, _common_device, _stream_handle, load, sgr_heads, sgr_kv_batch, sgr_kv_cache,
-                      sgr_norm_rope)
+from .binding import (SGR_OK, SgrError, _common_device, load, sgr_heads, sgr_kv_batch, sgr_kv_cache, sgr_norm_rope)
+
+# A call of a few microseconds on the GPU should not wait for its arguments:
+# sgr_heads structures go as packed bytes, devices are compared by index and
+# the current stream is asked for as a number.
+_pack_heads = struct.Struct("@Pqqii").pack
+assert struct.calcsize("@Pqqii") == ctypes.sizeof(sgr_heads)
 
 
 def _check(rc: int, what: str) -> None:
@@ -27,23 +33,40 @@ def _check(rc: int, what: str) -> None:
         raise SgrError(rc, what)
 
 
-def _heads(t, name: str, shape=None) -> sgr_heads:
+def _wrong_heads(t, name: str, shape, index: int):
     import torch
 
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: all tensors must be on one CUDA device, got {t.device} and cuda:{index}")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    tokens, heads, dim = t.shape
-    if shape is not None and (tokens, heads, dim) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {[tokens, heads, dim]}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must have unit inner stride")
+
+
+def _heads(t, name: str, shape, index: int) -> bytes:
+    """The sgr_heads of a tensor of this shape on this device."""
+    import torch
+
+    tokens, heads, dim = shape
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
+        _wrong_heads(t, name, shape, index)
     ts, hs, es = t.stride()
-    if es != 1 and dim > 1:
-        raise ValueError(f"{name} must have unit inner stride")
+    if es != 1:
+        _wrong_heads(t, name, shape, index)
     # Strides of axes with one element are arbitrary in torch.
-    return sgr_heads(t.data_ptr(), ts if tokens > 1 else heads * dim, hs if heads > 1 else dim, heads, 0)
+    return _pack_heads(t.data_ptr(), ts if tokens > 1 else heads * dim, hs if heads > 1 else dim, heads, 0)
+
+
+def _shape3(t, name: str):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    return t.shape
 
 
 def _int32(t, name: str, dim: int):
@@ -78,6 +101,7 @@ class KvCache:
         if k_scale.stride(0) != v_scale.stride(0):
             raise ValueError("k_scale and v_scale must have the same strides")
         self.device = _common_device((k, v, k_scale, v_scale))
+        self.index = self.device.index
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         pages, self.heads, self.page_size, self.head_dim = k.shape
         self.c = sgr_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k.stride(0),
@@ -119,6 +143,7 @@ class KvBatch:
             tokens = batch
         self.block_table, self.seq_len, self.q_start = block_table, seq_len, q_start
         self.device = _common_device([t for t in (block_table, seq_len, q_start) if t is not None])
+        self.index = self.device.index
         self.batch, self.max_pages, self.tokens, self.max_new = batch, max_pages, int(tokens), int(max_new)
         self.c = sgr_kv_batch(block_table.data_ptr(), seq_len.data_ptr(),
                               q_start.data_ptr() if q_start is not None else None,
@@ -143,74 +168,88 @@ class RopeNorm:
                 raise ValueError(f"{n} must be a contiguous 1-D CUDA bfloat16 tensor")
         self.table, self.q_weight, self.k_weight = table, q_weight, k_weight
         tensors = [t for t in (table, q_weight, k_weight) if t is not None]
-        self.device = _common_device(tensors) if tensors else None
-        self.head_dim = {w.shape[0] for w in (q_weight, k_weight) if w is not None}
+        self.index = _common_device(tensors).index if tensors else None
+        dims = {w.shape[0] for w in (q_weight, k_weight) if w is not None}
+        if len(dims) > 1:
+            raise ValueError("q_weight and k_weight must have the same number of elements")
+        self.head_dim = dims.pop() if dims else None
         rows, rot = table.shape if table is not None else (0, 0)
         self.c = sgr_norm_rope(*(t.data_ptr() if t is not None else None for t in (q_weight, k_weight, table)),
                                float(eps), rows, rot, int(interleaved))
         self.ref = ctypes.addressof(self.c)
 
 
-def _on(device, others, name: str):
+def _on(index: int, others, what: str):
     for o in others:
-        if o is not None and o != device:
-            raise ValueError(f"{name}: all tensors must be on one CUDA device, got {device} and {o}")
+        if o is not None and o != index:
+            raise ValueError(f"{what}: all tensors must be on one CUDA device, got cuda:{index} and cuda:{o}")
 
 
-def _call(device, stream, fn):
-    """fn(stream handle) with `device` current."""
+def _launch(index: int, stream, what: str, fn, *args):
+    """fn(*args, stream handle) with device `index` current."""
     import torch
 
-    if torch.cuda.current_device() == device.index:
-        return fn(_stream_handle(stream, device))
-    with torch.cuda.device(device):
-        return fn(_stream_handle(stream, device))
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, int):
+        handle = stream
+    elif stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, tensors on cuda:{index}")
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
+    if rc != SGR_OK:
+        raise SgrError(rc, what)
 
 
-def _new(device, stream, make):
+def _new(index: int, stream, make):
     """A tensor allocated for use on `stream`."""
     import torch
 
     if stream is None:
         return make()
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=index)
     with torch.cuda.stream(stream):
         return make()
 
 
-def _addr(h):
-    return ctypes.addressof(h) if h is not None else None
+def _like(t, stream):
+    import torch
+
+    return _new(t.get_device(), stream, lambda: torch.empty(t.shape, dtype=t.dtype, device=t.device))
 
 
 def sgr_qk_norm_rope(q, k, positions, rope: RopeNorm, q_out=None, k_out=None, flags: int = 0, stream=None):
     """Queries and keys normalised per head and rotated to positions [tokens]
     (int32; a negative one gives a row of zeros); k may be None.  The outputs
     may be the inputs.  Returns (q_out, k_out)."""
-    import torch
-
-    hq = _heads(q, "q")
-    tokens, _, dim = q.shape
+    shape = _shape3(q, "q")
+    tokens, _, dim = shape
+    index = q.get_device()
+    hq = _heads(q, "q", shape, index)
     _int32(positions, "positions", 1)
     if positions.shape[0] != tokens:
         raise ValueError(f"positions must have {tokens} elements, got {positions.shape[0]}")
-    if rope.head_dim - {dim}:
+    if rope.head_dim is not None and rope.head_dim != dim:
         raise ValueError(f"norm weights must have {dim} elements")
     if q_out is None:
-        q_out = _new(q.device, stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
-    hqo = _heads(q_out, "q_out", tuple(q.shape))
+        q_out = _like(q, stream)
+    hqo = _heads(q_out, "q_out", shape, index)
     hk = hko = None
-    devices = [positions.device, rope.device, q_out.device]
     if k is not None:
-        hk = _heads(k, "k", (tokens, k.shape[1], dim))
+        shape = (tokens, _shape3(k, "k")[1], dim)
+        hk = _heads(k, "k", shape, index)
         if k_out is None:
-            k_out = _new(k.device, stream, lambda: torch.empty(k.shape, dtype=k.dtype, device=k.device))
-        hko = _heads(k_out, "k_out", tuple(k.shape))
-        devices += [k.device, k_out.device]
-    _on(q.device, devices, "sgr_qk_norm_rope")
-    _check(_call(q.device, stream, lambda s: load().sgr_qk_norm_rope(
-        _addr(hq), _addr(hk), _addr(hqo), _addr(hko), positions.data_ptr(), tokens, dim, rope.ref, flags, s)),
-        "sgr_qk_norm_rope")
+            k_out = _like(k, stream)
+        hko = _heads(k_out, "k_out", shape, index)
+    _on(index, (positions.get_device(), rope.index), "sgr_qk_norm_rope")
+    _launch(index, stream, "sgr_qk_norm_rope", load().sgr_qk_norm_rope, hq, hk, hqo, hko, positions.data_ptr(), tokens,
+            dim, rope.ref, flags)
     return q_out, k_out
 
 
@@ -219,25 +258,22 @@ def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, 
     """Append the new tokens' keys (normalised, rotated to their positions)
     and values [tokens, heads, head_dim] to the cache; with q, also normalise
     and rotate their queries into q_out (which may be q).  Returns q_out."""
-    import torch
-
+    index = cache.index
     shape = (batch.tokens, cache.heads, cache.head_dim)
-    hk, hv = _heads(k, "k", shape), _heads(v, "v", shape)
-    if rope.head_dim - {cache.head_dim}:
+    hk, hv = _heads(k, "k", shape, index), _heads(v, "v", shape, index)
+    if rope.head_dim is not None and rope.head_dim != cache.head_dim:
         raise ValueError(f"norm weights must have {cache.head_dim} elements")
     hq = hqo = None
-    devices = [batch.device, rope.device, k.device, v.device]
     if q is not None:
-        hq = _heads(q, "q", (batch.tokens, q.shape[1], cache.head_dim))
+        shape = (batch.tokens, _shape3(q, "q")[1], cache.head_dim)
+        hq = _heads(q, "q", shape, index)
         if q_out is None:
-            q_out = _new(q.device, stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
-        hqo = _heads(q_out, "q_out", tuple(q.shape))
-        devices += [q.device, q_out.device]
+            q_out = _like(q, stream)
+        hqo = _heads(q_out, "q_out", shape, index)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on(cache.device, devices, "sgr_kv_append")
-    _check(_call(cache.device, stream, lambda s: load().sgr_kv_append(
-        cache.ref, batch.ref, _addr(hq), _addr(hk), _addr(hv), _addr(hqo), rope.ref, flags, s)), "sgr_kv_append")
+    _on(index, (batch.index, rope.index), "sgr_kv_append")
+    _launch(index, stream, "sgr_kv_append", load().sgr_kv_append, cache.ref, batch.ref, hq, hk, hv, hqo, rope.ref, flags)
     return q_out
 
 
@@ -247,7 +283,7 @@ def kv_attention_workspace(cache: KvCache, batch: KvBatch, q_heads: int):
     import torch
 
     n = ctypes.c_int64(0)
-    _check(load().sgr_kv_attention_workspace(cache.device.index, cache.ref, batch.ref, q_heads, ctypes.byref(n)),
+    _check(load().sgr_kv_attention_workspace(cache.index, cache.ref, batch.ref, q_heads, ctypes.byref(n)),
            "sgr_kv_attention_workspace")
     return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
 
@@ -258,20 +294,17 @@ def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float |
     the cached positions up to their own (the last `window` of them where
     window > 0), scores times `scale` (1/sqrt(head_dim) by default).
     Returns out."""
-    import torch
-
-    tokens, heads, dim = batch.tokens, q.shape[1], cache.head_dim
-    hq = _heads(q, "q", (tokens, heads, dim))
+    index = cache.index
+    shape = (batch.tokens, _shape3(q, "q")[1], cache.head_dim)
+    hq = _heads(q, "q", shape, index)
     if out is None:
-        out = _new(q.device, stream, lambda: torch.empty(q.shape, dtype=q.dtype, device=q.device))
-    ho = _heads(out, "out", (tokens, heads, dim))
+        out = _like(q, stream)
+    ho = _heads(out, "out", shape, index)
     if workspace is None:
-        workspace = _new(q.device, stream, lambda: kv_attention_workspace(cache, batch, heads))
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _on(cache.device, (batch.device, q.device, out.device, workspace.device), "sgr_kv_attention")
-    scale = dim ** -0.5 if scale is None else scale
-    _check(_call(cache.device, stream, lambda s: load().sgr_kv_attention(
-        cache.ref, batch.ref, _addr(hq), _addr(ho), scale, window, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), flags, s)), "sgr_kv_attention")
+        workspace = _new(index, stream, lambda: kv_attention_workspace(cache, batch, shape[1]))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on(index, (batch.index, workspace.get_device()), "sgr_kv_attention")
+    _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention, cache.ref, batch.ref, hq, ho,
+            shape[2] ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.nbytes, flags)
     return out

@@ -130,6 +130,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load (building first if needed) the CUDA library; raise if impossible."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -390,11 +390,19 @@ AttnKernel attn_kernel(int dim, int nt) {
   return nt == 8 ? attn_kernel_of<128, 8>() : nt == 16 ? attn_kernel_of<128, 16>() : attn_kernel_of<128, 32>();
 }
 
+// Caches of at most this many tiles a sequence are not split over CTAs: the
+// second launch that joins costs more than the tiles' time in turn.
+#ifndef SGR_KV_WHOLE_TILES
+#define SGR_KV_WHOLE_TILES 4
+#endif
+constexpr int kWholeTiles = SGR_KV_WHOLE_TILES;
+
 struct AttnPlan {
   int nt;           // rows of a row tile
   int grid;
   bool split;       // whether a row tile may span CTAs
   bool reuse;       // whether a sequence may have several row tiles
+  bool fits;        // 31 bits hold the number of units
   int64_t bytes;    // workspace
 };
 
@@ -406,9 +414,10 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
   const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
-  const long long units = c.heads * row_tiles * (tiles > 1 ? tiles : 1);
+  a.split = tiles > kWholeTiles;
+  const long long units = c.heads * row_tiles * (a.split ? tiles : 1);
+  a.fits = units < (1LL << 31) && tiles < (1 << 24);
   a.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
-  a.split = tiles > 1;
   a.reuse = rows > a.nt;
   a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
   return a;
@@ -439,7 +448,7 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
   const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads);
-  if (workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
+  if (!a.fits || workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   // (a cache without pages: the maps are never used)
   if (!make_cache_tmap(&tk, c->num_pages ? c->k : workspace, *c) || !make_cache_tmap(&tv, c->num_pages ? c->v : workspace, *c))
@@ -452,7 +461,9 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window > 0 ? window : INT_MAX;
   p.group = q->heads / c->heads;
+  p.group_inv = p.group > 1 ? (unsigned)((1ULL << 32) / p.group) : 0xffffffffu;
   p.reuse = a.reuse ? 1 : 0;
+  p.whole = a.split ? 0 : 1;
   p.err = dev->err;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2LL * a.grid * a.nt * c->head_dim);

@@ -32,7 +32,8 @@
 // Work split: every CTA takes the same number of (row tile, 128-token tile)
 // units of all sequences and heads, in order, whatever the lengths; a row
 // tile that spans CTAs leaves partial sums (o, M, l) in the workspace and a
-// second kernel joins them in order (the same bits on every run).
+// second kernel joins them in order (the same bits on every run).  For short
+// caches (`whole`) a row tile is one unit and nothing is joined.
 //
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile.
@@ -80,7 +81,9 @@ struct AttnParams {
   float scale_log2;  // scale * log2(e)
   int window;        // INT_MAX: none
   int group;         // query heads a key/value head
+  unsigned group_inv;  // floor(2^32 / group), at most 2^32 - 1
   int reuse;         // row tiles of a sequence share the cache's bytes
+  int whole;         // a row tile is one unit
   unsigned* err;
   float* part_o;      // [2 grid][NT][D]
   float2* part_ml;    // [2 grid][NT]  maximum, sum
@@ -115,10 +118,6 @@ struct AttnCtl {
   int abort;
   int go[2][2];
   unsigned nan_tokens[4];
-  // where this CTA's share begins: sequence (-1: none), head, row tile, units of it to skip
-  int start_b, start_h, start_j, start_skip;
-  KvSeq start_seq;
-  long long scan[Sh::kThreads / 32];
   AttnSeg seg[kAttnQueue];
   float kscale[S][8], vexp[S][8];  // of a stage's pages
   int flags[S];                    // 1: some token is not live, 2: rows see different tokens
@@ -140,43 +139,38 @@ constexpr int attn_smem_bytes() {
   return 1024 + attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + S::kQBufs * S::kQBytes;
 }
 
-// Row tile j of a sequence: its rows, the positions they see, its units (a
-// row tile that sees nothing is one unit: its zeros).
+// Row tile j of a sequence: its rows, the positions they see, its tiles, its
+// units (a row tile that sees nothing is one unit: its zeros).
 struct AttnItem {
-  int r0, nrows, tlo, thi, ta, tb;
-  __device__ __forceinline__ int units() const { return tb > ta ? tb - ta : 1; }
+  int r0, nrows, tlo, thi, ta, tb, units;
 };
 
+// r / group for 0 <= r < 2^31: the product is at most one too small.
+__device__ __forceinline__ int div_group(const AttnParams& p, int r) {
+  const int q = (int)__umulhi((unsigned)r, p.group_inv);
+  return q + (r - q * p.group >= p.group ? 1 : 0);
+}
+
 template <int NT>
-__device__ __forceinline__ AttnItem attn_item(const KvSeq& s, int group, int window, int j) {
+__device__ __forceinline__ AttnItem attn_item(const AttnParams& p, const KvSeq& s, int j) {
   AttnItem it;
   it.r0 = j * NT;
-  it.nrows = min(NT, s.n * group - it.r0);
-  const int first = s.len - s.n, p0 = first + it.r0 / group;
-  it.thi = max(first + (it.r0 + it.nrows - 1) / group + 1, 0);
-  it.tlo = window > p0 ? 0 : p0 - window + 1;
+  it.nrows = min(NT, s.n * p.group - it.r0);
+  const int first = s.len - s.n, p0 = first + div_group(p, it.r0);
+  it.thi = max(first + div_group(p, max(it.r0 + it.nrows - 1, 0)) + 1, 0);
+  it.tlo = p.window > p0 ? 0 : p0 - p.window + 1;
   it.ta = it.thi > 0 ? it.tlo / kAttnTile : 0;
   it.tb = (it.thi + kAttnTile - 1) / kAttnTile;
+  it.units = p.whole ? 1 : max(it.tb - it.ta, 1);
   return it;
 }
 
 template <int NT>
-__device__ __forceinline__ long long attn_seq_units(const KvSeq& s, int group, int window) {
-  const int nt = (s.n * group + NT - 1) / NT;
-  long long u = 0;
-  for (int j = 0; j < nt; ++j) u += attn_item<NT>(s, group, window, j).units();
+__device__ __forceinline__ int attn_seq_units(const AttnParams& p, const KvSeq& s) {
+  int u = 0;
+  for (int j = 0; j * NT < s.n * p.group; ++j) u += attn_item<NT>(p, s, j).units;
   return u;
 }
-
-// Equal shares: CTA c of `active` takes units [share_begin(c), share_begin(c + 1)).
-struct AttnShare {
-  long long per, rest;  // the first `rest` CTAs take one more than `per`
-  __device__ __forceinline__ long long begin(long long c) const { return c * per + min(c, rest); }
-  __device__ __forceinline__ int cta_of(long long u) const {
-    const long long x = rest * (per + 1);
-    return (int)(u < x ? u / (per + 1) : rest + (u - x) / per);
-  }
-};
 
 // 2^d for whole d <= 0 (0 from -127 down), on the integer unit.
 __device__ __forceinline__ float exp2_whole(float d) {
@@ -297,7 +291,6 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       mbar_init(smem_u32(&c.segempty[i]), kSoftmax + 3);  // and the MMA and query warps
     }
     c.abort = 0;
-    c.start_b = -1;
     fence_mbar_init();
   }
   if (warp == kSoftmax + 1) {
@@ -316,84 +309,66 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
   pdl_launch_dependents();
   pdl_wait();
 
-  // ------------------------------------------------ this CTA's share of the work
-  // Each thread counts the units of its (consecutive) sequences; the one that
-  // holds the share's first unit says where it lies.
-  const int ps = p.cache.page_shift, hk = p.cache.heads;
-  const int per_thread = (p.batch.batch + Sh::kThreads - 1) / Sh::kThreads;
-  const int b_first = tid * per_thread, b_last = min(b_first + per_thread, p.batch.batch);
-  KvSeq own{0, 0, 0};
-  long long units = 0, mine = 0;
-  for (int b = b_first; b < b_last; ++b) {
-    own = kv_seq(p.batch, ps, b, p.err);
-    units = attn_seq_units<NT>(own, p.group, p.window);  // (of the last one: all there is to know with one a thread)
-    mine += units * hk;
-  }
-  long long upto = mine;
+  if (warp == kSoftmax) {
+    // ------------------------------------------------ this CTA's share of the work
+    // CTA c of `active` takes the units [begin(c), begin(c + 1)) of all
+    // sequences: the first `rest` CTAs one more than `per`.  (The host refuses
+    // what might not fit 31 bits.)
+    const int ps = p.cache.page_shift, hk = p.cache.heads;
+    int b = 0, h = 0, j = 0, skip = 0, u = 0, u1 = 0, per = 0, rest = 0;
+    KvSeq s{0, 0, 0};
+    {
+      // Each lane counts its (consecutive) sequences.
+      const int per_lane = (p.batch.batch + 31) / 32, b_first = lane * per_lane;
+      const int b_last = min(b_first + per_lane, p.batch.batch);
+      int mine = 0;
+#pragma unroll 4
+      for (int x = b_first; x < b_last; ++x) mine += attn_seq_units<NT>(p, kv_seq(p.batch, ps, x, p.err)) * hk;
+      int upto = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += up;
-  }
-  if (lane == 31) c.scan[warp] = upto;
-  __syncthreads();
-  long long total = 0, before = upto - mine;
-#pragma unroll
-  for (int w = 0; w < Sh::kThreads / 32; ++w) {
-    before += w < warp ? c.scan[w] : 0;
-    total += c.scan[w];
-  }
-  // (with fewer units than CTAs the last ones have none, the others one each)
-  const int active = (int)min(total, (long long)gridDim.x);
-  AttnShare share{0, 0};
-  if (active > 0) {
-    if (total >> 31)
-      share.per = total / active;
-    else
-      share.per = (unsigned)total / (unsigned)active;
-    share.rest = total - share.per * active;
-  }
-  const bool busy = (int)blockIdx.x < active;
-  const long long u0 = busy ? share.begin(blockIdx.x) : 0, u1 = busy ? share.begin(blockIdx.x + 1) : 0;
-  if (busy && u0 >= before && u0 < before + mine) {
-    int b = b_last - 1;
-    if (per_thread > 1) {
-      for (b = b_first;; ++b) {
-        own = kv_seq(p.batch, ps, b, nullptr);
-        units = attn_seq_units<NT>(own, p.group, p.window);
-        if (u0 < before + units * hk) break;
-        before += units * hk;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += up;
+      }
+      const int total = __shfl_sync(0xffffffffu, upto, 31);
+      // (with fewer units than CTAs the last ones have none, the others one each)
+      const int active = min(total, (int)gridDim.x), c0 = (int)blockIdx.x;
+      if (c0 < active) {
+        per = total / active;
+        rest = total - per * active;
+        u = c0 * per + min(c0, rest);
+        u1 = u + per + (c0 < rest ? 1 : 0);
+        const int before = upto - mine;
+        const int src = __ffs(__ballot_sync(0xffffffffu, u >= before && u < upto)) - 1;
+        int off = u - __shfl_sync(0xffffffffu, before, max(src, 0)), units = 0;
+        // (row offsets that run backwards may count more units than 31 bits hold)
+        bool found = src >= 0;
+        for (b = max(src, 0) * per_lane; found; ++b) {
+          if (b >= p.batch.batch) found = false;
+          if (!found) break;
+          s = kv_seq(p.batch, ps, b, nullptr);
+          units = attn_seq_units<NT>(p, s);
+          if (off < units * hk) break;
+          off -= units * hk;
+        }
+        if (!found) u1 = u, off = 0, units = 1;
+        h = off / units;
+        off -= h * units;
+        for (int x; found && off >= (x = attn_item<NT>(p, s, j).units); ++j) off -= x;
+        skip = off;
       }
     }
-    long long off = u0 - before;
-    int h = 0, j = 0;
-    for (; off >= units; off -= units) ++h;
-    AttnItem it = attn_item<NT>(own, p.group, p.window, 0);
-    while (off >= it.units()) {
-      off -= it.units();
-      it = attn_item<NT>(own, p.group, p.window, ++j);
-    }
-    c.start_b = b;
-    c.start_h = h;
-    c.start_j = j;
-    c.start_skip = (int)off;
-    c.start_seq = own;
-  }
-  __syncthreads();
-
-  if (warp == kSoftmax) {
+    auto cta_of = [&](int x) {  // the CTA that takes unit x
+      const int y = rest * (per + 1);
+      return x < y ? x / (per + 1) : rest + (x - y) / per;
+    };
     // ------------------------------------------------------- walk and TMA loads
     const uint64_t policy = p.reuse ? policy_evict_last() : policy_evict_first();
-    int b = c.start_b, h = c.start_h, j = c.start_j, skip = c.start_skip, sq = 0;
-    long long u = u0;  // next unit
-    KvSeq s = c.start_seq;
+    int sq = 0;
     AttnItem it{};
     bool ok = true;
     AttnPiece piece{};  // of the row tile that goes on in the next CTA
-    if (b >= 0)
-      it = attn_item<NT>(s, p.group, p.window, j);
-    else
-      u = u1;
+    if (u < u1) it = attn_item<NT>(p, s, j);
     int t = 0, t_end = 0;  // tiles of the segment handed out last
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok && !mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
@@ -433,18 +408,18 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
               s = kv_seq(p.batch, ps, b, nullptr);
             } while (s.n == 0);
           }
-          it = attn_item<NT>(s, p.group, p.window, 0);
+          it = attn_item<NT>(p, s, 0);
         }
-        const int units = it.units(), take = (int)min(u1 - u, (long long)(units - skip));
+        const int units = it.units, take = min(u1 - u, units - skip);
         u += take;
         if (it.tb <= it.ta) {  // rows that see nothing: zeros
           for (int e = lane; e < it.nrows * (D / 8); e += 32) {
-            const int r = it.r0 + e / (D / 8);
-            *reinterpret_cast<uint4*>(p.out.p + (long long)(s.row0 + r / p.group) * p.out.ts +
-                                      (long long)(h * p.group + r % p.group) * p.out.hs + e % (D / 8) * 8) =
+            const int r = it.r0 + e / (D / 8), tok = div_group(p, r);
+            *reinterpret_cast<uint4*>(p.out.p + (long long)(s.row0 + tok) * p.out.ts +
+                                      (long long)(h * p.group + r - tok * p.group) * p.out.hs + e % (D / 8) * 8) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
-          it = attn_item<NT>(s, p.group, p.window, ++j);
+          it = attn_item<NT>(p, s, ++j);
           continue;
         }
         AttnSeg g;
@@ -455,23 +430,23 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         g.nrows = it.nrows;
         g.first = s.len - s.n;
         g.ta = it.ta + skip;
-        g.tb = g.ta + take;
+        g.tb = p.whole ? it.tb : g.ta + take;
         g.tlo = it.tlo;
         g.thi = it.thi;
         g.slot = 2 * (int)blockIdx.x + (skip == 0 ? 1 : 0);
         g.pad = 0;
         hand_out(g);
         if (!ok) return false;
-        if (g.kind == kSegStart) piece = {share.cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
+        if (g.kind == kSegStart) piece = {cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
         t = g.ta;
         t_end = g.tb;
         cur = it;
         cur_h = h;
         cur_b = b;
-        cur_p0 = g.first + it.r0 / p.group;
+        cur_p0 = g.first + div_group(p, it.r0);
         cur_p1 = it.thi - 1;
         skip = 0;
-        if (g.kind & kSegEnd) it = attn_item<NT>(s, p.group, p.window, ++j);
+        if (g.kind & kSegEnd) it = attn_item<NT>(p, s, ++j);
       }
       const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
       ++t;
@@ -500,16 +475,16 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         x.vs = p.cache.v_scale[at];
       }
     };
-    // Two tiles ahead of the copies: table entries, then (dependent) scales,
-    // which reach the stage while its copies are under way.
-    Tile a{}, n1{}, n2{};
-    bool has_a = next_tile(a), has_1 = has_a && next_tile(n1);
-    if (has_a) load_scales(a);
+    // One tile ahead of the copies: its table entries are asked for before
+    // this tile's scales arrive, which reach the stage behind its copies.
+    Tile a{}, next{};
+    bool has = next_tile(a);
+    if (has) load_scales(a);
     int i = 0, slot = 0;
     uint32_t par = 0;
     const int per_tile = kAttnTile >> ps;
     const uint32_t page_bytes = (uint32_t)D << ps;
-    while (has_a && ok) {
+    while (has && ok) {
       if (i >= S) wait(&c.empty[slot], par ^ 1u);
       if (!ok) break;
       const unsigned live = __ballot_sync(0xffffffffu, a.page >= 0);
@@ -524,8 +499,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         tma_load_4d(dst + Sh::kTileBytes, &tmK, 0, 0, a.h, a.page, kb, policy);
         tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, vb, policy);
       }
-      const bool has_2 = has_1 && next_tile(n2);
-      if (has_1) load_scales(n1);
+      has = next_tile(next);
       if (lane < per_tile) {
         c.kscale[slot][lane] = a.ks;
         // (an exponent of -inf marks a page that is not there)
@@ -539,10 +513,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         slot = 0;
         par ^= 1u;
       }
-      a = n1;
-      n1 = n2;
-      has_a = has_1;
-      has_1 = has_2;
+      a = next;
+      if (has) load_scales(a);
     }
     AttnSeg stop{};
     stop.kind = kSegStop;
@@ -651,29 +623,35 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
       ++sq;
       if (g.kind & kSegStop) break;
-      uint4 v[kPass];
-      long long out_at[kPass];
-      int pos[kPass];
-#pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        const int q = i * kRows + qt / kLanes, r = g.r0 + q;
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        pos[i] = -1;  // a row that is none sees nothing
-        out_at[i] = 0;
+      // Row `pass` of this thread's: two are under way while one is converted.
+      auto load_row = [&](int pass, long long& out_at, int& pos) {
+        const int q = pass * kRows + qt / kLanes;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        pos = -1;  // a row that is none sees nothing
+        out_at = 0;
         if (q < g.nrows) {
-          const int tok = r / p.group, head = g.h * p.group + r - tok * p.group;
-          pos[i] = g.first + tok;
-          out_at[i] = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
-          v[i] = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
+          const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
+          pos = g.first + tok;
+          out_at = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
+          v = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         }
-      }
+        return v;
+      };
+      long long out0, out1 = 0;
+      int pos0, pos1 = -1;
+      uint4 v0 = load_row(0, out0, pos0), v1 = v0;
+      if (kPass > 1) v1 = load_row(1, out1, pos1);
       if (lane == 0) ok = mbar_wait_or_abort(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < kPass; ++i) {
-        const int q = i * kRows + qt / kLanes;
+        const int q = i * kRows + qt / kLanes, pos = pos0;
+        const long long out_at = out0;
+        const uint4 v = v0;
+        v0 = v1, out0 = out1, pos0 = pos1;
+        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1);
         uint32_t mag = 0;
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) mag = max(mag, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
 #pragma unroll
@@ -683,7 +661,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         k = min(max(k, -120), 126);
         const float sc = kv_exp2i(k);
         float x[8], h[8];
-        unpack8(v[i], x);
+        unpack8(v, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= sc;
         const uint2 hi = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
@@ -698,8 +676,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         if (l == 0) {
           // a row with an infinity or NaN gets NaN
           c.qf[buf][q] = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k) * p.scale_log2;
-          c.qpos[buf][q] = pos[i];
-          c.qout[buf][q] = out_at[i];
+          c.qpos[buf][q] = pos;
+          c.qout[buf][q] = out_at;
         }
       }
       fence_proxy_async_smem();
@@ -782,7 +760,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.sempty[sb]));
-        const int pi = tok >> ps, flags = c.flags[slot], pos = t * kAttnTile + tok;
+        const int pi = tok >> p.cache.page_shift, flags = c.flags[slot], pos = t * kAttnTile + tok;
         const float ks = c.kscale[slot][pi], ve = c.vexp[slot][pi];
         const bool live = !(flags & 1) || (pos >= g.tlo && pos < g.thi && ve > -INFINITY);
 #pragma unroll
@@ -988,9 +966,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnPa
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
-  const int r = own.r0 + q;
-  __nv_bfloat16* out = p.out.p + (long long)(own.row0 + r / p.group) * p.out.ts +
-                       (long long)(own.h * p.group + r % p.group) * p.out.hs + lane * kE;
+  const int r = own.r0 + q, tok = div_group(p, r);
+  __nv_bfloat16* out = p.out.p + (long long)(own.row0 + tok) * p.out.ts +
+                       (long long)(own.h * p.group + r - tok * p.group) * p.out.hs + lane * kE;
   if constexpr (kE == 4)
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
   else

@@ -158,9 +158,9 @@ def test_validate_kv_attention(kw, status):
 def test_binding_refuses_cpu_tensors_and_wrong_types():
     x = torch.zeros(2, 4, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
-        attention._heads(x, "q")
+        attention._heads(x, "q", (2, 4, 128), 0)
     with pytest.raises(TypeError):
-        attention._heads(x.float(), "q")
+        attention._heads(x.float(), "q", (2, 4, 128), 0)
     with pytest.raises(ValueError):
         sgr.KvCache(torch.zeros(1, 1, 16, 64, dtype=torch.uint8), torch.zeros(1, 1, 16, 64, dtype=torch.uint8), x, x)
     with pytest.raises(TypeError):
