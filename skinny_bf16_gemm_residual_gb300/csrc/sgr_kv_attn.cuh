@@ -20,14 +20,15 @@
 // and lo rows sit side by side in the operand (2 NT columns of the
 // accumulator) and are added in FP32.
 //
-// Softmax: the maximum m of a tile's column is rounded up to a whole number,
-// so every rescaling is by a power of two: exact, without the exponential
-// unit, and P uses E4M3's whole range in every tile however far the running
-// maximum lies above it.  The product of a tile is read back and accumulated
-// in registers (thread d holds o[.][d]), O = O 2^(M-M') + O_tile 2^(m-M'), so
-// no accumulator in tensor memory is ever rescaled.  A page's key scale
-// multiplies the score; its value scale 2^e is added to the exponent of P and
-// taken out of the sum of weights again.
+// Softmax: weights are 2^(s' - R) with a whole number R for each column that
+// only moves, up, when a score exceeds it (one vote of the four warps a tile;
+// then the tile's maxima are found), so what came before is rescaled seldom
+// and by a power of two: exactly.  The product of a tile is read back and
+// accumulated in registers (thread d holds o[.][d]); no accumulator in tensor
+// memory is ever rescaled.  Weights are 256 p in hi and lo: 8 bits down to
+// p = 2^-14, 4 bits to 2^-19, nothing below 2^-23 of the largest so far.  A
+// page's key scale multiplies the score; its value scale 2^e is added to the
+// exponent of P and taken out of the sum of weights again.
 //
 // Work split: every CTA takes the same number of (row tile, 128-token tile)
 // units of all sequences and heads, in order, whatever the lengths; a row
@@ -52,7 +53,14 @@
 namespace sgr {
 
 constexpr int kAttnTile = 128;  // tokens
+#ifndef NAP_W
+#define NAP_W 64
+#define NAP_Q 64
+#define NAP_M 20
+#define NAP_S 0
+#endif
 constexpr int kAttnQueue = 8;   // segments handed out ahead
+constexpr int kNapWalk = NAP_W, kNapQuery = NAP_Q, kNapMma = NAP_M, kNapSoftmax = NAP_S;
 
 // A run of tiles [ta, tb) of one row tile, the unit that the roles work by.
 enum : int { kSegStart = 1, kSegEnd = 2, kSegStop = 4 };
@@ -124,8 +132,8 @@ struct AttnCtl {
   long long qout[Q][NT];           // a row's place in the output
   alignas(16) float qf[Q][NT];     // its score factor
   int qpos[Q][NT];                 // the last position that it sees
-  alignas(16) float wmax[2][Sh::kSoftmax][C], wsum[Sh::kSoftmax][C];
-  alignas(16) float m[Sh::kSoftmax][C], alpha[Sh::kSoftmax][2][C], beta[Sh::kSoftmax][2][C];  // a warp's own copies
+  alignas(16) float wmax[Sh::kSoftmax][C], wsum[Sh::kSoftmax][C];
+  alignas(16) float ref[Sh::kSoftmax][C], alpha[Sh::kSoftmax][2][C];  // a warp's own copies
 };
 
 template <int D, int NT>
@@ -371,7 +379,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
     if (u < u1) it = attn_item<NT>(p, s, j);
     int t = 0, t_end = 0;  // tiles of the segment handed out last
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
+      if (ok && !mbar_wait_nap<kNapWalk>(smem_u32(bar), parity, abort_flag)) {
         if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
         *abort_flag = 1;
         ok = false;
@@ -595,6 +603,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         }
         // Nothing to issue: bounded, as every wait.
         if (idle == 0) since = globaltimer_ns();
+        if (kNapMma) __nanosleep(kNapMma);
         if ((++idle & 63u) == 0) {
           if (*abort_flag) ok = false;
           if (globaltimer_ns() - since > SGR_WAIT_LIMIT_NS) {
@@ -616,7 +625,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
     while (true) {
       const int qi = sq % kAttnQueue;
       bool ok = true;
-      if (lane == 0) ok = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
+      if (lane == 0) ok = mbar_wait_nap<kNapQuery>(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       const AttnSeg g = c.seg[qi];
       __syncwarp();
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       int pos0, pos1 = -1;
       uint4 v0 = load_row(0, out0, pos0), v1 = v0;
       if (kPass > 1) v1 = load_row(1, out1, pos1);
-      if (lane == 0) ok = mbar_wait_or_abort(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
+      if (lane == 0) ok = mbar_wait_nap<kNapQuery>(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll 1
       for (int i = 0; i < kPass; ++i) {
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
     // After a wait that ran out (abort) the waits fall through, so that the
     // warps keep meeting at their barriers until the segments end.
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
+      if (!mbar_wait_nap<kNapSoftmax>(smem_u32(bar), parity, abort_flag)) {
         if (!*abort_flag) report_error(p.err, kErrWaitMma);
         *abort_flag = 1;
       }
@@ -707,13 +716,30 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       else
         asm volatile("bar.sync 2, 128;" ::: "memory");
     };
+    auto any_of_group = [&](bool x) {  // of its 128 threads
+      uint32_t any;
+      __syncwarp();
+      if (Sh::kGroups == 1 || group == 0)
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(any)
+            : "r"((uint32_t)x)
+            : "memory");
+      else
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(any)
+            : "r"((uint32_t)x)
+            : "memory");
+      return any != 0;
+    };
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)q0;  // tensor-memory lanes of this warp
     float o[C], l[C];
-    float run = 0.f;  // running maximum of column q0 + lane
+    float run = 0.f;  // R of column q0 + lane
     unsigned nan_rows = 0;
     int i = 0, slot = 0, sq = 0, buf = 0;
     uint32_t par = 0, qpar = 0;
-    bool scaled_before = false;  // whether the tile before needs its factors
+    bool scaled_before = false;  // whether R moved with the tile before
     // O of tile k, read back and accumulated.
     auto accumulate = [&](int k, bool scaled) {
       wait(&c.ofull[k & 1], (k >> 1) & 1);
@@ -725,11 +751,10 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       if (lane == 0) mbar_arrive(smem_u32(&c.oempty[k & 1]));
       if (scaled) {
 #pragma unroll
-        for (int q = 0; q < C; ++q) o[q] = fmaf(x[q], c.beta[warp][k & 1][q], o[q] * c.alpha[warp][k & 1][q]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < C; ++q) o[q] += x[q];
+        for (int q = 0; q < C; ++q) o[q] *= c.alpha[warp][k & 1][q];
       }
+#pragma unroll
+      for (int q = 0; q < C; ++q) o[q] += x[q];
     };
     while (true) {
       const int qi = sq % kAttnQueue;
@@ -749,7 +774,9 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
 #pragma unroll
       for (int q = 0; q < C; ++q) o[q] = l[q] = 0.f;
       run = -3.0e38f;
+      if (lane < C) c.ref[warp][lane] = run;
       nan_rows = 0;
+      __syncwarp();
       for (int t = g.ta; t < g.tb; ++t) {
         const int sb = i & 1;
         wait(&c.sfull[sb], (i >> 1) & 1);
@@ -764,8 +791,8 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
         const float ks = c.kscale[slot][pi], ve = c.vexp[slot][pi];
         const bool live = !(flags & 1) || (pos >= g.tlo && pos < g.thi && ve > -INFINITY);
 #pragma unroll
-        for (int q = 0; q < C; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q0 + q], ve);
-        if (flags & 2) {
+        for (int q = 0; q < C; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q0 + q], ve + 8.f);  // weights come as 256 p
+        if (__builtin_expect(flags & 2, 0)) {
 #pragma unroll
           for (int q = 0; q < C; ++q) {
             const int last = c.qpos[buf][q0 + q];
@@ -775,44 +802,41 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
 #pragma unroll
           for (int q = 0; q < C; ++q) x[q] = -INFINITY;
         }
-        // The tile's maximum of each column, rounded up; lane q keeps column
-        // q's.  Weights are taken relative to the running maximum where the
-        // tile's lies at most 2^4 below it (then nothing is rescaled), else to
-        // the tile's own.
         float top = -INFINITY;
 #pragma unroll
-        for (int q = 0; q < C; ++q) {
-          const float w = warp_max(x[q]);
-          if (lane == q) top = w;
+        for (int q = 0; q < C; ++q) top = fmaxf(top, x[q] - c.ref[warp][q]);
+        const bool scaled = any_of_group(top > 8.8f);  // E4M3 ends at 448 = 2^8.8
+        if (__builtin_expect(scaled, 0)) {
+          // R of the columns that are exceeded moves one above the tile's
+          // maximum (room for the next tiles); lane q keeps column q's.
+          top = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < C; ++q) {
+            const float w = warp_max(x[q]);
+            if (lane == q) top = w;
+          }
+          if (lane < C) c.wmax[warp][lane] = top;
+          meet();
+          if (lane < C) {
+            const int w0 = warp & ~3;
+            top = fmaxf(fmaxf(c.wmax[w0][lane], c.wmax[w0 + 1][lane]), fmaxf(c.wmax[w0 + 2][lane], c.wmax[w0 + 3][lane]));
+            const float now = top - run > 8.8f ? ceilf(top) - 7.f : run;
+            c.alpha[warp][sb][lane] = exp2_whole(run - now);
+            c.ref[warp][lane] = run = now;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < C; ++q) l[q] *= c.alpha[warp][sb][q];
         }
-        if (lane < C) c.wmax[sb][warp][lane] = top;
-        meet();
-        bool scaled = false;
-        if (lane < C) {
-          const int w0 = warp & ~3;
-          top = fmaxf(fmaxf(c.wmax[sb][w0][lane], c.wmax[sb][w0 + 1][lane]), fmaxf(c.wmax[sb][w0 + 2][lane], c.wmax[sb][w0 + 3][lane]));
-          const float m = fmaxf(ceilf(top), -3.0e38f), now = fmaxf(run, m), ref = now - m <= 4.f ? now : m;
-          const float al = exp2_whole(run - now), be = exp2_whole(ref - now);
-          c.m[warp][lane] = ref - 8.f;  // weights come as 256 p
-          c.alpha[warp][sb][lane] = al;
-          c.beta[warp][sb][lane] = be;
-          scaled = al != 1.f || be != 1.f;
-          run = now;
-        }
-        scaled = __any_sync(0xffffffffu, scaled);
         const float iv = live ? kv_exp2i(-(int)ve) : 0.f;  // the value scale does not count in the sum of weights
 #pragma unroll
-        for (int q = 0; q < C; ++q) x[q] = ex2(x[q] - c.m[warp][q]);
-        if (scaled) {
-#pragma unroll
-          for (int q = 0; q < C; ++q) l[q] = fmaf(x[q] * iv, c.beta[warp][sb][q], l[q] * c.alpha[warp][sb][q]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < C; ++q) l[q] = fmaf(x[q], iv, l[q]);
+        for (int q = 0; q < C; ++q) {
+          x[q] = ex2(x[q] - c.ref[warp][q]);
+          l[q] = fmaf(x[q], iv, l[q]);
         }
         const bool joined = t > g.ta;
         if (joined) wait(&c.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);  // the weights before are read
-        if (flags) {
+        if (__builtin_expect(flags, 0)) {
           wait(&c.vfull[slot], par);
           const uint32_t vt = ring + (uint32_t)slot * Sh::kStageBytes;
           // Values of tokens that no row sees must not reach the product
@@ -888,7 +912,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
       if (lane < C) {
         const int w0 = warp & ~3;
         const float sum = c.wsum[w0][lane] + c.wsum[w0 + 1][lane] + c.wsum[w0 + 2][lane] + c.wsum[w0 + 3][lane];
-        c.m[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;
+        c.ref[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;  // (R is not needed any more)
         if (!whole && (warp & 3) == 0 && q0 + lane < g.nrows)
           p.part_ml[(long long)g.slot * NT + q0 + lane] = make_float2(run, sum);
       }
@@ -899,7 +923,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
           const float v = nan_rows >> q & 1 ? __int_as_float(0x7fffffff) : o[q];
           if (q0 + q < g.nrows) {
             if (whole)
-              p.out.p[c.qout[buf][q0 + q] + tok] = __float2bfloat16(v * c.m[warp][q]);
+              p.out.p[c.qout[buf][q0 + q] + tok] = __float2bfloat16(v * c.ref[warp][q]);
             else
               p.part_o[((long long)g.slot * NT + q0 + q) * D + tok] = v;
           }

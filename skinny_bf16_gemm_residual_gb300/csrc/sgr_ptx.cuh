@@ -154,6 +154,24 @@ __device__ __forceinline__ bool mbar_wait_sleepy_or_abort(uint32_t bar, uint32_t
   }
 }
 
+// The same with a nap of about kNs nanoseconds between polls, for roles that
+// wait most of the time next to warps that compute (a poll is an instruction
+// slot of theirs).
+template <int kNs>
+__device__ __forceinline__ bool mbar_wait_nap(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      if (kNs > 0) __nanosleep(kNs);
+      if (mbar_test_wait(bar, parity)) return true;
+    }
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > SGR_WAIT_LIMIT_NS) return false;
+  }
+}
+
 // ------------------------------------------------------------ cache policies
 __device__ __forceinline__ uint64_t policy_evict_first() {
   uint64_t p;
