@@ -295,14 +295,12 @@ int launch(Fn fn, dim3 grid, int threads, size_t smem, unsigned flags, void* str
   return SGR_OK;
 }
 
-// Heads that one block of 4 warps takes of a row: one pass of its warps while
-// that does not fill the GPU (few rows: latency), up to four passes beyond
-// (the row's cosines, sines and weights are then read once for more heads).
-int rope_heads_per_block(int sms, long long rows, int heads, int dim, int threads) {
-  const int pass = threads / 32 * (32 / (dim / 8));
-  int passes = 1;
-  while (passes < 4 && rows * ((heads + pass * passes - 1) / (pass * passes)) > 16LL * sms) passes *= 2;
-  return pass * passes;
+// Passes over a row's heads of one block: one while that does not fill the
+// GPU (few rows: latency), four beyond (the reads of four heads a thread are
+// then under way at once, and the row's cosines, sines and weights are read
+// once for them).
+int rope_passes(int sms, long long rows, int heads, int per_pass) {
+  return rows * ((heads + per_pass - 1) / per_pass) > 16LL * sms && heads > per_pass ? 4 : 1;
 }
 
 int run_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* qo, const sgr_heads* ko, const int* positions,
@@ -319,26 +317,32 @@ int run_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* qo, const 
   p.positions = positions;
   p.nr = norm_rope_of(*nr);
   p.err = dev->err;
-  const int heads = p.q.heads + p.k.heads;
-  p.heads_per_block = rope_heads_per_block(dev->sms, tokens, heads, dim, sgr::kRopeThreads);
-  const dim3 grid(tokens, (heads + p.heads_per_block - 1) / p.heads_per_block);
-  return launch(dim == 64 ? sgr::qk_norm_rope_kernel<64> : sgr::qk_norm_rope_kernel<128>, grid, sgr::kRopeThreads, 0,
-                flags, stream, p);
+  const int per_pass = sgr::kRopeThreads / (dim / 8), passes = rope_passes(dev->sms, tokens, p.q.heads + p.k.heads, per_pass);
+  p.heads_per_block = per_pass * passes;
+  p.q_chunks = (p.q.heads + p.heads_per_block - 1) / p.heads_per_block;
+  const dim3 grid(tokens, p.q_chunks + (p.k.heads + p.heads_per_block - 1) / p.heads_per_block);
+  void (*fn)(const sgr::RopeParams) =
+      dim == 64 ? (passes == 4 ? sgr::qk_norm_rope_kernel<64, 4> : sgr::qk_norm_rope_kernel<64, 1>)
+                : (passes == 4 ? sgr::qk_norm_rope_kernel<128, 4> : sgr::qk_norm_rope_kernel<128, 1>);
+  return launch(fn, grid, sgr::kRopeThreads, 0, flags, stream, p);
 }
 
 using AppendFn = void (*)(const sgr::AppendParams);
 
+template <int D, int kQPass>
+AppendFn append_fn_pass(int pass) {
+  if (pass == 1) return sgr::kv_append_kernel<D, 1, kQPass>;
+  if (pass == 2) return sgr::kv_append_kernel<D, 2, kQPass>;
+  if (pass == 4 || D == 64) return sgr::kv_append_kernel<D, 4, kQPass>;
+  return sgr::kv_append_kernel<D, D == 64 ? 4 : 8, kQPass>;
+}
+
 // The kernel whose threads hold a whole page of new tokens, or `most` of them.
-AppendFn append_fn(int dim, int page_size, int most) {
-  const int tok = sgr::kAppendThreads / (dim / 8);
-  const int n = most < page_size ? most : page_size;
+AppendFn append_fn(int dim, int page_size, int most, int q_passes) {
+  const int tok = sgr::kAppendThreads / (dim / 8), n = most < page_size ? most : page_size;
   const int pass = n <= tok ? 1 : n <= 2 * tok ? 2 : n <= 4 * tok ? 4 : 8;
-  if (dim == 64)
-    return pass == 1 ? sgr::kv_append_kernel<64, 1> : pass == 2 ? sgr::kv_append_kernel<64, 2> : sgr::kv_append_kernel<64, 4>;
-  return pass == 1   ? sgr::kv_append_kernel<128, 1>
-         : pass == 2 ? sgr::kv_append_kernel<128, 2>
-         : pass == 4 ? sgr::kv_append_kernel<128, 4>
-                     : sgr::kv_append_kernel<128, 8>;
+  if (dim == 64) return q_passes == 4 ? append_fn_pass<64, 4>(pass) : append_fn_pass<64, 1>(pass);
+  return q_passes == 4 ? append_fn_pass<128, 4>(pass) : append_fn_pass<128, 1>(pass);
 }
 
 int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* k,
@@ -360,12 +364,14 @@ int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q,
   // most (n - 1) / page_size + 2 of them.
   long long slots = (long long)b->tokens / c->page_size + 2LL * b->batch;
   if (slots > b->tokens) slots = b->tokens;
-  p.heads_per_block = q ? rope_heads_per_block(dev->sms, b->tokens, q->heads, c->head_dim, sgr::kAppendThreads) : 1;
+  const int per_pass = sgr::kAppendThreads / (c->head_dim / 8);
+  const int q_passes = q ? rope_passes(dev->sms, b->tokens, q->heads, per_pass) : 1;
+  p.heads_per_block = per_pass * q_passes;
   p.q_chunks = q ? (q->heads + p.heads_per_block - 1) / p.heads_per_block : 0;
   const long long q_blocks = (long long)b->tokens * p.q_chunks, blocks = q_blocks + slots * c->heads * 2;
   if (blocks > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
   p.q_blocks = (int)q_blocks;
-  return launch(append_fn(c->head_dim, c->page_size, b->tokens), dim3((unsigned)blocks), sgr::kAppendThreads, 0,
+  return launch(append_fn(c->head_dim, c->page_size, b->tokens, q_passes), dim3((unsigned)blocks), sgr::kAppendThreads, 0,
                 flags, stream, p);
 }
 

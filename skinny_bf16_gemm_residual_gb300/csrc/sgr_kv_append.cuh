@@ -53,52 +53,58 @@ struct RopeParams {
   const int* positions;
   NormRope nr;
   unsigned* err;
-  int heads_per_block;
+  int heads_per_block, q_chunks;  // of a block, and blocks of a row's query heads
 };
 
-// Heads [h0, h1) of one row (query heads first, then key heads), D / 8 lanes
-// a head.  The lanes keep their 8 elements' cosines, sines and weights in
-// registers over the row's heads.
-template <int D>
-__device__ __forceinline__ void rope_row(const KvHeads& q, const KvHeads& k, const KvHeads& qo, const KvHeads& ko,
-                                         const NormRope& nr, int row, int pos, int h0, int h1, unsigned* err) {
-  constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % kLanes;
-  RopeLane<D> rl;
-  float wq[8], wk[8];
-  rl.load(nr, max(pos, 0), lane, err);
-  load_weight(nr.q_weight, l, wq);
-  load_weight(nr.k_weight, l, wk);
-  for (int hb = h0 + warp * kPerWarp; hb < h1; hb += (int)(blockDim.x >> 5) * kPerWarp) {
-    const int h = hb + lane / kLanes;
-    const bool live = h < h1, is_k = h >= q.heads;
-    const KvHeads& src = is_k ? k : q;
-    const KvHeads& dst = is_k ? ko : qo;
-    const int hh = is_k ? h - q.heads : h;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (live) v = *reinterpret_cast<const uint4*>(src.p + (long long)row * src.ts + (long long)hh * src.hs + 8 * l);
-    float x[8];
-    unpack8(v, x);
-    if (nr.q_weight || nr.k_weight) {
-      float w[8];
+// kPass passes of the block's warps over heads h0, h0 + 1, ... of one row of
+// src, D / 8 lanes a head.  All passes' reads are asked for first; the lanes
+// keep their pairs' cosines and sines and their weights over the heads.
+template <int D, int kPass>
+__device__ __forceinline__ void rope_row(const KvHeads& src, const KvHeads& dst, const __nv_bfloat16* weight,
+                                         const NormRope& nr, int row, int pos, int h0, unsigned* err) {
+  constexpr int kPerWarp = 32 / (D / 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, step = (int)(blockDim.x >> 5) * kPerWarp;
+  const HeadLane<D> hl(lane, nr.rot, nr.interleaved != 0);
+  const int first = h0 + warp * kPerWarp + lane / (D / 8);
+  const __nv_bfloat16* in = src.p + (long long)row * src.ts + (long long)first * src.hs;
+  uint4 v[kPass];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = is_k ? wk[j] : wq[j];
-      head_norm<D>(x, w, (is_k ? nr.k_weight : nr.q_weight) != nullptr, nr.eps);
-    }
-    rl.rotate(x, nr.interleaved != 0);
-    if (live)
-      *reinterpret_cast<uint4*>(dst.p + (long long)row * dst.ts + (long long)hh * dst.hs + 8 * l) =
-          pos >= 0 ? pack8(x) : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < kPass; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (first + i * step < src.heads) v[i] = hl.read(in);
+    in += step * src.hs;
+  }
+  float4 c, s;
+  hl.angles(nr, max(pos, 0), c, s, err);
+  float w[8];
+  load_weight<D>(weight, hl, w);
+  __nv_bfloat16* out = dst.p + (long long)row * dst.ts + (long long)first * dst.hs;
+  if (pos < 0) {  // a padding row: zeros
+    const float zero[8] = {};
+    for (int h = first; h < min(src.heads, first + kPass * step); h += step, out += step * dst.hs) hl.write(out, zero);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    float x[8];
+    unpack8(v[i], x);
+    if (weight) head_norm<D>(x, w, nr.eps);
+    hl.rotate(x, c, s);
+    if (first + i * step < src.heads) hl.write(out, x);
+    out += step * dst.hs;
   }
 }
 
-template <int D>
+// Blocks y < q_chunks take query heads, the others key heads.
+template <int D, int kPass>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeParams p) {
   pdl_launch_dependents();
   pdl_wait();
-  const int row = blockIdx.x, heads = p.q.heads + p.k.heads;
-  const int h0 = (int)blockIdx.y * p.heads_per_block;
-  rope_row<D>(p.q, p.k, p.qo, p.ko, p.nr, row, p.positions[row], h0, min(h0 + p.heads_per_block, heads), p.err);
+  const int row = blockIdx.x, y = blockIdx.y, pos = p.positions[row];
+  if (y < p.q_chunks)
+    rope_row<D, kPass>(p.q, p.qo, p.nr.q_weight, p.nr, row, pos, y * p.heads_per_block, p.err);
+  else
+    rope_row<D, kPass>(p.k, p.ko, p.nr.k_weight, p.nr, row, pos, (y - p.q_chunks) * p.heads_per_block, p.err);
 }
 
 // ---------------------------------------------------------------------- append
@@ -115,16 +121,18 @@ struct AppendParams {
   int heads_per_block;  // query heads of such a block
 };
 
-// The sequence of row `row` (rows 0 .. tokens-1), found by all threads of the
-// block: one pass over the row offsets, each thread its share.
-__device__ __forceinline__ int find_row(const KvBatch& bt, int row, int* found) {
+// The sequence of row `row` (-1: none), found by each warp in one pass over
+// the row offsets.
+__device__ __forceinline__ int find_row(const KvBatch& bt, int row) {
   if (!bt.q_start) return row;
-  if (threadIdx.x == 0) *found = -1;
-  __syncthreads();
-  for (int b = threadIdx.x; b < bt.batch; b += blockDim.x)
-    if (bt.q_start[b] <= row && row < bt.q_start[b + 1]) *found = b;
-  __syncthreads();
-  return *found;
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < bt.batch; b0 += 32) {
+    const int b = b0 + lane;
+    const bool here = b < bt.batch && bt.q_start[b] <= row && row < bt.q_start[b + 1];
+    const unsigned any = __ballot_sync(0xffffffffu, here);
+    if (any) return b0 + __ffs(any) - 1;
+  }
+  return -1;
 }
 
 // The page that the call's slot-th page write goes to: sequence and block of
@@ -174,19 +182,19 @@ __device__ __forceinline__ bool find_page(const KvBatch& bt, int page_shift, int
   return found[0] >= 0;
 }
 
-// kPass: 256-thread passes over a page's new tokens (8 elements a thread).
-template <int D, int kPass>
+// kPass: 256-thread passes over a page's new tokens (8 elements a thread);
+// kQPass: passes of the query blocks over a row's heads.
+template <int D, int kPass, int kQPass>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
   __shared__ int scratch[kAppendThreads / 32 + 2];
   pdl_launch_dependents();
   pdl_wait();
   if ((int)blockIdx.x < p.q_blocks) {
     const int row = (int)blockIdx.x / p.q_chunks, h0 = ((int)blockIdx.x % p.q_chunks) * p.heads_per_block;
-    const int b = find_row(p.batch, row, scratch);
+    const int b = find_row(p.batch, row);
     if (b < 0) return;  // a row of no sequence
     const KvSeq s = kv_seq(p.batch, p.cache.page_shift, b, p.err);
-    rope_row<D>(p.q, p.q, p.qo, p.qo, p.nr, row, s.len - s.n + row - s.row0, h0, min(h0 + p.heads_per_block, p.q.heads),
-                p.err);
+    rope_row<D, kQPass>(p.q, p.qo, p.nr.q_weight, p.nr, row, s.len - s.n + row - s.row0, h0, p.err);
     return;
   }
   // ------------------------------------------------- one page's K or V of a head
@@ -209,25 +217,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
   const int e_old = joined ? (int)((__float_as_uint(*scale) >> 23) & 0xFF) - 127 : kKvExpMin;
 
   constexpr int kLanes = D / 8, kTok = kAppendThreads / kLanes;  // tokens a pass
-  const int lane = threadIdx.x & 31, l = threadIdx.x % kLanes, tok = threadIdx.x / kLanes;
+  const int lane = threadIdx.x & 31, tok = threadIdx.x / kLanes;
   const KvHeads& src = is_v ? p.v : p.k;
   const bool norm = !is_v && p.nr.k_weight;
-  float w[8], x[kPass][8];
-  load_weight(norm ? p.nr.k_weight : nullptr, l, w);
-  float amax = 0.f;
+  const HeadLane<D> hl(lane, is_v ? 0 : p.nr.rot, p.nr.interleaved != 0);
+  uint4 v[kPass];
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     const int t = t0 + i * kTok + tok;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < t1) v[i] = hl.read(src.p + (long long)(s.row0 + t - first) * src.ts + (long long)h * src.hs);
+  }
+  float w[8], x[kPass][8];
+  load_weight<D>(norm ? p.nr.k_weight : nullptr, hl, w);
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
     if (t0 + i * kTok >= t1) break;  // no token of this pass in the block
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (t < t1)
-      v = *reinterpret_cast<const uint4*>(src.p + (long long)(s.row0 + t - first) * src.ts + (long long)h * src.hs + 8 * l);
-    unpack8(v, x[i]);
+    unpack8(v[i], x[i]);
     if (!is_v) {
-      if (norm) head_norm<D>(x[i], w, true, p.nr.eps);
-      RopeLane<D> rl;
-      rl.load(p.nr, min(t, t1 - 1), lane, p.err);
-      rl.rotate(x[i], p.nr.interleaved != 0);
+      float4 cs, sn;
+      hl.angles(p.nr, min(t0 + i * kTok + tok, t1 - 1), cs, sn, p.err);
+      if (norm) head_norm<D>(x[i], w, p.nr.eps);
+      hl.rotate(x[i], cs, sn);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -262,10 +274,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     const int t = t0 + i * kTok + tok;
-    if (t < t1)
-      *reinterpret_cast<uint2*>(codes + (long long)(t - page0) * p.cache.token_stride + 8 * l) =
-          make_uint2(to_e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv),
-                     to_e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv));
+    if (t < t1) {
+      uint8_t* c = codes + (long long)(t - page0) * p.cache.token_stride;
+      *reinterpret_cast<uint32_t*>(c + hl.o0) = to_e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+      *reinterpret_cast<uint32_t*>(c + hl.o1) = to_e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+    }
   }
   if (threadIdx.x == 0) *scale = kv_exp2i(e);
 }

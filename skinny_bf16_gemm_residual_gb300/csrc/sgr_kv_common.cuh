@@ -93,95 +93,84 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-}
-
-// A head of D elements is held by D / 8 neighbouring lanes, 8 consecutive
-// elements each.  Element j of a lane becomes x_j c_j + partner_j s_j, its
-// partner being the other of its pair: x_{j^1} of the same lane
-// (interleaved), or element j of the lane rot/16 lanes up or down.  Lanes of
-// elements past rot keep theirs (an infinity times a zero sine is not zero).
+// A head of D elements is held by D / 8 neighbouring lanes, each with two runs
+// of four elements, at o0 and o1, chosen so that a lane holds both elements
+// of its four pairs: the same place of the two halves of the rotated part, or
+// eight consecutive elements (interleaved pairs, elements past rot, no
+// rotation).
 template <int D>
-struct RopeLane {
-  float c[8], s[8];
-  int partner;  // lane of the warp that holds the other halves (not interleaved)
-  bool turns;   // whether this lane's elements are rotated
+struct HeadLane {
+  int o0, o1;
+  bool turns, split;  // whether the lane's elements are rotated, and as (run, run) pairs
 
-  __device__ __forceinline__ void load(const NormRope& nr, int pos, int lane, unsigned* err) {
-    const int l = lane % (D / 8), half = nr.rot / 2;
-    partner = lane;
-    turns = 8 * l < nr.rot;  // rot = 0: no rotation
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = s[j] = 0.f;
+  __device__ __forceinline__ HeadLane(int lane, int rot, bool interleaved) {
+    const int l = lane % (D / 8);
+    turns = 8 * l < rot;
+    split = turns && !interleaved;
+    o0 = split ? 4 * l : 8 * l;
+    o1 = split ? rot / 2 + 4 * l : 8 * l + 4;
+  }
+
+  __device__ __forceinline__ uint4 read(const __nv_bfloat16* head) const {
+    const uint2 a = *reinterpret_cast<const uint2*>(head + o0), b = *reinterpret_cast<const uint2*>(head + o1);
+    return make_uint4(a.x, a.y, b.x, b.y);
+  }
+
+  __device__ __forceinline__ void write(__nv_bfloat16* head, const float (&x)[8]) const {
+    *reinterpret_cast<uint2*>(head + o0) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    *reinterpret_cast<uint2*>(head + o1) = make_uint2(pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+  }
+
+  // Cosines and sines of the lane's four pairs at a position.
+  __device__ __forceinline__ void angles(const NormRope& nr, int pos, float4& c, float4& s, unsigned* err) const {
+    c = s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (!turns) return;
     if (pos >= nr.table_rows) {
       report_error(err, kErrIndex);
       pos = nr.table_rows - 1;
     }
-    const float* row = nr.table + (long long)pos * nr.rot;
-    if (nr.interleaved) {
-      const float4 cv = *reinterpret_cast<const float4*>(row + 4 * l);
-      const float4 sv = *reinterpret_cast<const float4*>(row + half + 4 * l);
-      const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
+    const float* row = nr.table + (long long)pos * nr.rot + (split ? o0 : o0 / 2);
+    c = *reinterpret_cast<const float4*>(row);
+    s = *reinterpret_cast<const float4*>(row + nr.rot / 2);
+  }
+
+  __device__ __forceinline__ void rotate(float (&x)[8], const float4& c, const float4& s) const {
+    if (!turns) return;  // (and an infinity times a zero sine is not zero)
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    if (split) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c[2 * j] = c[2 * j + 1] = cc[j];
-        s[2 * j] = -ss[j];
-        s[2 * j + 1] = ss[j];
-      }
+      for (int j = 0; j < 4; ++j) turn(x[j], x[4 + j], cc[j], ss[j]);
     } else {
-      const bool second = 8 * l >= half;
-      const int i = second ? 8 * l - half : 8 * l;
-      partner = second ? lane - half / 8 : lane + half / 8;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 cv = *reinterpret_cast<const float4*>(row + i + 4 * q);
-        const float4 sv = *reinterpret_cast<const float4*>(row + half + i + 4 * q);
-        c[4 * q] = cv.x, c[4 * q + 1] = cv.y, c[4 * q + 2] = cv.z, c[4 * q + 3] = cv.w;
-        s[4 * q] = sv.x, s[4 * q + 1] = sv.y, s[4 * q + 2] = sv.z, s[4 * q + 3] = sv.w;
-      }
-      if (!second) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = -s[j];
-      }
+      for (int j = 0; j < 4; ++j) turn(x[2 * j], x[2 * j + 1], cc[j], ss[j]);
     }
   }
 
-  // Rotation of the heads that the warp's lane groups hold (all lanes take part).
-  __device__ __forceinline__ void rotate(float (&x)[8], bool interleaved) const {
-    float y[8];
-    if (interleaved) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], partner);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = turns ? fmaf(y[j], s[j], x[j] * c[j]) : x[j];
+  static __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float na = a * c - b * s, nb = b * c + a * s;
+    a = na, b = nb;
   }
 };
 
-// RMS norm of the heads that the warp's lane groups hold, where `norm` (all
-// lanes take part).
+// The lane's 8 norm weights; ones where there are none.
 template <int D>
-__device__ __forceinline__ void head_norm(float (&x)[8], const float (&w)[8], bool norm, float eps) {
+__device__ __forceinline__ void load_weight(const __nv_bfloat16* w, const HeadLane<D>& hl, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = 1.f;
+  if (w) unpack8(hl.read(w), x);
+}
+
+// RMS norm of the heads that the warp's lane groups hold (all lanes take part).
+template <int D>
+__device__ __forceinline__ void head_norm(float (&x)[8], const float (&w)[8], float eps) {
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
 #pragma unroll
   for (int o = D / 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float r = norm ? 1.0f / sqrtf(sum * (1.0f / D) + eps) : 1.0f;
+  const float r = rsqrtf(fmaf(sum, 1.0f / D, eps));
 #pragma unroll
   for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-}
-
-// A lane's 8 norm weights; ones where there are none.
-__device__ __forceinline__ void load_weight(const __nv_bfloat16* w, int lane_in_head, float (&x)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = 1.f;
-  if (w) unpack8(*reinterpret_cast<const uint4*>(w + 8 * lane_in_head), x);
 }
 
 }  // namespace sgr
