@@ -13,7 +13,8 @@
 #include "sgr_attention.h"
 #include "sgr_internal.h"
 #include "sgr_kv_append.cuh"
-#include "sgr_kv_attn.cuh"
+#include "sgr_kv_attn_few.cuh"
+#include "sgr_kv_attn_rows.cuh"
 
 namespace {
 
@@ -391,7 +392,14 @@ AttnKernel attn_kernel_of() {
           sgr::AttnShape<D, NT>::kThreads};
 }
 
+template <int D>
+AttnKernel attn_rows_kernel_of() {
+  return {sgr::kv_attn_rows_kernel<D>, sgr::kv_attn_join_kernel<D, sgr::kRowsNT>, sgr::rows_attn_smem_bytes<D>(),
+          sgr::kRowsThreads};
+}
+
 AttnKernel attn_kernel(int dim, int nt) {
+  if (nt == sgr::kRowsNT) return dim == 64 ? attn_rows_kernel_of<64>() : attn_rows_kernel_of<128>();
   if (dim == 64) return nt == 8 ? attn_kernel_of<64, 8>() : nt == 16 ? attn_kernel_of<64, 16>() : attn_kernel_of<64, 32>();
   return nt == 8 ? attn_kernel_of<128, 8>() : nt == 16 ? attn_kernel_of<128, 16>() : attn_kernel_of<128, 32>();
 }
@@ -402,6 +410,12 @@ AttnKernel attn_kernel(int dim, int nt) {
 #define SGR_KV_WHOLE_TILES 4
 #endif
 constexpr int kWholeTiles = SGR_KV_WHOLE_TILES;
+
+// Rows of a sequence and key/value head from which the 128-row kernel is taken.
+#ifndef SGR_KV_MANY_ROWS
+#define SGR_KV_MANY_ROWS 65
+#endif
+constexpr int kManyRows = SGR_KV_MANY_ROWS;
 
 struct AttnPlan {
   int nt;           // rows of a row tile
@@ -417,13 +431,14 @@ struct AttnPlan {
 AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
-  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows < kManyRows ? 32 : sgr::kRowsNT;
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
   const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
   a.split = tiles > kWholeTiles;
   const long long units = c.heads * row_tiles * (a.split ? tiles : 1);
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
-  a.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
+  const long long ctas = a.nt == sgr::kRowsNT ? sms : 2LL * sms;
+  a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
   a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
   return a;
@@ -499,7 +514,7 @@ int kv_init_device(int dev) {
     }
     bool ok = true;
     for (int dim : {64, 128})
-      for (int nt : {8, 16, 32})
+      for (int nt : {8, 16, 32, sgr::kRowsNT})
         ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(attn_kernel(dim, nt).fn)) == cudaSuccess;
     if (prev != dev) cudaSetDevice(prev);
     if (ok)

@@ -1,48 +1,19 @@
 // sgr_kv_attn.cuh -- attention of new tokens over the paged E4M3 cache
-// (sgr_attention.h):
+// (sgr_attention.h): what its two kernels share -- the work and its split, the
+// warp that walks it and loads pages, and the join of partial sums.
 //
-//     o = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q.k_t)
+// The unit of work is a row tile (up to NT query rows that share a key/value
+// head: the head's query group, times the new tokens of a sequence) against a
+// 128-token tile of the cache.  Every CTA takes the same number of units of
+// all sequences and heads, in order, whatever the lengths; a row tile that
+// spans CTAs leaves partial sums (o, R, l) in the workspace and a second kernel
+// joins them in order (the same bits on every run).  For short caches
+// (`whole`) a row tile is one unit and nothing is joined.
 //
-// Per row tile (up to NT query rows that share a key/value head: the head's
-// query group, times the new tokens) and 128-token tile of the cache:
-//
-//     S^T [128 tokens, NT] = K Q^T      codes of K as they are in the cache
-//     P^T = 2^(S' - m)                  one thread per token
-//     O^T [D, NT]          = V^T P^T    codes of V as they are, read M-major
-//
-// Both products run on the FP8 tensor core (tcgen05.mma kind::f8f6f4) with
-// the cache's codes as the 128-row operand straight from TMA, so that nothing
-// is converted per cached element.  The small operands are brought into E4M3
-// as two parts b = hi + lo / 32, each row (or tile) scaled by a power of two
-// that puts its largest magnitude in [128, 256]: hi = e4m3(b),
-// lo = e4m3(32 (b - hi)).  That holds 8 significant bits (all of a BF16
-// query) down to 2^-14 of the largest and an absolute 2^-22 of it below.  hi
-// and lo rows sit side by side in the operand (2 NT columns of the
-// accumulator) and are added in FP32.
-//
-// Softmax: weights are 2^(s' - R) with a whole number R for each column that
-// only moves, up, when a score exceeds it (one vote of the four warps a tile;
-// then the tile's maxima are found), so what came before is rescaled seldom
-// and by a power of two: exactly.  The product of a tile is read back and
-// accumulated in registers (thread d holds o[.][d]); no accumulator in tensor
-// memory is ever rescaled.  Weights are 256 p in hi and lo: 8 bits down to
-// p = 2^-14, 4 bits to 2^-19, nothing below 2^-23 of the largest so far.  A
-// page's key scale multiplies the score; its value scale 2^e is added to the
-// exponent of P and taken out of the sum of weights again.
-//
-// Work split: every CTA takes the same number of (row tile, 128-token tile)
-// units of all sequences and heads, in order, whatever the lengths; a row
-// tile that spans CTAs leaves partial sums (o, M, l) in the workspace and a
-// second kernel joins them in order (the same bits on every run).  For short
-// caches (`whole`) a row tile is one unit and nothing is joined.
-//
-// Bound: the cache bytes, 2 D a token and key/value head, each read once per
-// row tile.
-//
-// Roles (two CTAs an SM): 4 or 8 softmax warps (thread = token, then = element
-// d; with 8, two groups of 4 take half of the columns each), one warp that
-// walks the work, loads pages by TMA and hands out segments, one that issues
-// the MMAs, two that bring the next segments' queries into the operand.
+// Both kernels feed the FP8 tensor core (tcgen05.mma kind::f8f6f4) with the
+// cache's codes straight from TMA.  The other operands, queries and weights,
+// are brought into E4M3 as two parts, hi = e4m3(b) and lo = e4m3 of the rest,
+// each row scaled by a power of two, which holds 8 significant bits.
 #pragma once
 
 #include <cuda.h>
@@ -98,55 +69,6 @@ struct AttnParams {
   AttnPiece* pieces;  // [grid]
 };
 
-template <int D, int NT>
-struct AttnShape {
-  static constexpr int kGroups = NT == 8 ? 1 : 2;  // of 4 softmax warps
-  static constexpr int kC = NT / kGroups;          // columns a softmax thread
-  static constexpr int kSoftmax = 4 * kGroups;     // warps
-  static constexpr int kThreads = 32 * (kSoftmax + 4);
-  static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
-  static constexpr int kTileBytes = kAttnTile * D;
-  static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
-  // As many stages and query buffers as two CTAs an SM allow.
-  static constexpr int kStages = D == 128 ? (NT <= 16 ? 3 : 2) : (NT == 8 ? 6 : NT == 16 ? 5 : 4);
-  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : 4;
-  static constexpr int kPBytes = kCols * kAttnTile;
-  static constexpr int kQBytes = kCols * D;
-  static constexpr int kTmemCols = 4 * kCols;  // S and O, two each
-};
-
-template <int D, int NT>
-struct AttnCtl {
-  using Sh = AttnShape<D, NT>;
-  static constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC;
-  uint64_t kfull[S], vfull[S], empty[S];
-  uint64_t sfull[2], sempty[2], ofull[2], oempty[2], qfull[Q], qempty[Q], pfull, drain;
-  uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
-  uint32_t tmem;
-  int abort;
-  int go[2][2];
-  unsigned nan_tokens[4];
-  AttnSeg seg[kAttnQueue];
-  float kscale[S][8], vexp[S][8];  // of a stage's pages
-  int flags[S];                    // 1: some token is not live, 2: rows see different tokens
-  long long qout[Q][NT];           // a row's place in the output
-  alignas(16) float qf[Q][NT];     // its score factor
-  int qpos[Q][NT];                 // the last position that it sees
-  alignas(16) float wmax[Sh::kSoftmax][C], wsum[Sh::kSoftmax][C];
-  alignas(16) float ref[Sh::kSoftmax][C], alpha[Sh::kSoftmax][2][C];  // a warp's own copies
-};
-
-template <int D, int NT>
-constexpr int attn_ctl_bytes() {
-  return (int)((sizeof(AttnCtl<D, NT>) + 1023) / 1024 * 1024);
-}
-
-template <int D, int NT>
-constexpr int attn_smem_bytes() {
-  using S = AttnShape<D, NT>;
-  return 1024 + attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + S::kQBufs * S::kQBytes;
-}
-
 // Row tile j of a sequence: its rows, the positions they see, its tiles, its
 // units (a row tile that sees nothing is one unit: its zeros).
 struct AttnItem {
@@ -180,6 +102,252 @@ __device__ __forceinline__ int attn_seq_units(const AttnParams& p, const KvSeq& 
   return u;
 }
 
+// The warp that walks a CTA's share of the work: finds it, hands out its
+// segments, loads the pages of its tiles by TMA (V, then K, of a stage of the
+// ring) and writes their scales beside them.  Rows that see nothing get their
+// zeros here.  Executed by one whole warp.
+template <int D, int NT, class Ctl>
+__device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                          uint32_t ring) {
+  constexpr int S = Ctl::kStages, M = Ctl::kMeta, kTile = kAttnTile * D, kStage = 2 * kTile;
+  const int lane = threadIdx.x & 31;
+  volatile int* abort_flag = &c.abort;
+  // ------------------------------------------------ this CTA's share of the work
+  // CTA c of `active` takes the units [begin(c), begin(c + 1)) of all
+  // sequences: the first `rest` CTAs one more than `per`.  (The host refuses
+  // what might not fit 31 bits.)
+  const int ps = p.cache.page_shift, hk = p.cache.heads;
+  int b = 0, h = 0, j = 0, skip = 0, u = 0, u1 = 0, per = 0, rest = 0;
+  KvSeq s{0, 0, 0};
+  {
+    // Each lane counts its (consecutive) sequences.
+    const int per_lane = (p.batch.batch + 31) / 32, b_first = lane * per_lane;
+    const int b_last = min(b_first + per_lane, p.batch.batch);
+    int mine = 0;
+#pragma unroll 4
+    for (int x = b_first; x < b_last; ++x) mine += attn_seq_units<NT>(p, kv_seq(p.batch, ps, x, p.err)) * hk;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += up;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
+    // (with fewer units than CTAs the last ones have none, the others one each)
+    const int active = min(total, (int)gridDim.x), c0 = (int)blockIdx.x;
+    if (c0 < active) {
+      per = total / active;
+      rest = total - per * active;
+      u = c0 * per + min(c0, rest);
+      u1 = u + per + (c0 < rest ? 1 : 0);
+      const int before = upto - mine;
+      const int src = __ffs(__ballot_sync(0xffffffffu, u >= before && u < upto)) - 1;
+      int off = u - __shfl_sync(0xffffffffu, before, max(src, 0)), units = 0;
+      // (row offsets that run backwards may count more units than 31 bits hold)
+      bool found = src >= 0;
+      for (b = max(src, 0) * per_lane; found; ++b) {
+        if (b >= p.batch.batch) found = false;
+        if (!found) break;
+        s = kv_seq(p.batch, ps, b, nullptr);
+        units = attn_seq_units<NT>(p, s);
+        if (off < units * hk) break;
+        off -= units * hk;
+      }
+      if (!found) u1 = u, off = 0, units = 1;
+      h = off / units;
+      off -= h * units;
+      for (int x; found && off >= (x = attn_item<NT>(p, s, j).units); ++j) off -= x;
+      skip = off;
+    }
+  }
+  auto cta_of = [&](int x) {  // the CTA that takes unit x
+    const int y = rest * (per + 1);
+    return x < y ? x / (per + 1) : rest + (x - y) / per;
+  };
+  // ------------------------------------------------------- walk and TMA loads
+  const uint64_t policy = p.reuse ? policy_evict_last() : policy_evict_first();
+  int sq = 0;
+  AttnItem it{};
+  bool ok = true;
+  AttnPiece piece{};  // of the row tile that goes on in the next CTA
+  if (u < u1) it = attn_item<NT>(p, s, j);
+  int t = 0, t_end = 0;  // tiles of the segment handed out last
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait_nap<kNapWalk>(smem_u32(bar), parity, abort_flag)) {
+      if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
+      *abort_flag = 1;
+      ok = false;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  };
+  auto hand_out = [&](const AttnSeg& g) {
+    const int qi = sq % kAttnQueue;
+    wait(&c.segempty[qi], ((sq / kAttnQueue) & 1) ^ 1);
+    if (!ok) return;
+    if (lane == 0) {
+      c.seg[qi] = g;
+      mbar_arrive(smem_u32(&c.segfull[qi]));
+    }
+    ++sq;
+  };
+  struct Tile {
+    int h, flags;
+  int live0, live1;  // its tokens that some row sees
+    int page;  // this lane's table entry, -1 = none
+    float ks, vs;
+  };
+  AttnItem cur{};
+  int cur_h = 0, cur_b = 0, cur_p0 = 0, cur_p1 = 0;
+  // The next tile of this CTA's share; hands out the segments it enters.
+  auto next_tile = [&](Tile& x) -> bool {
+    while (t == t_end) {
+      if (u >= u1 || !ok) return false;
+      if (it.nrows <= 0) {  // past the last row tile of the head
+        j = 0;
+        if (s.n == 0 || ++h == hk) {
+          h = 0;
+          do {
+            if (++b >= p.batch.batch) return false;
+            s = kv_seq(p.batch, ps, b, nullptr);
+          } while (s.n == 0);
+        }
+        it = attn_item<NT>(p, s, 0);
+      }
+      const int units = it.units, take = min(u1 - u, units - skip);
+      u += take;
+      if (it.tb <= it.ta) {  // rows that see nothing: zeros
+        for (int e = lane; e < it.nrows * (D / 8); e += 32) {
+          const int r = it.r0 + e / (D / 8), tok = div_group(p, r);
+          *reinterpret_cast<uint4*>(p.out.p + (long long)(s.row0 + tok) * p.out.ts +
+                                    (long long)(h * p.group + r - tok * p.group) * p.out.hs + e % (D / 8) * 8) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        it = attn_item<NT>(p, s, ++j);
+        continue;
+      }
+      AttnSeg g;
+      g.kind = (skip == 0 ? kSegStart : 0) | (skip + take == units ? kSegEnd : 0);
+      g.h = h;
+      g.row0 = s.row0;
+      g.r0 = it.r0;
+      g.nrows = it.nrows;
+      g.first = s.len - s.n;
+      g.ta = it.ta + skip;
+      g.tb = p.whole ? it.tb : g.ta + take;
+      g.tlo = it.tlo;
+      g.thi = it.thi;
+      g.slot = 2 * (int)blockIdx.x + (skip == 0 ? 1 : 0);
+      g.pad = 0;
+      hand_out(g);
+      if (!ok) return false;
+      if (g.kind == kSegStart) piece = {cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
+      t = g.ta;
+      t_end = g.tb;
+      cur = it;
+      cur_h = h;
+      cur_b = b;
+      cur_p0 = g.first + div_group(p, it.r0);
+      cur_p1 = it.thi - 1;
+      skip = 0;
+      if (g.kind & kSegEnd) it = attn_item<NT>(p, s, ++j);
+    }
+    const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
+    ++t;
+    x.h = cur_h;
+  x.live0 = max(cur.tlo - x0, 0);
+  x.live1 = min(cur.thi - x0, kAttnTile);
+    x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
+    if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
+    // This lane's page of the tile, where some row sees a position of it.
+    const int block = (x0 >> ps) + lane, at = block << ps;
+    x.page = -1;
+    if (lane < (kAttnTile >> ps) && at < cur.thi && at + (1 << ps) > cur.tlo) {
+      x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
+      x.flags |= 4;
+    }
+    return true;
+  };
+  // Checks the entry and asks for the page's scales.
+  auto load_scales = [&](Tile& x) {
+    if ((x.flags & 4) && (x.page < 0 || x.page >= p.cache.num_pages)) {
+      report_error(p.err, kErrIndex);
+      x.page = -1;
+    }
+    x.ks = x.vs = 0.f;
+    if (x.page >= 0) {
+      const long long at = (long long)x.page * p.cache.scale_stride + x.h;
+      x.ks = p.cache.k_scale[at];
+      x.vs = p.cache.v_scale[at];
+    }
+  };
+  // One tile ahead of the copies: its table entries are asked for before
+  // this tile's scales arrive, which reach the stage behind its copies.
+  Tile a{}, next{};
+  bool has = next_tile(a);
+  if (has) load_scales(a);
+  int i = 0, slot = 0;
+  uint32_t par = 0;
+  const int per_tile = kAttnTile >> ps;
+  const uint32_t page_bytes = (uint32_t)D << ps;
+  while (has && ok) {
+    if (i >= S) wait(&c.empty[slot], par ^ 1u);
+    if (!ok) break;
+    const unsigned live = __ballot_sync(0xffffffffu, a.page >= 0);
+    const uint32_t kb = smem_u32(&c.kfull[slot]), vb = smem_u32(&c.vfull[slot]);
+    if (lane == 0) {
+      mbar_expect_tx(kb, (uint32_t)__popc(live) * page_bytes);
+      mbar_arrive_expect_tx(vb, (uint32_t)__popc(live) * page_bytes);
+    }
+    __syncwarp();
+    if (a.page >= 0) {
+      const uint32_t dst = ring + (uint32_t)slot * kStage + (uint32_t)lane * page_bytes;
+      tma_load_4d(dst + kTile, &tmK, 0, 0, a.h, a.page, kb, policy);
+      tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, vb, policy);
+    }
+    has = next_tile(next);
+    const int meta = i % M;
+    if (lane < per_tile) {
+      c.kscale[meta][lane] = a.ks;
+      // (an exponent of -inf marks a page that is not there)
+      c.vexp[meta][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
+    }
+    if (lane == 0) {
+      c.flags[meta] = (a.flags & 3) | (__popc(live) < per_tile ? 1 : 0);
+      c.live[meta][0] = a.live0;
+      c.live[meta][1] = a.live1;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(kb);
+    ++i;
+    if (++slot == S) {
+      slot = 0;
+      par ^= 1u;
+    }
+    a = next;
+    if (has) load_scales(a);
+  }
+  bool stopped = false;
+  if (Ctl::kStopStage && ok) {  // a stage that ends the sequence
+    if (i >= S) wait(&c.empty[slot], par ^ 1u);
+    stopped = ok;
+    if (ok && lane == 0) {
+      c.flags[i % M] = 8;
+      mbar_arrive(smem_u32(&c.kfull[slot]));
+      mbar_arrive(smem_u32(&c.vfull[slot]));
+    }
+  }
+  AttnSeg stop{};
+  stop.kind = kSegStop;
+  hand_out(stop);
+  if (lane == 0) p.pieces[blockIdx.x] = piece;
+  // Every copy that this warp issued lands before the CTA may exit.  (The
+  // stage that the stop took was empty: its copies have landed.)
+  bool landed = true;
+  for (int k = max(i - S + (stopped ? 1 : 0), 0); k < i && landed; ++k)
+    landed = mbar_wait(smem_u32(&c.kfull[k % S]), (k / S) & 1) && mbar_wait(smem_u32(&c.vfull[k % S]), (k / S) & 1);
+  if (!landed) report_error(p.err, kErrDrain);
+}
+
 // 2^d for whole d <= 0 (0 from -127 down), on the integer unit.
 __device__ __forceinline__ float exp2_whole(float d) {
   return __int_as_float((__float_as_int(fmaxf(d, -127.f) + 12582912.f) << 23) + 0x3f800000);
@@ -197,752 +365,53 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
-// Sums of C columns over the warp's lanes: lane l returns column l / (32 / C).
-template <int C>
-__device__ __forceinline__ float warp_column_sums(float (&x)[C]) {
-  const int lane = threadIdx.x & 31;
-  int d = 16;
+// Eight elements (of a BF16 row held by kLanes neighbouring lanes) as hi and lo
+// codes, b = hi + lo / lo_scale, b = x * sign / factor with the row's largest
+// |b| in [128, 256).  A row with an infinity or NaN gets a NaN factor.
+struct QuerySplit {
+  uint2 hi, lo;
+  float factor;
+};
+
+template <int kLanes>
+__device__ __forceinline__ QuerySplit split_query(const uint4& v, float sign, float lo_scale) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t mag = 0;
 #pragma unroll
-  for (int n = C / 2; n > 0; n >>= 1, d >>= 1) {
-    const bool upper = (lane & d) != 0;
+  for (int k = 0; k < 4; ++k) mag = max(mag, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
 #pragma unroll
-    for (int k = 0; k < n; ++k) {
-      const float give = upper ? x[k] : x[k + n], keep = upper ? x[k + n] : x[k];
-      x[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-    }
-  }
+  for (int o = kLanes / 2; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
+  const int ex = (int)(mag >> 7);  // biased exponent of the row's largest magnitude
+  int k = ex == 0 ? 126 : 134 - ex;
+  k = min(max(k, -120), 126);
+  const float sc = kv_exp2i(k) * sign;
+  float x[8], h[8];
+  unpack8(v, x);
 #pragma unroll
-  for (; d > 0; d >>= 1) x[0] += __shfl_xor_sync(0xffffffffu, x[0], d);
-  return x[0];
+  for (int e = 0; e < 8; ++e) x[e] *= sc;
+  QuerySplit s;
+  s.hi = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
+  from_e4m3x4(s.hi.x, h[0], h[1], h[2], h[3]);
+  from_e4m3x4(s.hi.y, h[4], h[5], h[6], h[7]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = (x[e] - h[e]) * lo_scale;  // exact
+  s.lo = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
+  s.factor = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k);
+  return s;
 }
 
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
-}
-
-constexpr float kLoScale = 1.f / 32.f;
-
-// Two values in [0, 256] -> their hi codes (bytes 0, 1) and lo codes (bytes 2,
-// 3).  (FP16 holds b to 11 bits, b - hi exactly.)
-__device__ __forceinline__ uint32_t split2(float a, float b) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 x, y;\n\t"
-      "cvt.rn.f16x2.f32 x, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 h, x;\n\t"
-      "cvt.rn.f16x2.e4m3x2 y, h;\n\t"
-      "sub.rn.f16x2 x, x, y;\n\t"
-      "mul.rn.f16x2 x, x, %3;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n\t"
-      "mov.b32 %0, {h, l};\n\t}"
-      : "=r"(r)
-      : "f"(a), "f"(b), "r"(0x50005000u));  // 0x5000 = 32
-  return r;
-}
-
-// x[q] = hi[q] + lo[q] / 32 of C accumulator columns at `hi`, the lo ones
-// `apart` columns on.
-template <int C>
-__device__ __forceinline__ void tmem_ld_sum(uint32_t hi, uint32_t apart, float (&x)[C]) {
-  if constexpr (C == 8) {
-    float v[8], w[8];
-    tmem_ld8x2(hi, hi + apart, v, w);
-#pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = fmaf(w[q], kLoScale, v[q]);
-  } else {
-    float v[16];
-    tmem_ld16(hi, x);
-    tmem_ld16(hi + apart, v);
-#pragma unroll
-    for (int q = 0; q < 16; ++q) x[q] = fmaf(v[q], kLoScale, x[q]);
-  }
-}
-
-template <int D, int NT>
-__global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
-    kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
-  using Sh = AttnShape<D, NT>;
-  constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC, kCols = Sh::kCols, kSoftmax = Sh::kSoftmax;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  AttnCtl<D, NT>& c = *reinterpret_cast<AttnCtl<D, NT>*>(smem_raw + (base - raw));
-  const uint32_t ring = base + attn_ctl_bytes<D, NT>();
-  const uint32_t pbuf = ring + S * Sh::kStageBytes, qbuf = pbuf + Sh::kPBytes;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort_flag = &c.abort;
-
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(smem_u32(&c.kfull[i]), 1);
-      mbar_init(smem_u32(&c.vfull[i]), 1);
-      mbar_init(smem_u32(&c.empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&c.sfull[i]), 1);
-      mbar_init(smem_u32(&c.sempty[i]), kSoftmax);
-      mbar_init(smem_u32(&c.ofull[i]), 1);
-      mbar_init(smem_u32(&c.oempty[i]), kSoftmax);
-    }
-    for (int i = 0; i < Q; ++i) {
-      mbar_init(smem_u32(&c.qfull[i]), 2);
-      mbar_init(smem_u32(&c.qempty[i]), 1 + kSoftmax);  // the last MMA that reads it, the softmax warps
-    }
-    mbar_init(smem_u32(&c.pfull), kSoftmax);
-    mbar_init(smem_u32(&c.drain), 1);
-    for (int i = 0; i < kAttnQueue; ++i) {
-      mbar_init(smem_u32(&c.segfull[i]), 1);
-      mbar_init(smem_u32(&c.segempty[i]), kSoftmax + 3);  // and the MMA and query warps
-    }
-    c.abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == kSoftmax + 1) {
-    tmem_alloc(smem_u32(&c.tmem), Sh::kTmemCols);
-    tmem_relinquish();
-  }
-  if (tid == 32) {
-    prefetch_tmap(&tmK);
-    prefetch_tmap(&tmV);
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = c.tmem;
-  // (only now: a dependent that allocates tensor memory must not come first)
-  pdl_launch_dependents();
-  pdl_wait();
-
-  if (warp == kSoftmax) {
-    // ------------------------------------------------ this CTA's share of the work
-    // CTA c of `active` takes the units [begin(c), begin(c + 1)) of all
-    // sequences: the first `rest` CTAs one more than `per`.  (The host refuses
-    // what might not fit 31 bits.)
-    const int ps = p.cache.page_shift, hk = p.cache.heads;
-    int b = 0, h = 0, j = 0, skip = 0, u = 0, u1 = 0, per = 0, rest = 0;
-    KvSeq s{0, 0, 0};
-    {
-      // Each lane counts its (consecutive) sequences.
-      const int per_lane = (p.batch.batch + 31) / 32, b_first = lane * per_lane;
-      const int b_last = min(b_first + per_lane, p.batch.batch);
-      int mine = 0;
-#pragma unroll 4
-      for (int x = b_first; x < b_last; ++x) mine += attn_seq_units<NT>(p, kv_seq(p.batch, ps, x, p.err)) * hk;
-      int upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += up;
-      }
-      const int total = __shfl_sync(0xffffffffu, upto, 31);
-      // (with fewer units than CTAs the last ones have none, the others one each)
-      const int active = min(total, (int)gridDim.x), c0 = (int)blockIdx.x;
-      if (c0 < active) {
-        per = total / active;
-        rest = total - per * active;
-        u = c0 * per + min(c0, rest);
-        u1 = u + per + (c0 < rest ? 1 : 0);
-        const int before = upto - mine;
-        const int src = __ffs(__ballot_sync(0xffffffffu, u >= before && u < upto)) - 1;
-        int off = u - __shfl_sync(0xffffffffu, before, max(src, 0)), units = 0;
-        // (row offsets that run backwards may count more units than 31 bits hold)
-        bool found = src >= 0;
-        for (b = max(src, 0) * per_lane; found; ++b) {
-          if (b >= p.batch.batch) found = false;
-          if (!found) break;
-          s = kv_seq(p.batch, ps, b, nullptr);
-          units = attn_seq_units<NT>(p, s);
-          if (off < units * hk) break;
-          off -= units * hk;
-        }
-        if (!found) u1 = u, off = 0, units = 1;
-        h = off / units;
-        off -= h * units;
-        for (int x; found && off >= (x = attn_item<NT>(p, s, j).units); ++j) off -= x;
-        skip = off;
-      }
-    }
-    auto cta_of = [&](int x) {  // the CTA that takes unit x
-      const int y = rest * (per + 1);
-      return x < y ? x / (per + 1) : rest + (x - y) / per;
-    };
-    // ------------------------------------------------------- walk and TMA loads
-    const uint64_t policy = p.reuse ? policy_evict_last() : policy_evict_first();
-    int sq = 0;
-    AttnItem it{};
-    bool ok = true;
-    AttnPiece piece{};  // of the row tile that goes on in the next CTA
-    if (u < u1) it = attn_item<NT>(p, s, j);
-    int t = 0, t_end = 0;  // tiles of the segment handed out last
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !mbar_wait_nap<kNapWalk>(smem_u32(bar), parity, abort_flag)) {
-        if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
-        *abort_flag = 1;
-        ok = false;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    };
-    auto hand_out = [&](const AttnSeg& g) {
-      const int qi = sq % kAttnQueue;
-      wait(&c.segempty[qi], ((sq / kAttnQueue) & 1) ^ 1);
-      if (!ok) return;
-      if (lane == 0) {
-        c.seg[qi] = g;
-        mbar_arrive(smem_u32(&c.segfull[qi]));
-      }
-      ++sq;
-    };
-    struct Tile {
-      int h, flags;
-      int page;  // this lane's table entry, -1 = none
-      float ks, vs;
-    };
-    AttnItem cur{};
-    int cur_h = 0, cur_b = 0, cur_p0 = 0, cur_p1 = 0;
-    // The next tile of this CTA's share; hands out the segments it enters.
-    auto next_tile = [&](Tile& x) -> bool {
-      while (t == t_end) {
-        if (u >= u1 || !ok) return false;
-        if (it.nrows <= 0) {  // past the last row tile of the head
-          j = 0;
-          if (s.n == 0 || ++h == hk) {
-            h = 0;
-            do {
-              if (++b >= p.batch.batch) return false;
-              s = kv_seq(p.batch, ps, b, nullptr);
-            } while (s.n == 0);
-          }
-          it = attn_item<NT>(p, s, 0);
-        }
-        const int units = it.units, take = min(u1 - u, units - skip);
-        u += take;
-        if (it.tb <= it.ta) {  // rows that see nothing: zeros
-          for (int e = lane; e < it.nrows * (D / 8); e += 32) {
-            const int r = it.r0 + e / (D / 8), tok = div_group(p, r);
-            *reinterpret_cast<uint4*>(p.out.p + (long long)(s.row0 + tok) * p.out.ts +
-                                      (long long)(h * p.group + r - tok * p.group) * p.out.hs + e % (D / 8) * 8) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          it = attn_item<NT>(p, s, ++j);
-          continue;
-        }
-        AttnSeg g;
-        g.kind = (skip == 0 ? kSegStart : 0) | (skip + take == units ? kSegEnd : 0);
-        g.h = h;
-        g.row0 = s.row0;
-        g.r0 = it.r0;
-        g.nrows = it.nrows;
-        g.first = s.len - s.n;
-        g.ta = it.ta + skip;
-        g.tb = p.whole ? it.tb : g.ta + take;
-        g.tlo = it.tlo;
-        g.thi = it.thi;
-        g.slot = 2 * (int)blockIdx.x + (skip == 0 ? 1 : 0);
-        g.pad = 0;
-        hand_out(g);
-        if (!ok) return false;
-        if (g.kind == kSegStart) piece = {cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
-        t = g.ta;
-        t_end = g.tb;
-        cur = it;
-        cur_h = h;
-        cur_b = b;
-        cur_p0 = g.first + div_group(p, it.r0);
-        cur_p1 = it.thi - 1;
-        skip = 0;
-        if (g.kind & kSegEnd) it = attn_item<NT>(p, s, ++j);
-      }
-      const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
-      ++t;
-      x.h = cur_h;
-      x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
-      if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
-      // This lane's page of the tile, where some row sees a position of it.
-      const int block = (x0 >> ps) + lane, at = block << ps;
-      x.page = -1;
-      if (lane < (kAttnTile >> ps) && at < cur.thi && at + (1 << ps) > cur.tlo) {
-        x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
-        x.flags |= 4;
-      }
-      return true;
-    };
-    // Checks the entry and asks for the page's scales.
-    auto load_scales = [&](Tile& x) {
-      if ((x.flags & 4) && (x.page < 0 || x.page >= p.cache.num_pages)) {
-        report_error(p.err, kErrIndex);
-        x.page = -1;
-      }
-      x.ks = x.vs = 0.f;
-      if (x.page >= 0) {
-        const long long at = (long long)x.page * p.cache.scale_stride + x.h;
-        x.ks = p.cache.k_scale[at];
-        x.vs = p.cache.v_scale[at];
-      }
-    };
-    // One tile ahead of the copies: its table entries are asked for before
-    // this tile's scales arrive, which reach the stage behind its copies.
-    Tile a{}, next{};
-    bool has = next_tile(a);
-    if (has) load_scales(a);
-    int i = 0, slot = 0;
-    uint32_t par = 0;
-    const int per_tile = kAttnTile >> ps;
-    const uint32_t page_bytes = (uint32_t)D << ps;
-    while (has && ok) {
-      if (i >= S) wait(&c.empty[slot], par ^ 1u);
-      if (!ok) break;
-      const unsigned live = __ballot_sync(0xffffffffu, a.page >= 0);
-      const uint32_t kb = smem_u32(&c.kfull[slot]), vb = smem_u32(&c.vfull[slot]);
-      if (lane == 0) {
-        mbar_expect_tx(kb, (uint32_t)__popc(live) * page_bytes);
-        mbar_arrive_expect_tx(vb, (uint32_t)__popc(live) * page_bytes);
-      }
-      __syncwarp();
-      if (a.page >= 0) {
-        const uint32_t dst = ring + (uint32_t)slot * Sh::kStageBytes + (uint32_t)lane * page_bytes;
-        tma_load_4d(dst + Sh::kTileBytes, &tmK, 0, 0, a.h, a.page, kb, policy);
-        tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, vb, policy);
-      }
-      has = next_tile(next);
-      if (lane < per_tile) {
-        c.kscale[slot][lane] = a.ks;
-        // (an exponent of -inf marks a page that is not there)
-        c.vexp[slot][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
-      }
-      if (lane == 0) c.flags[slot] = (a.flags & 3) | (__popc(live) < per_tile ? 1 : 0);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(kb);
-      ++i;
-      if (++slot == S) {
-        slot = 0;
-        par ^= 1u;
-      }
-      a = next;
-      if (has) load_scales(a);
-    }
-    AttnSeg stop{};
-    stop.kind = kSegStop;
-    hand_out(stop);
-    if (lane == 0) p.pieces[blockIdx.x] = piece;
-    // Every copy that this warp issued lands before the CTA may exit.
-    bool landed = true;
-    for (int k = i > S ? i - S : 0; k < i && landed; ++k)
-      landed = mbar_wait(smem_u32(&c.kfull[k % S]), (k / S) & 1) && mbar_wait(smem_u32(&c.vfull[k % S]), (k / S) & 1);
-    if (!landed) report_error(p.err, kErrDrain);
-  } else if (warp == kSoftmax + 1) {
-    // ------------------------------------------------------------- MMA issuer
-    // Issues whichever of the two products can go: V^T P^T of the oldest tile
-    // whose weights are written, or K Q^T of the next one.  Neither waits for
-    // the other's inputs.
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(kAttnTile, kCols), idesc_o = idesc_s | (1u << 15);
-      const uint32_t acc_o = tmem + 2 * kCols;
-      int sq = 0, filled = -1, t = 0, t_end = 0;  // segments read, query buffer in use, its tiles
-      int i = 0, islot = 0, k = 0, kslot = 0;     // tiles scored, tiles weighted
-      uint32_t ipar = 0, kpar = 0;
-      bool fresh = false, stop = false, ok = true;
-      uint64_t since = 0;
-      unsigned idle = 0;
-      while (ok && (!stop || k < i)) {
-        if (k < i && mbar_test_wait(smem_u32(&c.pfull), k & 1) && mbar_test_wait(smem_u32(&c.vfull[kslot]), kpar) &&
-            mbar_test_wait(smem_u32(&c.oempty[k & 1]), ((k >> 1) & 1) ^ 1)) {
-          tc_fence_after();
-          // D = 64: the upper half of the 128 rows reads the K tile behind V;
-          // its rows of the accumulator are not used.
-          const uint64_t vd = smem_desc_rows<D>(ring + (uint32_t)kslot * Sh::kStageBytes, Sh::kTileBytes);
-          const uint64_t pd = smem_desc_rows<128>(pbuf);
-#pragma unroll
-          for (int kk = 0; kk < kAttnTile / 32; ++kk)
-            mma_e4m3(acc_o + (k & 1) * kCols, vd + (uint64_t)(kk * (32 * D >> 4)), pd + (uint64_t)(kk * 2), idesc_o, kk > 0);
-          mma_commit(smem_u32(&c.ofull[k & 1]));
-          mma_commit(smem_u32(&c.empty[kslot]));
-          ++k;
-          if (++kslot == S) {
-            kslot = 0;
-            kpar ^= 1u;
-          }
-          idle = 0;
-          continue;
-        }
-        if (!stop && t == t_end) {
-          const int qi = sq % kAttnQueue;
-          if (mbar_test_wait(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1)) {
-            stop = (c.seg[qi].kind & kSegStop) != 0;
-            t = c.seg[qi].ta;
-            t_end = c.seg[qi].tb;
-            mbar_arrive(smem_u32(&c.segempty[qi]));
-            ++sq;
-            ++filled;
-            fresh = true;
-            idle = 0;
-            continue;
-          }
-        } else if (!stop && (!fresh || mbar_test_wait(smem_u32(&c.qfull[filled % Q]), (filled / Q) & 1)) &&
-                   mbar_test_wait(smem_u32(&c.kfull[islot]), ipar) &&
-                   mbar_test_wait(smem_u32(&c.sempty[i & 1]), ((i >> 1) & 1) ^ 1)) {
-          fresh = false;
-          tc_fence_after();
-          const uint64_t kd = smem_desc_rows<D>(ring + (uint32_t)islot * Sh::kStageBytes + Sh::kTileBytes);
-          const uint64_t qd = smem_desc_rows<D>(qbuf + (uint32_t)(filled % Q) * Sh::kQBytes);
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_e4m3(tmem + (i & 1) * kCols, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc_s, kk > 0);
-          mma_commit(smem_u32(&c.sfull[i & 1]));
-          if (++t == t_end) mma_commit(smem_u32(&c.qempty[filled % Q]));
-          ++i;
-          if (++islot == S) {
-            islot = 0;
-            ipar ^= 1u;
-          }
-          idle = 0;
-          continue;
-        }
-        // Nothing to issue: bounded, as every wait.
-        if (idle == 0) since = globaltimer_ns();
-        if (kNapMma) __nanosleep(kNapMma);
-        if ((++idle & 63u) == 0) {
-          if (*abort_flag) ok = false;
-          if (globaltimer_ns() - since > SGR_WAIT_LIMIT_NS) {
-            report_error(p.err, kErrWaitFull);
-            *abort_flag = 1;
-            ok = false;
-          }
-        }
-      }
-      mma_commit(smem_u32(&c.drain));
-      if (!mbar_wait(smem_u32(&c.drain), 0)) report_error(p.err, kErrDrain);
-    }
-  } else if (warp >= kSoftmax + 2) {
-    // ----------------------------------------------------------- query operand
-    constexpr int kLanes = D / 8, kRows = 64 / kLanes, kPass = NT / kRows;
-    const int qt = tid - 32 * (kSoftmax + 2), l = qt % kLanes;
-    int sq = 0, buf = 0;
-    uint32_t par = 0;
-    while (true) {
-      const int qi = sq % kAttnQueue;
-      bool ok = true;
-      if (lane == 0) ok = mbar_wait_nap<kNapQuery>(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      const AttnSeg g = c.seg[qi];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
-      ++sq;
-      if (g.kind & kSegStop) break;
-      // Row `pass` of this thread's: two are under way while one is converted.
-      auto load_row = [&](int pass, long long& out_at, int& pos) {
-        const int q = pass * kRows + qt / kLanes;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        pos = -1;  // a row that is none sees nothing
-        out_at = 0;
-        if (q < g.nrows) {
-          const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
-          pos = g.first + tok;
-          out_at = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
-          v = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
-        }
-        return v;
-      };
-      long long out0, out1 = 0;
-      int pos0, pos1 = -1;
-      uint4 v0 = load_row(0, out0, pos0), v1 = v0;
-      if (kPass > 1) v1 = load_row(1, out1, pos1);
-      if (lane == 0) ok = mbar_wait_nap<kNapQuery>(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-#pragma unroll 1
-      for (int i = 0; i < kPass; ++i) {
-        const int q = i * kRows + qt / kLanes, pos = pos0;
-        const long long out_at = out0;
-        const uint4 v = v0;
-        v0 = v1, out0 = out1, pos0 = pos1;
-        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1);
-        uint32_t mag = 0;
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mag = max(mag, max(u[k] & 0x7FFFu, (u[k] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, o));
-        const int ex = (int)(mag >> 7);  // biased exponent of the row's largest magnitude
-        int k = ex == 0 ? 126 : 134 - ex;
-        k = min(max(k, -120), 126);
-        const float sc = kv_exp2i(k);
-        float x[8], h[8];
-        unpack8(v, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= sc;
-        const uint2 hi = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
-        from_e4m3x4(hi.x, h[0], h[1], h[2], h[3]);
-        from_e4m3x4(hi.y, h[4], h[5], h[6], h[7]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = (x[e] - h[e]) * 32.f;  // exact
-        const uint2 lo = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
-        const uint32_t qb = qbuf + (uint32_t)(buf * Sh::kQBytes) + (uint32_t)((l & 1) * 8);
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(hi.x), "r"(hi.y) : "memory");
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(NT + q, l >> 1)), "r"(lo.x), "r"(lo.y) : "memory");
-        if (l == 0) {
-          // a row with an infinity or NaN gets NaN
-          c.qf[buf][q] = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k) * p.scale_log2;
-          c.qpos[buf][q] = pos;
-          c.qout[buf][q] = out_at;
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.qfull[buf]));
-      if (++buf == Q) {
-        buf = 0;
-        par ^= 1u;
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- softmax
-    // After a wait that ran out (abort) the waits fall through, so that the
-    // warps keep meeting at their barriers until the segments end.
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!mbar_wait_nap<kNapSoftmax>(smem_u32(bar), parity, abort_flag)) {
-        if (!*abort_flag) report_error(p.err, kErrWaitMma);
-        *abort_flag = 1;
-      }
-      __syncwarp();
-    };
-    const int group = warp >> 2, tok = tid & 127, q0 = group * C;  // columns q0 .. q0 + C - 1
-    auto meet = [&] {  // the group's 4 warps
-      __syncwarp();
-      if (Sh::kGroups == 1 || group == 0)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      else
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-    };
-    auto any_of_group = [&](bool x) {  // of its 128 threads
-      uint32_t any;
-      __syncwarp();
-      if (Sh::kGroups == 1 || group == 0)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(any)
-            : "r"((uint32_t)x)
-            : "memory");
-      else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(any)
-            : "r"((uint32_t)x)
-            : "memory");
-      return any != 0;
-    };
-    const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)q0;  // tensor-memory lanes of this warp
-    float o[C], l[C];
-    float run = 0.f;  // R of column q0 + lane
-    unsigned nan_rows = 0;
-    int i = 0, slot = 0, sq = 0, buf = 0;
-    uint32_t par = 0, qpar = 0;
-    bool scaled_before = false;  // whether R moved with the tile before
-    // O of tile k, read back and accumulated.
-    auto accumulate = [&](int k, bool scaled) {
-      wait(&c.ofull[k & 1], (k >> 1) & 1);
-      tc_fence_after();
-      float x[C];
-      tmem_ld_sum<C>(lane_base + 2 * kCols + (k & 1) * kCols, NT, x);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.oempty[k & 1]));
-      if (scaled) {
-#pragma unroll
-        for (int q = 0; q < C; ++q) o[q] *= c.alpha[warp][k & 1][q];
-      }
-#pragma unroll
-      for (int q = 0; q < C; ++q) o[q] += x[q];
-    };
-    while (true) {
-      const int qi = sq % kAttnQueue;
-      if (tok == 0) c.go[group][sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
-      meet();
-      if (!c.go[group][sq & 1]) {
-        if (tok == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
-        *abort_flag = 1;
-        break;
-      }
-      const AttnSeg g = c.seg[qi];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
-      ++sq;
-      if (g.kind & kSegStop) break;
-      wait(&c.qfull[buf], qpar);
-#pragma unroll
-      for (int q = 0; q < C; ++q) o[q] = l[q] = 0.f;
-      run = -3.0e38f;
-      if (lane < C) c.ref[warp][lane] = run;
-      nan_rows = 0;
-      __syncwarp();
-      for (int t = g.ta; t < g.tb; ++t) {
-        const int sb = i & 1;
-        wait(&c.sfull[sb], (i >> 1) & 1);
-        wait(&c.kfull[slot], par);  // (orders this thread's reads of the page scales)
-        tc_fence_after();
-        float x[C];
-        tmem_ld_sum<C>(lane_base + sb * kCols, NT, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.sempty[sb]));
-        const int pi = tok >> p.cache.page_shift, flags = c.flags[slot], pos = t * kAttnTile + tok;
-        const float ks = c.kscale[slot][pi], ve = c.vexp[slot][pi];
-        const bool live = !(flags & 1) || (pos >= g.tlo && pos < g.thi && ve > -INFINITY);
-#pragma unroll
-        for (int q = 0; q < C; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q0 + q], ve + 8.f);  // weights come as 256 p
-        if (__builtin_expect(flags & 2, 0)) {
-#pragma unroll
-          for (int q = 0; q < C; ++q) {
-            const int last = c.qpos[buf][q0 + q];
-            if (!(live && pos <= last && pos > last - p.window)) x[q] = -INFINITY;
-          }
-        } else if (!live) {
-#pragma unroll
-          for (int q = 0; q < C; ++q) x[q] = -INFINITY;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int q = 0; q < C; ++q) top = fmaxf(top, x[q] - c.ref[warp][q]);
-        const bool scaled = any_of_group(top > 8.8f);  // E4M3 ends at 448 = 2^8.8
-        if (__builtin_expect(scaled, 0)) {
-          // R of the columns that are exceeded moves one above the tile's
-          // maximum (room for the next tiles); lane q keeps column q's.
-          top = -INFINITY;
-#pragma unroll
-          for (int q = 0; q < C; ++q) {
-            const float w = warp_max(x[q]);
-            if (lane == q) top = w;
-          }
-          if (lane < C) c.wmax[warp][lane] = top;
-          meet();
-          if (lane < C) {
-            const int w0 = warp & ~3;
-            top = fmaxf(fmaxf(c.wmax[w0][lane], c.wmax[w0 + 1][lane]), fmaxf(c.wmax[w0 + 2][lane], c.wmax[w0 + 3][lane]));
-            const float now = top - run > 8.8f ? ceilf(top) - 7.f : run;
-            c.alpha[warp][sb][lane] = exp2_whole(run - now);
-            c.ref[warp][lane] = run = now;
-          }
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < C; ++q) l[q] *= c.alpha[warp][sb][q];
-        }
-        const float iv = live ? kv_exp2i(-(int)ve) : 0.f;  // the value scale does not count in the sum of weights
-#pragma unroll
-        for (int q = 0; q < C; ++q) {
-          x[q] = ex2(x[q] - c.ref[warp][q]);
-          l[q] = fmaf(x[q], iv, l[q]);
-        }
-        const bool joined = t > g.ta;
-        if (joined) wait(&c.ofull[(i - 1) & 1], ((i - 1) >> 1) & 1);  // the weights before are read
-        if (__builtin_expect(flags, 0)) {
-          wait(&c.vfull[slot], par);
-          const uint32_t vt = ring + (uint32_t)slot * Sh::kStageBytes;
-          // Values of tokens that no row sees must not reach the product
-          // (0 x NaN): their codes become zeros.
-          if (!live && group == 0) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + (uint32_t)(tok * D + k * 16)), "r"(0u) : "memory");
-          }
-          if (flags & 2) {
-            // A NaN value that some rows see and others do not: those that do
-            // get their NaN here, and the code becomes zero.
-            bool nan = false;
-            if (live && group == 0) {
-#pragma unroll
-              for (int k = 0; k < D / 16; ++k) {
-                const uint4 u = lds128(vt + (uint32_t)(tok * D + k * 16));
-                const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) nan |= (((w4[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-              }
-            }
-            const unsigned any = __ballot_sync(0xffffffffu, nan);
-            if (lane == 0 && group == 0) c.nan_tokens[warp] = any;
-            __syncwarp();
-            asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");
-            if ((c.nan_tokens[0] | c.nan_tokens[1] | c.nan_tokens[2] | c.nan_tokens[3]) != 0) {
-              for (int k = 0; k < kAttnTile; ++k) {
-                if (!(c.nan_tokens[k >> 5] >> (k & 31) & 1) || tok >= D) continue;
-                if ((lds8(vt + swizzled<D>(k, tok >> 4) + (tok & 15)) & 0x7F) != 0x7F) continue;
-                for (int q = 0; q < C; ++q) {
-                  const int last = c.qpos[buf][q0 + q], kp = t * kAttnTile + k;
-                  if (kp <= last && kp > last - p.window) nan_rows |= 1u << q;
-                }
-              }
-              __syncwarp();
-              asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");  // all have seen the codes
-              if (nan) {
-                for (int k = 0; k < D; ++k)
-                  if ((lds8(vt + (uint32_t)(tok * D + k)) & 0x7F) == 0x7F) sts8(vt + (uint32_t)(tok * D + k), 0);
-              }
-            }
-            __syncwarp();
-          }
-        }
-        const uint32_t col = (uint32_t)(tok & 15), chunk = tok >> 4;
-#pragma unroll
-        for (int q = 0; q < C; q += 2) {
-          const uint32_t u = split2(x[q], x[q + 1]);
-          // (q0 is a multiple of 8: it does not change the swizzle)
-          sts8(pbuf + q0 * 128 + swizzled<128>(q, chunk) + col, u);
-          sts8(pbuf + q0 * 128 + swizzled<128>(q + 1, chunk) + col, u >> 8);
-          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q, chunk) + col, u >> 16);
-          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q + 1, chunk) + col, u >> 24);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&c.pfull));
-        if (joined) accumulate(i - 1, scaled_before);
-        scaled_before = scaled;
-        ++i;
-        if (++slot == S) {
-          slot = 0;
-          par ^= 1u;
-        }
-      }
-      accumulate(i - 1, scaled_before);
-      // ------------------------------------------------------- the segment's end
-      const float part = warp_column_sums<C>(l);
-      if (lane % (32 / C) == 0) c.wsum[warp][lane / (32 / C)] = part;
-      meet();
-      const bool whole = (g.kind & (kSegStart | kSegEnd)) == (kSegStart | kSegEnd);
-      if (lane < C) {
-        const int w0 = warp & ~3;
-        const float sum = c.wsum[w0][lane] + c.wsum[w0 + 1][lane] + c.wsum[w0 + 2][lane] + c.wsum[w0 + 3][lane];
-        c.ref[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;  // (R is not needed any more)
-        if (!whole && (warp & 3) == 0 && q0 + lane < g.nrows)
-          p.part_ml[(long long)g.slot * NT + q0 + lane] = make_float2(run, sum);
-      }
-      __syncwarp();
-      if (tok < D) {
-#pragma unroll
-        for (int q = 0; q < C; ++q) {
-          const float v = nan_rows >> q & 1 ? __int_as_float(0x7fffffff) : o[q];
-          if (q0 + q < g.nrows) {
-            if (whole)
-              p.out.p[c.qout[buf][q0 + q] + tok] = __float2bfloat16(v * c.ref[warp][q]);
-            else
-              p.part_o[((long long)g.slot * NT + q0 + q) * D + tok] = v;
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.qempty[buf]));
-      if (++buf == Q) {
-        buf = 0;
-        qpar ^= 1u;
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kSoftmax + 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, Sh::kTmemCols);
-  }
 }
 
 // Joins the partial sums of row tiles that span CTAs: block c takes the row

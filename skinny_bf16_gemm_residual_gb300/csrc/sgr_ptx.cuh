@@ -346,12 +346,12 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64
 // Instruction descriptor for kind::f8f6f4 with E4M3 A and B (format 0), FP32
 // D (bits 4-5 = 1), both K-major: N >> 3 at bits 17-22, M >> 4 at 24-28.
 // (An M-major A operand -- element (m, k) of consecutive m next to one another
-// -- sets bit 15.)
+// -- sets bit 15, an N-major B operand bit 16.)
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] . B[smem]^T: the A operand (M = 128 rows x K = 16)
+// D[tmem] (+)= A[tmem] . B[smem]^T (kind::f16, BF16 or FP16 by idesc): the A operand (M = 128 rows x K = 16)
 // read from tensor memory, row i in lane i, two 16-bit elements per 32-bit
 // column (lower K index in the low half), 8 columns from `a_tmem`.
 __device__ __forceinline__ void mma_bf16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,

@@ -194,6 +194,9 @@ ATTEND = [
     (64, 64, 4, 4, [2000], [70], 129),
     (64, 128, 32, 2, [290, 140], [33, 9], 0),
     (128, 32, 40, 1, [400], [2], 1),
+    (128, 16, 24, 1, [900, 200], [30, 200], 0),        # rows in many row tiles, a whole prompt
+    (64, 32, 9, 3, [700, 130, 5], [100, 1, 5], 64),
+    (128, 128, 16, 2, [1300], [17], 1000),
 ]
 
 
@@ -241,30 +244,45 @@ def test_attention_sharp_and_shifted_scores():
     ref.check_attention(got, want, mag, "spike")
 
 
-def test_page_scales_far_apart():
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1.0])
+def test_other_scales(scale):
+    """Negative, zero and unit factors of the scores, few rows and many."""
+    pr = ref.Problem(64, 32, 1, [300], [11], seed=9)
+    q = (0.4 * pr.randn(11, 8, 64)).bfloat16()
+    for heads in (1, 8):
+        x = q[:, :heads].contiguous()
+        want, mag = ref.attention(x, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, scale, 0)
+        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), x.cuda(), scale=scale)
+        ref.check_attention(got, want, mag)
+
+
+@pytest.mark.parametrize("heads", [4, 80])
+def test_page_scales_far_apart(heads):
     """Scales of neighbouring pages that differ by up to 2^40."""
     pr = ref.Problem(128, 16, 1, [100], [1], seed=8)
     for i, f in ((0, (0, -3, 1, -40, 2, 0, 1)), (1, (0, 20, -20, 3, -40, 10, 0))):
         for block, e in enumerate(f):
             pr.scale[i][int(pr.block_table[0, block])] *= 2.0 ** e
-    q = (0.3 * pr.randn(1, 4, 128)).bfloat16()
+    q = (0.3 * pr.randn(1, heads, 128)).bfloat16()
     want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, None, 16, 128 ** -0.5, 0)
     got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), q.cuda())
     ref.check_attention(got, want, mag)
 
 
-def test_nan_reaches_only_rows_that_see_it():
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads", [1, 3, 5, 30])
+def test_nan_reaches_only_rows_that_see_it(dim, heads):
     """A NaN key or value at a position that the later rows see and the
     earlier ones do not; a NaN before every window."""
     for which in (0, 1):
         for window in (0, 20):
-            pr = ref.Problem(128, 32, 1, [150], [6], seed=4 + which)
+            pr = ref.Problem(dim, 32, 1, [150], [6], seed=4 + which)
             at = [147] + ([100, 128] if window else [])
             for t in at:
                 pr.codes[which][int(pr.block_table[0, t // 32]), 0, t % 32, 5] = ref.NAN_CODE
-            q = pr.randn(6, 3, 128).bfloat16()
+            q = pr.randn(6, heads, dim).bfloat16()
             want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32,
-                                      128 ** -0.5, window)
+                                      dim ** -0.5, window)
             got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), window=window).cpu()
             assert torch.equal(got.isnan(), want.isnan())
             ref.check_attention(got, want, mag)
