@@ -273,7 +273,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       report_error(p.err, kErrIndex);
       x.page = -1;
     }
-    x.ks = x.vs = 0.f;
+    x.ks = x.vs = 1.f;
     if (x.page >= 0) {
       const long long at = (long long)x.page * p.cache.scale_stride + x.h;
       x.ks = p.cache.k_scale[at];

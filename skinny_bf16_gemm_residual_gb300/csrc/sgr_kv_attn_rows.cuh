@@ -255,8 +255,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool live = !flags || (tok >= c.live[meta][0] && tok < c.live[meta][1] &&
                                    c.vexp[meta][tok >> p.cache.page_shift] > -INFINITY);
       const uint32_t vt = ring + (uint32_t)slot * kStage, wt = wide + (uint32_t)buf * kWide;
-      uint32_t mask[4] = {0u, 0u, 0u, 0u};
+      bool nans = false;
+      if (flags & 2) {
 #pragma unroll
+        for (int e = 0; e < 4; ++e) c.nan_mask[buf][tok][e] = 0u;
+      }
+#pragma unroll 2
       for (int k = 0; k < D / 16; ++k) {
         uint4 u = lds128(vt + swizzled<D>(tok, k));
         if (!live) u = make_uint4(0u, 0u, 0u, 0u);
@@ -270,13 +274,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           nan |= (w4[e] & 0x7F7F7F7Fu) + 0x01010101u;
         }
         if (__builtin_expect(nan & 0x80808080u, 0)) {
+          uint32_t mask = 0;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if ((w4[e >> 2] >> (8 * (e & 3)) & 0x7F) == 0x7F) {
               const uint32_t at = (e & 1) ? 0xFFFF0000u : 0x0000FFFFu;
               h[e >> 1] = (flags & 2) ? h[e >> 1] & ~at : h[e >> 1] | (at & 0x7FFF7FFFu);
-              mask[k >> 1] |= 1u << ((k & 1) * 16 + e);
+              mask |= 1u << e;
             }
+          if (flags & 2) c.nan_mask[buf][tok][k >> 1] |= mask << ((k & 1) * 16);
+          nans = true;
         }
         // 16 elements: two chunks of the token's row in block k / 4
         const uint32_t at = wt + (uint32_t)(k / 4) * (kAttnTile * 128);
@@ -284,10 +291,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         sts128(at + swizzled<128>(tok, (k & 3) * 2 + 1), h[4], h[5], h[6], h[7]);
       }
       if (flags & 2) {
-        const unsigned any = __ballot_sync(0xffffffffu, (mask[0] | mask[1] | mask[2] | mask[3]) != 0);
+        const unsigned any = __ballot_sync(0xffffffffu, nans);
         if (lane == 0) c.nan_tokens[buf][warp - 8] = any;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c.nan_mask[buf][tok][e] = mask[e];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool real = q < g.nrows;
       const int last = real ? g.first + rtok : -1;  // the row sees positions (last - window, last]
       const int see0 = max(g.tlo, last - p.window + 1), see1 = min(g.thi - 1, last);
-      const float qf = c.qf[q];
+      const float qf = c.qf[q] == 0.f ? 1e-30f : c.qf[q];  // (a masked score, -inf, times zero is not -inf)
       float R = -3.0e38f, l = 0.f;
       unsigned nan_d[4] = {0u, 0u, 0u, 0u};  // elements of the output that saw a NaN value
       for (int t = g.ta; t < g.tb; ++t, ++i, ++mine) {
@@ -369,32 +374,40 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         tc_fence_after();
         const int flags = c.flags[meta], ps = p.cache.page_shift;
         const int c0 = see0 - t * kAttnTile, cn = see1 - t * kAttnTile - c0;  // columns that the row sees: c0 .. c0 + cn
-        uint32_t x[2][32];
+        // The loops over a tile's columns stay rolled: unrolled, the body does
+        // not fit the instruction caches, and the warps of four roles then
+        // wait for instructions most of the time (236 against ROLLED_US us).
+        uint32_t x[32];
+        if (__builtin_expect(flags, 0)) {  // what the row does not see: no score
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            tmem_ld32(s_cols + 32 * k, x);
+            tmem_wait_ld32(x);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const bool there = cn >= 0 && c.vexp[meta][(32 * k + 16 * h) >> ps] > -INFINITY;
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                w[e] = there && (unsigned)(32 * k + 16 * h + e - c0) <= (unsigned)cn ? x[16 * h + e] : 0xFF800000u;
+              tmem_st16(s_cols + 32 * k + 16 * h, w);
+            }
+          }
+          tmem_wait_st();
+        }
         // The tile's maximum, in units of the weights' exponent.
         float top = -INFINITY;
-        tmem_ld32(s_cols, x[0]);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          uint32_t(&y)[32] = x[k & 1];
-          tmem_wait_ld32(y);
-          if (k < 3) tmem_ld32(s_cols + 32 * (k + 1), x[(k + 1) & 1]);
+          tmem_ld32(s_cols + 32 * k, x);
+          tmem_wait_ld32(x);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (32 * k + 16 * h) >> ps;
-            const float kq = c.kscale[meta][pi] * qf, add = c.vexp[meta][pi];
-            if (__builtin_expect(flags, 0)) {
+            float m[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int col = 32 * k + 16 * h + e;
-                const float z = fmaf(__uint_as_float(y[16 * h + e]), kq, add);
-                if (cn >= 0 && (unsigned)(col - c0) <= (unsigned)cn && add > -INFINITY) top = fmaxf(top, z);
-              }
-            } else {
-              float m = __uint_as_float(y[16 * h]);
-#pragma unroll
-              for (int e = 1; e < 16; ++e) m = fmaxf(m, __uint_as_float(y[16 * h + e]));
-              top = fmaxf(top, fmaf(m, kq, add));
-            }
+            for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(x[16 * h + e]));
+            top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), c.kscale[meta][pi] * qf, c.vexp[meta][pi]));
           }
         }
         const bool move = top - R > 7.5f;  // (weights are 256 p: FP16 ends below 2^16)
@@ -403,15 +416,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           R = now;
           l *= a;
           if (t > g.ta) {  // (the product before is done: its weights' place has new scores)
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
-              tmem_ld32(o_cols + 32 * k, x[0]);
-              tmem_wait_ld32(x[0]);
+              tmem_ld32(o_cols + 32 * k, x);
+              tmem_wait_ld32(x);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 uint32_t w[16];
 #pragma unroll
-                for (int f = 0; f < 16; ++f) w[f] = __float_as_uint(__uint_as_float(x[0][16 * e + f]) * a);
+                for (int f = 0; f < 16; ++f) w[f] = __float_as_uint(__uint_as_float(x[16 * e + f]) * a);
                 tmem_st16(o_cols + 32 * k + 16 * e, w);
               }
             }
@@ -419,46 +432,37 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         // Weights, 256 p in FP16, over the scores' columns [0, 64): a chunk's
         // lie where scores were that are read already.
-        tmem_ld32(s_cols, x[0]);
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          uint32_t(&y)[32] = x[k & 1];
-          tmem_wait_ld32(y);
-          if (k < 3) tmem_ld32(s_cols + 32 * (k + 1), x[(k + 1) & 1]);
+          tmem_ld32(s_cols + 32 * k, x);
+          tmem_wait_ld32(x);
           uint32_t w[16];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (32 * k + 16 * h) >> ps;
             const float ve = c.vexp[meta][pi], kq = c.kscale[meta][pi] * qf, add = (ve + 8.f) - R;
-            float z[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) z[e] = fmaf(__uint_as_float(y[16 * h + e]), kq, add);
-            if (__builtin_expect(flags, 0)) {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int col = 32 * k + 16 * h + e;
-                if (!(cn >= 0 && (unsigned)(col - c0) <= (unsigned)cn && add > -INFINITY)) z[e] = -INFINITY;
-              }
-            }
             float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              z[e] = ex2(z[e]);
-              sum[e & 1] += z[e];
+            for (int e = 0; e < 8; ++e) {
+              const float z0 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e]), kq, add));
+              const float z1 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e + 1]), kq, add));
+              sum[0] += z0, sum[1] += z1;
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[8 * h + e]) : "f"(z1), "f"(z0));
             }
             l = fmaf(sum[0] + sum[1], ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f, l);  // without the value scale
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[8 * h + e]) : "f"(z[2 * e + 1]), "f"(z[2 * e]));
           }
           tmem_st16(s_cols + 16 * k, w);
         }
         tmem_wait_st();
         if (__builtin_expect(flags & 2, 0)) {
           wait(&c.wfull[i & 1], (i >> 1) & 1);
-          for (int k = 0; k < kAttnTile; ++k)
-            if ((c.nan_tokens[i & 1][k >> 5] >> (k & 31) & 1) && (unsigned)(k - c0) <= (unsigned)cn && cn >= 0)
+          for (int m = 0; m < 4; ++m)
+            for (unsigned left = c.nan_tokens[i & 1][m]; left; left &= left - 1) {
+              const int k = 32 * m + __ffs(left) - 1;
+              if (cn < 0 || (unsigned)(k - c0) > (unsigned)cn) continue;
+#pragma unroll
               for (int e = 0; e < 4; ++e) nan_d[e] |= c.nan_mask[i & 1][k][e];
+            }
         }
         tc_fence_before();
         __syncwarp();
@@ -472,15 +476,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int head = g.h * p.group + r - rtok * p.group;
       __nv_bfloat16* out = p.out.p + (long long)(g.row0 + rtok) * p.out.ts + (long long)head * p.out.hs;
       float* part = p.part_o + ((long long)g.slot * NT + q) * D;
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < D / 32; ++k) {
         uint32_t x[32];
         tmem_ld32(o_cols + 32 * k, x);
         tmem_wait_ld32(x);
-        if (__builtin_expect(nan_d[k] != 0, 0)) {
+        const unsigned nan = k == 0 ? nan_d[0] : k == 1 ? nan_d[1] : k == 2 ? nan_d[2] : nan_d[3];
+        if (__builtin_expect(nan != 0, 0)) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (nan_d[k] >> e & 1) x[e] = 0x7fffffffu;
+            if (nan >> e & 1) x[e] = 0x7fffffffu;
         }
         if (real && whole) {
 #pragma unroll
