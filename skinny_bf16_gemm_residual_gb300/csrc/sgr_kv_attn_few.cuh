@@ -32,9 +32,8 @@
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile.
 //
-// Roles (two CTAs an SM): 4 or 8 softmax warps (thread = token, then = element
-// d; with 8, two groups of 4 take half of the columns each), one warp that
-// walks the work, loads pages by TMA and hands out segments, one that issues
+// Roles (two CTAs an SM, one with 32 rows): a group of 4 softmax warps for every
+// 8 rows (thread = token, then = element d), one warp that walks the work, loads pages by TMA and hands out segments, one that issues
 // the MMAs, two that bring the next segments' queries into the operand.
 #pragma once
 
@@ -44,15 +43,16 @@ namespace sgr {
 
 template <int D, int NT>
 struct AttnShape {
-  static constexpr int kGroups = NT == 8 ? 1 : 2;  // of 4 softmax warps
-  static constexpr int kC = NT / kGroups;          // columns a softmax thread
-  static constexpr int kSoftmax = 4 * kGroups;     // warps
+  static constexpr int kC = 8;             // columns a softmax thread
+  static constexpr int kGroups = NT / kC;  // of 4 softmax warps
+  static constexpr int kSoftmax = 4 * kGroups;
   static constexpr int kThreads = 32 * (kSoftmax + 4);
+  static constexpr int kCtas = NT == 32 ? 1 : 2;  // an SM
   static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
-  // As many stages and query buffers as two CTAs an SM allow.
-  static constexpr int kStages = D == 128 ? (NT <= 16 ? 3 : 2) : (NT == 8 ? 6 : NT == 16 ? 5 : 4);
+  // As many stages and query buffers as kCtas an SM allow.
+  static constexpr int kStages = D == 128 ? (NT == 32 ? 5 : 3) : (NT == 32 ? 8 : NT == 16 ? 5 : 6);
   static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : 4;
   static constexpr int kPBytes = kCols * kAttnTile;
   static constexpr int kQBytes = kCols * D;
@@ -69,7 +69,7 @@ struct AttnCtl {
   uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
   uint32_t tmem;
   int abort;
-  int go[2][2];
+  int go[Sh::kGroups][2];
   unsigned nan_tokens[4];
   AttnSeg seg[kAttnQueue];
   float kscale[S][8], vexp[S][8];  // of a stage's pages
@@ -134,22 +134,15 @@ __device__ __forceinline__ uint32_t split2(float a, float b) {
 // `apart` columns on.
 template <int C>
 __device__ __forceinline__ void tmem_ld_sum(uint32_t hi, uint32_t apart, float (&x)[C]) {
-  if constexpr (C == 8) {
-    float v[8], w[8];
-    tmem_ld8x2(hi, hi + apart, v, w);
+  static_assert(C == 8, "the load of two runs of 8 columns");
+  float v[8], w[8];
+  tmem_ld8x2(hi, hi + apart, v, w);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = fmaf(w[q], kLoScale, v[q]);
-  } else {
-    float v[16];
-    tmem_ld16(hi, x);
-    tmem_ld16(hi + apart, v);
-#pragma unroll
-    for (int q = 0; q < 16; ++q) x[q] = fmaf(v[q], kLoScale, x[q]);
-  }
+  for (int q = 0; q < 8; ++q) x[q] = fmaf(w[q], kLoScale, v[q]);
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
+__global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::kCtas)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Sh = AttnShape<D, NT>;
   constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC, kCols = Sh::kCols, kSoftmax = Sh::kSoftmax;
@@ -362,26 +355,16 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
     const int group = warp >> 2, tok = tid & 127, q0 = group * C;  // columns q0 .. q0 + C - 1
     auto meet = [&] {  // the group's 4 warps
       __syncwarp();
-      if (Sh::kGroups == 1 || group == 0)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      else
-        asm volatile("bar.sync 2, 128;" ::: "memory");
+      named_bar_sync(1 + group, 128);
     };
     auto any_of_group = [&](bool x) {  // of its 128 threads
       uint32_t any;
       __syncwarp();
-      if (Sh::kGroups == 1 || group == 0)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(any)
-            : "r"((uint32_t)x)
-            : "memory");
-      else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(any)
-            : "r"((uint32_t)x)
-            : "memory");
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(any)
+          : "r"((uint32_t)x), "r"(1 + group)
+          : "memory");
       return any != 0;
     };
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)q0;  // tensor-memory lanes of this warp
@@ -513,7 +496,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
             const unsigned any = __ballot_sync(0xffffffffu, nan);
             if (lane == 0 && group == 0) c.nan_tokens[warp] = any;
             __syncwarp();
-            asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");
+            named_bar_sync(1 + Sh::kGroups, 32 * kSoftmax);
             if ((c.nan_tokens[0] | c.nan_tokens[1] | c.nan_tokens[2] | c.nan_tokens[3]) != 0) {
               for (int k = 0; k < kAttnTile; ++k) {
                 if (!(c.nan_tokens[k >> 5] >> (k & 31) & 1) || tok >= D) continue;
@@ -524,7 +507,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, 2)
                 }
               }
               __syncwarp();
-              asm volatile("bar.sync 3, %0;" ::"n"(32 * kSoftmax) : "memory");  // all have seen the codes
+              named_bar_sync(1 + Sh::kGroups, 32 * kSoftmax);  // all have seen the codes
               if (nan) {
                 for (int k = 0; k < D; ++k)
                   if ((lds8(vt + (uint32_t)(tok * D + k)) & 0x7F) == 0x7F) sts8(vt + (uint32_t)(tok * D + k), 0);
