@@ -24,14 +24,8 @@
 namespace sgr {
 
 constexpr int kAttnTile = 128;  // tokens
-#ifndef NAP_W
-#define NAP_W 64
-#define NAP_Q 64
-#define NAP_M 20
-#define NAP_S 0
-#endif
 constexpr int kAttnQueue = 8;   // segments handed out ahead
-constexpr int kNapWalk = NAP_W, kNapQuery = NAP_Q, kNapMma = NAP_M, kNapSoftmax = NAP_S;
+constexpr int kNap = 64;        // nanoseconds between the polls of roles that mostly wait
 
 // A run of tiles [ta, tb) of one row tile, the unit that the roles work by.
 enum : int { kSegStart = 1, kSegEnd = 2, kSegStop = 4 };
@@ -173,7 +167,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   if (u < u1) it = attn_item<NT>(p, s, j);
   int t = 0, t_end = 0;  // tiles of the segment handed out last
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_wait_nap<kNapWalk>(smem_u32(bar), parity, abort_flag)) {
+    if (ok && !mbar_wait_nap<kNap>(smem_u32(bar), parity, abort_flag)) {
       if (!*abort_flag) report_error(p.err, kErrWaitEmpty);
       *abort_flag = 1;
       ok = false;
@@ -192,7 +186,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   };
   struct Tile {
     int h, flags;
-  int live0, live1;  // its tokens that some row sees
+    int live0, live1;  // its tokens that some row sees
     int page;  // this lane's table entry, -1 = none
     float ks, vs;
   };
@@ -254,8 +248,8 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
     ++t;
     x.h = cur_h;
-  x.live0 = max(cur.tlo - x0, 0);
-  x.live1 = min(cur.thi - x0, kAttnTile);
+    x.live0 = max(cur.tlo - x0, 0);
+    x.live1 = min(cur.thi - x0, kAttnTile);
     x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
     if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
     // This lane's page of the tile, where some row sees a position of it.
