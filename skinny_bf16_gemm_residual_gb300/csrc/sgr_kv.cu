@@ -435,7 +435,7 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
   const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
   a.split = tiles > kWholeTiles;
-  const long long units = c.heads * row_tiles * (a.split ? tiles : 1);
+  const long long units = c.heads * row_tiles * (a.split ? tiles + 1 : 1);
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms;  // resident: one or two an SM
   a.grid = (int)(units < ctas ? units : ctas);

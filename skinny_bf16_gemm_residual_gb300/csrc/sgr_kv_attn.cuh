@@ -5,8 +5,9 @@
 // The unit of work is a row tile (up to NT query rows that share a key/value
 // head: the head's query group, times the new tokens of a sequence) against a
 // 128-token tile of the cache.  Every CTA takes the same number of units of
-// all sequences and heads, in order, whatever the lengths; a row tile that
-// spans CTAs leaves partial sums (o, R, l) in the workspace and a second kernel
+// all sequences and heads, in order, whatever the lengths (and one more unit
+// for each row tile, which is what its beginning and end cost: without it CTAs
+// with many short sequences finish last); a row tile that spans CTAs leaves partial sums (o, R, l) in the workspace and a second kernel
 // joins them in order (the same bits on every run).  For short caches
 // (`whole`) a row tile is one unit and nothing is joined.
 //
@@ -85,7 +86,7 @@ __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, const KvSeq& 
   it.tlo = p.window > p0 ? 0 : p0 - p.window + 1;
   it.ta = it.thi > 0 ? it.tlo / kAttnTile : 0;
   it.tb = (it.thi + kAttnTile - 1) / kAttnTile;
-  it.units = p.whole ? 1 : max(it.tb - it.ta, 1);
+  it.units = p.whole || it.tb <= it.ta ? 1 : it.tb - it.ta + 1;  // the first for its beginning and end
   return it;
 }
 
@@ -220,21 +221,22 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
         continue;
       }
       AttnSeg g;
-      g.kind = (skip == 0 ? kSegStart : 0) | (skip + take == units ? kSegEnd : 0);
+      g.ta = p.whole ? it.ta : it.ta + max(skip - 1, 0);
+      g.tb = p.whole ? it.tb : it.ta + skip + take - 1;
+      if (g.tb <= g.ta) continue;  // the share ends with the first unit: no tile
+      g.kind = (g.ta == it.ta ? kSegStart : 0) | (skip + take == units ? kSegEnd : 0);
       g.h = h;
       g.row0 = s.row0;
       g.r0 = it.r0;
       g.nrows = it.nrows;
       g.first = s.len - s.n;
-      g.ta = it.ta + skip;
-      g.tb = p.whole ? it.tb : g.ta + take;
       g.tlo = it.tlo;
       g.thi = it.thi;
-      g.slot = 2 * (int)blockIdx.x + (skip == 0 ? 1 : 0);
+      g.slot = 2 * (int)blockIdx.x + (g.kind & kSegStart ? 1 : 0);
       g.pad = 0;
       hand_out(g);
       if (!ok) return false;
-      if (g.kind == kSegStart) piece = {cta_of(u + units - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
+      if (g.kind == kSegStart) piece = {cta_of(u + units - skip - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
       t = g.ta;
       t_end = g.tb;
       cur = it;
