@@ -383,25 +383,29 @@ using JoinFn = void (*)(const sgr::AttnParams);
 struct AttnKernel {
   AttnFn fn;
   JoinFn join;
-  int smem, threads;
+  int smem, threads, join_rows;
 };
 
 template <int D, int NT>
 AttnKernel attn_kernel_of() {
   return {sgr::kv_attn_kernel<D, NT>, sgr::kv_attn_join_kernel<D, NT>, sgr::attn_smem_bytes<D, NT>(),
-          sgr::AttnShape<D, NT>::kThreads};
+          sgr::AttnShape<D, NT>::kThreads, sgr::JoinShape<NT>::kRows};
 }
 
 template <int D>
 AttnKernel attn_rows_kernel_of() {
   return {sgr::kv_attn_rows_kernel<D>, sgr::kv_attn_join_kernel<D, sgr::kRowsNT>, sgr::rows_attn_smem_bytes<D>(),
-          sgr::kRowsThreads};
+          sgr::kRowsThreads, sgr::JoinShape<sgr::kRowsNT>::kRows};
+}
+
+template <int D>
+AttnKernel attn_few_kernel(int nt) {
+  return nt == 8 ? attn_kernel_of<D, 8>() : nt == 16 ? attn_kernel_of<D, 16>() : nt == 24 ? attn_kernel_of<D, 24>() : attn_kernel_of<D, 32>();
 }
 
 AttnKernel attn_kernel(int dim, int nt) {
   if (nt == sgr::kRowsNT) return dim == 64 ? attn_rows_kernel_of<64>() : attn_rows_kernel_of<128>();
-  if (dim == 64) return nt == 8 ? attn_kernel_of<64, 8>() : nt == 16 ? attn_kernel_of<64, 16>() : attn_kernel_of<64, 32>();
-  return nt == 8 ? attn_kernel_of<128, 8>() : nt == 16 ? attn_kernel_of<128, 16>() : attn_kernel_of<128, 32>();
+  return dim == 64 ? attn_few_kernel<64>(nt) : attn_few_kernel<128>(nt);
 }
 
 // Caches of at most this many tiles a sequence are not split over CTAs: the
@@ -431,13 +435,13 @@ struct AttnPlan {
 AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
-  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows < kManyRows ? 32 : sgr::kRowsNT;
+  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows < kManyRows ? 32 : sgr::kRowsNT;
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
   const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
   a.split = tiles > kWholeTiles;
   const long long units = c.heads * row_tiles * (a.split ? tiles + 1 : 1);
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
-  const long long ctas = a.nt >= 32 ? sms : 2LL * sms;  // resident: one or two an SM
+  const long long ctas = a.nt >= 24 ? sms : 2LL * sms;  // resident: one or two an SM
   a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
   a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
@@ -492,7 +496,7 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   const AttnKernel k = attn_kernel(c->head_dim, a.nt);
   rc = launch(k.fn, dim3(a.grid), k.threads, k.smem, flags, stream, tk, tv, p);
   if (rc != SGR_OK || !a.split) return rc;
-  return launch(k.join, dim3(a.grid, a.nt / 8), sgr::kJoinThreads, 0, flags, stream, p);
+  return launch(k.join, dim3(a.grid, a.nt / k.join_rows), sgr::kJoinThreads, 0, flags, stream, p);
 }
 
 }  // namespace
@@ -514,7 +518,7 @@ int kv_init_device(int dev) {
     }
     bool ok = true;
     for (int dim : {64, 128})
-      for (int nt : {8, 16, 32, sgr::kRowsNT})
+      for (int nt : {8, 16, 24, 32, sgr::kRowsNT})
         ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(attn_kernel(dim, nt).fn)) == cudaSuccess;
     if (prev != dev) cudaSetDevice(prev);
     if (ok)

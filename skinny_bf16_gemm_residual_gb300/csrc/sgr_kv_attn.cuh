@@ -410,48 +410,87 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   return v;
 }
 
-// Joins the partial sums of row tiles that span CTAs: block c takes the row
-// tile that begins in CTA c and ends in a later one, if any, a warp a row; its
-// pieces are those of CTAs c, c + 1, ..., last.
+// Joins the partial sums of row tiles that span CTAs: blocks x = c take the row
+// tile that begins in CTA c and ends in a later one, if any; its pieces are
+// those of CTAs c, c + 1, ..., last.  A row is joined by kParts warps, each
+// taking every kParts-th run of 8 pieces with all its reads under way at once
+// (one memory round trip for the owner, one for the pieces: few long sequences
+// have tens of pieces a row), in a fixed order.
 constexpr int kJoinThreads = 256;
+
+template <int NT>
+struct JoinShape {
+  static constexpr int kParts = NT <= 16 ? 4 : 1;  // warps a row
+  static constexpr int kRows = kJoinThreads / 32 / kParts;
+};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnParams p) {
-  constexpr int kE = D / 32;  // elements a lane
+  constexpr int kE = D / 32, kParts = JoinShape<NT>::kParts, kRows = JoinShape<NT>::kRows;  // kE: elements a lane
+  __shared__ float part_o[kRows][kParts][D];
+  __shared__ float2 part_ml[kRows][kParts];
   pdl_launch_dependents();
   pdl_wait();
   const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = blockIdx.y * (kJoinThreads / 32) + warp;
+  const int row = warp / kParts, part = warp % kParts, q = blockIdx.y * kRows + row;
   const AttnPiece own = p.pieces[c0];
-  if (own.last <= c0 || q >= own.nrows) return;
+  if (own.last <= c0 || q >= own.nrows) return;  // (all warps of the row)
   const int n = own.last - c0 + 1;
   auto slot = [&](int k) { return (long long)(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * NT + q; };
   float m = -3.0e38f, sum = 0.f, o[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 32) {  // lane k: factor of piece k0 + k
-    float2 ml = make_float2(-3.0e38f, 0.f);
-    if (k0 + lane < n) ml = p.part_ml[slot(k0 + lane)];
-    const float now = fmaxf(m, warp_max(ml.x)), f = exp2_whole(ml.x - now), old = exp2_whole(m - now);
-    float w = ml.y * f;
+  for (int k0 = 8 * part; k0 < n; k0 += 8 * kParts) {
+    float v[8][kE];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-    sum = sum * old + w;
+    for (int k = 0; k < 8; ++k) {
+      const float* at = p.part_o + slot(min(k0 + k, n - 1)) * D + lane * kE;
+      if constexpr (kE == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(at);
+        v[k][0] = u.x, v[k][1] = u.y, v[k][2] = u.z, v[k][3] = u.w;
+      } else {
+        const float2 u = *reinterpret_cast<const float2*>(at);
+        v[k][0] = u.x, v[k][1] = u.y;
+      }
+    }
+    float2 ml = make_float2(-3.0e38f, 0.f);  // lane k: of piece k0 + k
+    if (lane < 8 && k0 + lane < n) ml = p.part_ml[slot(k0 + lane)];
+    const float now = fmaxf(m, warp_max(ml.x)), old = exp2_whole(m - now);
+    const float f = lane < 8 && k0 + lane < n ? exp2_whole(ml.x - now) : 0.f;
     m = now;
+    sum *= old;
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] *= old;
-    const int kn = min(32, n - k0);
-#pragma unroll 8
-    for (int k = 0; k < kn; ++k) {
+    const float w = ml.y * f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k0 + k >= n) break;
       const float fk = __shfl_sync(0xffffffffu, f, k);
-      const float* v = p.part_o + slot(k0 + k) * D + lane * kE;
-      if constexpr (kE == 4) {
-        const float4 u = *reinterpret_cast<const float4*>(v);
-        o[0] = fmaf(u.x, fk, o[0]), o[1] = fmaf(u.y, fk, o[1]), o[2] = fmaf(u.z, fk, o[2]), o[3] = fmaf(u.w, fk, o[3]);
-      } else {
-        const float2 u = *reinterpret_cast<const float2*>(v);
-        o[0] = fmaf(u.x, fk, o[0]), o[1] = fmaf(u.y, fk, o[1]);
-      }
+      sum += __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] = fmaf(v[k][e], fk, o[e]);
+    }
+  }
+  if constexpr (kParts > 1) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) part_o[row][part][lane * kE + e] = o[e];
+    if (lane == 0) part_ml[row][part] = make_float2(m, sum);
+    __syncwarp();
+    named_bar_sync(1 + row, 32 * kParts);
+    if (part > 0) return;
+    float all = m;
+#pragma unroll
+    for (int k = 1; k < kParts; ++k) all = fmaxf(all, part_ml[row][k].x);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      if (8 * k >= n) break;  // (a part without pieces)
+      const float f = exp2_whole(part_ml[row][k].x - all);
+      sum = fmaf(part_ml[row][k].y, f, sum);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] = fmaf(part_o[row][k][lane * kE + e], f, o[e]);
     }
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;

@@ -3,7 +3,7 @@
 //
 //     o = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q.k_t)
 //
-// Per row tile (NT = 8, 16 or 32 rows) and 128-token tile of the cache:
+// Per row tile (NT = 8, 16, 24 or 32 rows) and 128-token tile of the cache:
 //
 //     S^T [128 tokens, NT] = K Q^T      codes of K as they are in the cache
 //     P^T = 2^(S' - m)                  one thread per token
@@ -32,7 +32,7 @@
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile.
 //
-// Roles (two CTAs an SM, one with 32 rows): a group of 4 softmax warps for every
+// Roles (two CTAs an SM, one with 24 and 32 rows): a group of 4 softmax warps for every
 // 8 rows (thread = token, then = element d), one warp that walks the work, loads pages by TMA and hands out segments, one that issues
 // the MMAs, two that bring the next segments' queries into the operand.
 #pragma once
@@ -47,16 +47,16 @@ struct AttnShape {
   static constexpr int kGroups = NT / kC;  // of 4 softmax warps
   static constexpr int kSoftmax = 4 * kGroups;
   static constexpr int kThreads = 32 * (kSoftmax + 4);
-  static constexpr int kCtas = NT == 32 ? 1 : 2;  // an SM
+  static constexpr int kCtas = NT >= 24 ? 1 : 2;  // an SM
   static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
   // As many stages and query buffers as kCtas an SM allow.
-  static constexpr int kStages = D == 128 ? (NT == 32 ? 5 : 3) : (NT == 32 ? 8 : NT == 16 ? 5 : 6);
-  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : 4;
+  static constexpr int kStages = D == 128 ? (NT >= 24 ? 5 : 3) : (NT >= 24 ? 8 : NT == 16 ? 5 : 6);
+  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT >= 24 ? 3 : 4;
   static constexpr int kPBytes = kCols * kAttnTile;
   static constexpr int kQBytes = kCols * D;
-  static constexpr int kTmemCols = 4 * kCols;  // S and O, two each
+  static constexpr int kTmemCols = NT == 24 ? 256 : 4 * kCols;  // S and O, two each (a power of two)
 };
 
 template <int D, int NT>

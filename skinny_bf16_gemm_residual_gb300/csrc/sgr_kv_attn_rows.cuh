@@ -20,7 +20,7 @@
 // down to 2^-22 of the largest.
 //
 // A row's statistics stay in its thread: R, a whole number, is the first
-// tile's maximum rounded up and moves when a score exceeds it by more than
+// 32 scores' maximum rounded up and moves when a score exceeds it by more than
 // FP16 holds (2^7.5 times); then the sum and the row's accumulator (in tensor
 // memory) are rescaled by a power of two.  The weights overwrite the scores'
 // columns.
@@ -107,6 +107,12 @@ __device__ __forceinline__ uint32_t widen2(uint32_t x) {
   asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(x), "n"(SEL));  // codes in the low bytes, signs above
   t = (t << 7) & 0xBF80BF80u;                                   // the value times 2^-8
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x5C005C00u));  // 0x5C00 = 256
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -366,7 +372,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const int last = real ? g.first + rtok : -1;  // the row sees positions (last - window, last]
       const int see0 = max(g.tlo, last - p.window + 1), see1 = min(g.thi - 1, last);
       const float qf = c.qf[q] == 0.f ? 1e-30f : c.qf[q];  // (a masked score, -inf, times zero is not -inf)
-      float R = -3.0e38f, l = 0.f;
+      float R = 0.f, l = 0.f;
+      bool unset = true;  // whether the row has seen no position yet: R is its first maximum
       unsigned nan_d[4] = {0u, 0u, 0u, 0u};  // elements of the output that saw a NaN value
       for (int t = g.ta; t < g.tb; ++t, ++i, ++mine) {
         const int meta = i % M;
@@ -395,61 +402,71 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
           tmem_wait_st();
         }
-        // The tile's maximum, in units of the weights' exponent.
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          tmem_ld32(s_cols + 32 * k, x);
-          tmem_wait_ld32(x);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int pi = (32 * k + 16 * h) >> ps;
-            float m[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
-#pragma unroll
-            for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(x[16 * h + e]));
-            top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), c.kscale[meta][pi] * qf, c.vexp[meta][pi]));
-          }
-        }
-        const bool move = top - R > 7.5f;  // (weights are 256 p: FP16 ends below 2^16)
-        if (__any_sync(0xffffffffu, move)) {
-          const float now = move ? ceilf(top) : R, a = exp2_whole(R - now);
-          R = now;
-          l *= a;
-          if (t > g.ta) {  // (the product before is done: its weights' place has new scores)
-#pragma unroll 1
-            for (int k = 0; k < D / 32; ++k) {
-              tmem_ld32(o_cols + 32 * k, x);
-              tmem_wait_ld32(x);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t w[16];
-#pragma unroll
-                for (int f = 0; f < 16; ++f) w[f] = __float_as_uint(__uint_as_float(x[16 * e + f]) * a);
-                tmem_st16(o_cols + 32 * k + 16 * e, w);
-              }
-            }
-          }
-        }
         // Weights, 256 p in FP16, over the scores' columns [0, 64): a chunk's
-        // lie where scores were that are read already.
+        // lie where scores were that are read already.  Where a chunk exceeds
+        // what FP16 holds, R moves, and what was written is rescaled.
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           tmem_ld32(s_cols + 32 * k, x);
           tmem_wait_ld32(x);
-          uint32_t w[16];
+          float z[32];
+          float iv[2];  // the value scales do not count in the sum of weights
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (32 * k + 16 * h) >> ps;
             const float ve = c.vexp[meta][pi], kq = c.kscale[meta][pi] * qf, add = (ve + 8.f) - R;
+            iv[h] = ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              z[16 * h + e] = fmaf(__uint_as_float(x[16 * h + e]), kq, add);
+              top[h] = fmaxf(top[h], z[16 * h + e]);
+            }
+          }
+          const float most = fmaxf(top[0], top[1]);
+          const bool move = most > (unset ? -3.0e38f : 15.5f);
+          if (__any_sync(0xffffffffu, move)) {
+            const float up = move ? ceilf(most - 8.f) : 0.f, a = move && !unset ? exp2_whole(-up) : 1.f;
+            unset = unset && !move;
+            R += up;
+            l *= a;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) z[e] -= up;
+            // The product before is done: its weights' place has new scores.
+            if (t > g.ta) {
+#pragma unroll 1
+              for (int n = 0; n < D / 16; ++n) {
+                float y[16];
+                uint32_t w[16];
+                tmem_ld16(o_cols + 16 * n, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * a);
+                tmem_st16(o_cols + 16 * n, w);
+              }
+            }
+#pragma unroll 1
+            for (int n = 0; n < k; ++n) {
+              float y[16];
+              uint32_t w[16];
+              tmem_ld16(s_cols + 16 * n, y);
+              const uint32_t aa = pack_f16(a, a);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(__float_as_uint(y[e])), "r"(aa));
+              tmem_st16(s_cols + 16 * n, w);
+            }
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float z0 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e]), kq, add));
-              const float z1 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e + 1]), kq, add));
+              const float z0 = ex2(z[16 * h + 2 * e]), z1 = ex2(z[16 * h + 2 * e + 1]);
               sum[0] += z0, sum[1] += z1;
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[8 * h + e]) : "f"(z1), "f"(z0));
+              w[8 * h + e] = pack_f16(z0, z1);
             }
-            l = fmaf(sum[0] + sum[1], ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f, l);  // without the value scale
+            l = fmaf(sum[0] + sum[1], iv[h], l);
           }
           tmem_st16(s_cols + 16 * k, w);
         }
