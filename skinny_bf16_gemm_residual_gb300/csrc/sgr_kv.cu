@@ -441,7 +441,7 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   a.split = tiles > kWholeTiles;
   const long long units = c.heads * row_tiles * (a.split ? tiles + 1 : 1);
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
-  const long long ctas = a.nt >= 24 ? sms : 2LL * sms;  // resident: one or two an SM
+  const long long ctas = a.nt >= 32 ? sms : 2LL * sms;  // resident: one or two an SM
   a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
   a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));

@@ -47,13 +47,13 @@ struct AttnShape {
   static constexpr int kGroups = NT / kC;  // of 4 softmax warps
   static constexpr int kSoftmax = 4 * kGroups;
   static constexpr int kThreads = 32 * (kSoftmax + 4);
-  static constexpr int kCtas = NT >= 24 ? 1 : 2;  // an SM
+  static constexpr int kCtas = NT > 24 ? 1 : 2;  // an SM
   static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
   // As many stages and query buffers as kCtas an SM allow.
-  static constexpr int kStages = D == 128 ? (NT >= 24 ? 5 : 3) : (NT >= 24 ? 8 : NT == 16 ? 5 : 6);
-  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT >= 24 ? 3 : 4;
+  static constexpr int kStages = D == 128 ? (NT == 32 ? 5 : NT == 24 ? 2 : 3) : (NT == 32 ? 8 : NT == 8 ? 6 : 5);
+  static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : D == 64 && NT == 24 ? 2 : 4;
   static constexpr int kPBytes = kCols * kAttnTile;
   static constexpr int kQBytes = kCols * D;
   static constexpr int kTmemCols = NT == 24 ? 256 : 4 * kCols;  // S and O, two each (a power of two)
