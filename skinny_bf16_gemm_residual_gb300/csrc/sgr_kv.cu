@@ -408,19 +408,6 @@ AttnKernel attn_kernel(int dim, int nt) {
   return dim == 64 ? attn_few_kernel<64>(nt) : attn_few_kernel<128>(nt);
 }
 
-// Caches of at most this many tiles a sequence are not split over CTAs: the
-// second launch that joins costs more than the tiles' time in turn.
-#ifndef SGR_KV_WHOLE_TILES
-#define SGR_KV_WHOLE_TILES 4
-#endif
-constexpr int kWholeTiles = SGR_KV_WHOLE_TILES;
-
-// Rows of a sequence and key/value head from which the 128-row kernel is taken.
-#ifndef SGR_KV_MANY_ROWS
-#define SGR_KV_MANY_ROWS 65
-#endif
-constexpr int kManyRows = SGR_KV_MANY_ROWS;
-
 struct AttnPlan {
   int nt;           // rows of a row tile
   int grid;
@@ -430,18 +417,35 @@ struct AttnPlan {
   int64_t bytes;    // workspace
 };
 
-// Row tiles as small as the rows of a sequence allow: the small operands and
-// accumulators are 2 nt columns wide, and so is the softmax work a tile.
 AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
-  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows < kManyRows ? 32 : sgr::kRowsNT;
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
-  const long long row_tiles = (long long)b.tokens * group / a.nt + b.batch;
-  a.split = tiles > kWholeTiles;
-  const long long units = c.heads * row_tiles * (a.split ? tiles + 1 : 1);
+  auto row_tiles = [&](int nt) {  // at most
+    const long long each = b.batch * ((rows + nt - 1) / nt), all = (long long)b.tokens * group / nt + b.batch;
+    return c.heads * (each < all ? each : all);
+  };
+  // Row tiles as small as the rows of a sequence allow: the small operands and
+  // accumulators are 2 nt columns wide, and so is the softmax work a tile
+  // (five drafted tokens and four heads a key/value head: 29.6 us in a tile of
+  // 24 against 34.0 in one of 32).
+  a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
+  // The 256-row kernel takes some 2.2 times a 32-row unit's time for eight
+  // times the rows, but 12 units' time to begin and end.  Measured, 32 rows
+  // against 256, over contexts of up to 3000: 19.5 and 21.3 us (4 sequences,
+  // 126 rows), 65.8 and 39.5 us (16 of them), 23.3 and 31.3 us (one, 700
+  // rows); for two chunks of some 600 tokens over 6007, 403 and 129 us.
+  if (rows > 64 && (double)tiles * ((double)row_tiles(32) - 2.2 * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms)
+    a.nt = sgr::kRowsNT;
+  // (resident CTAs)
+  const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);
+  // Short caches are not split over CTAs: the join's launch costs more than a
+  // few tiles in turn.  28 heads over 4, split and whole: 8.5 and 8.5 us (one
+  // sequence of 4 tiles), 14.3 and 11.3 (64 of them), 9.4 and 11.9 (one of 8),
+  // 17.7 and 15.7 (64: as many row tiles as CTAs, nearly), 25.0 and 27.1 (128).
+  a.split = tiles > (2 * items >= ctas && items <= ctas ? 8 : 4);
+  const long long units = a.split ? items * (tiles + 1) : items;
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
-  const long long ctas = a.nt >= 32 ? sms : 2LL * sms;  // resident: one or two an SM
   a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
   a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));

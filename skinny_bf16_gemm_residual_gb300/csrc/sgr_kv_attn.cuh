@@ -118,9 +118,13 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     // Each lane counts its (consecutive) sequences.
     const int per_lane = (p.batch.batch + 31) / 32, b_first = lane * per_lane;
     const int b_last = min(b_first + per_lane, p.batch.batch);
-    int mine = 0;
+    int mine = 0, units = 0;
 #pragma unroll 4
-    for (int x = b_first; x < b_last; ++x) mine += attn_seq_units<NT>(p, kv_seq(p.batch, ps, x, p.err)) * hk;
+    for (int x = b_first; x < b_last; ++x) {
+      s = kv_seq(p.batch, ps, x, p.err);
+      units = attn_seq_units<NT>(p, s);
+      mine += units * hk;
+    }
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -137,16 +141,24 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       u1 = u + per + (c0 < rest ? 1 : 0);
       const int before = upto - mine;
       const int src = __ffs(__ballot_sync(0xffffffffu, u >= before && u < upto)) - 1;
-      int off = u - __shfl_sync(0xffffffffu, before, max(src, 0)), units = 0;
+      int off = u - __shfl_sync(0xffffffffu, before, max(src, 0));
       // (row offsets that run backwards may count more units than 31 bits hold)
       bool found = src >= 0;
-      for (b = max(src, 0) * per_lane; found; ++b) {
-        if (b >= p.batch.batch) found = false;
-        if (!found) break;
-        s = kv_seq(p.batch, ps, b, nullptr);
-        units = attn_seq_units<NT>(p, s);
-        if (off < units * hk) break;
-        off -= units * hk;
+      b = max(src, 0) * per_lane;
+      if (per_lane == 1) {  // the lane still has its only sequence
+        s.row0 = __shfl_sync(0xffffffffu, s.row0, b);
+        s.n = __shfl_sync(0xffffffffu, s.n, b);
+        s.len = __shfl_sync(0xffffffffu, s.len, b);
+        units = __shfl_sync(0xffffffffu, units, b);
+      } else {
+        for (; found; ++b) {
+          if (b >= p.batch.batch) found = false;
+          if (!found) break;
+          s = kv_seq(p.batch, ps, b, nullptr);
+          units = attn_seq_units<NT>(p, s);
+          if (off < units * hk) break;
+          off -= units * hk;
+        }
       }
       if (!found) u1 = u, off = 0, units = 1;
       h = off / units;
