@@ -44,6 +44,13 @@
 extern "C" {
 #endif
 
+/* Flags of sgr_kv_attention and its workspace, beside SGR_FLAG_NO_PDL: the
+ * kernel for few rows (row tiles of at most 32) or many (256) whatever the
+ * sizes, for sweeps and tests.  Neither: the library's choice.  Both:
+ * SGR_ERR_UNSUPPORTED. */
+#define SGR_FLAG_KV_FEW_ROWS 0x2u
+#define SGR_FLAG_KV_MANY_ROWS 0x4u
+
 /*
  * Rows of heads, BF16: element (token, head, d) at
  * data + token * token_stride + head * head_stride + d (strides in elements,
@@ -159,10 +166,12 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
 int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* out,
                      float scale, int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream);
 
-/* Workspace that sgr_kv_attention needs for this batch and `q_heads` query
- * heads on `device`, in bytes.  Host-only apart from a device-attribute query. */
+/* Workspace that sgr_kv_attention needs for this batch, `q_heads` query heads
+ * and these flags on `device`, in bytes (a smaller one is
+ * SGR_ERR_UNSUPPORTED there).  Depends on the sizes in the structures, not on
+ * device data.  Host-only apart from a device-attribute query. */
 int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
-                               int64_t* bytes);
+                               unsigned flags, int64_t* bytes);
 
 /* Host-only argument checks of the three operators (their exact rules, but
  * for the size of the workspace). */

@@ -26,6 +26,8 @@ from .binding import (  # noqa: F401
     SGR_ERR_NULL,
     SGR_ERR_SHAPE,
     SGR_ERR_UNSUPPORTED,
+    SGR_FLAG_KV_FEW_ROWS,
+    SGR_FLAG_KV_MANY_ROWS,
     SGR_FLAG_NO_PDL,
     SGR_OK,
     SGR_PATH_AUTO,

@@ -277,13 +277,12 @@ def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, 
     return q_out
 
 
-def kv_attention_workspace(cache: KvCache, batch: KvBatch, q_heads: int):
-    """A workspace for sgr_kv_attention calls of this cache and batch size
-    (one for each call that may overlap with others on the GPU)."""
+def kv_attention_workspace(cache: KvCache, batch: KvBatch, q_heads: int, flags: int = 0):
+    """A workspace for sgr_kv_attention calls of these sizes and flags (one for each call that may overlap with others on the GPU)."""
     import torch
 
     n = ctypes.c_int64(0)
-    _check(load().sgr_kv_attention_workspace(cache.index, cache.ref, batch.ref, q_heads, ctypes.byref(n)),
+    _check(load().sgr_kv_attention_workspace(cache.index, cache.ref, batch.ref, q_heads, flags, ctypes.byref(n)),
            "sgr_kv_attention_workspace")
     return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
 
@@ -301,7 +300,7 @@ def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float |
         out = _like(q, stream)
     ho = _heads(out, "out", shape, index)
     if workspace is None:
-        workspace = _new(index, stream, lambda: kv_attention_workspace(cache, batch, shape[1]))
+        workspace = _new(index, stream, lambda: kv_attention_workspace(cache, batch, shape[1], flags))
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on(index, (batch.index, workspace.get_device()), "sgr_kv_attention")

@@ -27,6 +27,8 @@ SGR_ERR_LAUNCH = 6
 SGR_ERR_DEVICE = 7
 
 SGR_FLAG_NO_PDL = 0x1
+SGR_FLAG_KV_FEW_ROWS = 0x2
+SGR_FLAG_KV_MANY_ROWS = 0x4
 
 SGR_PATH_AUTO = 0
 SGR_PATH_SIMT = 1
@@ -172,7 +174,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.sgr_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp, U, vp]
         lib.sgr_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, U, vp]
         lib.sgr_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I, vp, i64, U, vp]
-        lib.sgr_kv_attention_workspace.argtypes = [I, vp, vp, I, ctypes.POINTER(i64)]
+        lib.sgr_kv_attention_workspace.argtypes = [I, vp, vp, I, U, ctypes.POINTER(i64)]
         lib.sgr_validate_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp]
         lib.sgr_validate_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp]
         lib.sgr_validate_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I]

@@ -417,7 +417,7 @@ struct AttnPlan {
   int64_t bytes;    // workspace
 };
 
-AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
+AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
@@ -435,8 +435,8 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   // against 256, over contexts of up to 3000: 19.5 and 21.3 us (4 sequences,
   // 126 rows), 65.8 and 39.5 us (16 of them), 23.3 and 31.3 us (one, 700
   // rows); for two chunks of some 600 tokens over 6007, 403 and 129 us.
-  if (rows > 64 && (double)tiles * ((double)row_tiles(32) - 2.2 * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms)
-    a.nt = sgr::kRowsNT;
+  const bool gains = rows > 64 && (double)tiles * ((double)row_tiles(32) - 2.2 * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms;
+  if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);
   // Short caches are not split over CTAs: the join's launch costs more than a
@@ -472,11 +472,12 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
                   int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
   int rc = validate_attention(c, b, q, out, scale, window);
   if (rc != SGR_OK || empty(*b)) return rc;
+  if ((flags & SGR_FLAG_KV_FEW_ROWS) && (flags & SGR_FLAG_KV_MANY_ROWS)) return SGR_ERR_UNSUPPORTED;
   if (!workspace) return SGR_ERR_NULL;
   if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
-  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads);
+  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads, flags);
   if (!a.fits || workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   // (a cache without pages: the maps are never used)
@@ -554,13 +555,13 @@ int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const
 }
 
 int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
-                               int64_t* bytes) {
+                               unsigned flags, int64_t* bytes) {
   if (!bytes) return SGR_ERR_NULL;
   int rc;
   if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
   if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
   if ((rc = sgr::kv_init_device(device)) != SGR_OK) return rc;
-  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads).bytes;
+  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads, flags).bytes;
   return SGR_OK;
 }
 

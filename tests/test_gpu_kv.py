@@ -10,6 +10,7 @@ import skinny_bf16_gemm_residual_gb300 as sgr
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-6
+FEW, MANY = sgr.SGR_FLAG_KV_FEW_ROWS, sgr.SGR_FLAG_KV_MANY_ROWS
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -201,21 +202,22 @@ ATTEND = [
 
 
 @pytest.mark.parametrize("dim,page,heads,hk,lens,new,window", ATTEND)
-@pytest.mark.parametrize("heads_inside", [False, True])
-def test_attention(dim, page, heads, hk, lens, new, window, heads_inside):
+@pytest.mark.parametrize("heads_inside,flags", [(False, FEW), (True, 0), (False, MANY)])
+def test_attention(dim, page, heads, hk, lens, new, window, heads_inside, flags):
     pr = ref.Problem(dim, page, hk, lens, new, seed=heads, heads_inside=heads_inside)
     q = (2 * pr.randn(pr.tokens, heads + 2, dim)).bfloat16()
     want, mag = ref.attention(q[:, :heads], pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, page,
                               dim ** -0.5, window)
     cache, batch = pr.cache(sgr), pr.batch(sgr)
-    got = sgr.sgr_kv_attention(cache, batch, q.cuda()[:, :heads], window=window)
+    got = sgr.sgr_kv_attention(cache, batch, q.cuda()[:, :heads], window=window, flags=flags)
     ref.check_attention(got, want, mag)
     again = torch.full((heads, pr.tokens, dim), 7.0, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
-    sgr.sgr_kv_attention(cache, batch, q.cuda()[:, :heads], out=again, window=window)
+    sgr.sgr_kv_attention(cache, batch, q.cuda()[:, :heads], out=again, window=window, flags=flags)
     assert torch.equal(again, got)  # the same bits in another layout
 
 
-def test_attention_sharp_and_shifted_scores():
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_attention_sharp_and_shifted_scores(flags):
     """Scores far apart (one position takes nearly all the weight), far from
     zero, and a spike over a long flat tail."""
     pr = ref.Problem(128, 64, 2, [3000, 500], [1, 1], seed=3)
@@ -223,7 +225,7 @@ def test_attention_sharp_and_shifted_scores():
     for factor, what in ((60.0, "sharp"), (0.0, "flat"), (1e4, "one position"), (1e-30, "tiny")):
         x = (q * factor).bfloat16()
         want, mag = ref.attention(x, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, None, 64, 128 ** -0.5, 0)
-        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), x.cuda())
+        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), x.cuda(), flags=flags)
         if factor <= 60:
             ref.check_attention(got, want, mag, what)
         else:
@@ -240,24 +242,25 @@ def test_attention_sharp_and_shifted_scores():
     x[0, 0, 0] = 8.0
     kk, vv = (c.float().double().cpu() * s.double().cpu()[:, :, None, None] for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
     want, mag = ref.attention(x, kk, vv, batch.block_table.cpu(), [n], None, 64, 0.125, 0)
-    got = sgr.sgr_kv_attention(cache, sgr.KvBatch(batch.block_table, batch.seq_len), x.bfloat16().cuda())
+    got = sgr.sgr_kv_attention(cache, sgr.KvBatch(batch.block_table, batch.seq_len), x.bfloat16().cuda(), flags=flags)
     ref.check_attention(got, want, mag, "spike")
 
 
+@pytest.mark.parametrize("flags", [FEW, MANY])
 @pytest.mark.parametrize("scale", [-0.3, 0.0, 1.0])
-def test_other_scales(scale):
+def test_other_scales(scale, flags):
     """Negative, zero and unit factors of the scores, few rows and many."""
     pr = ref.Problem(64, 32, 1, [300], [11], seed=9)
     q = (0.4 * pr.randn(11, 8, 64)).bfloat16()
     for heads in (1, 8):
         x = q[:, :heads].contiguous()
         want, mag = ref.attention(x, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, scale, 0)
-        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), x.cuda(), scale=scale)
+        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), x.cuda(), scale=scale, flags=flags)
         ref.check_attention(got, want, mag)
 
 
-@pytest.mark.parametrize("heads", [4, 80])
-def test_page_scales_far_apart(heads):
+@pytest.mark.parametrize("heads,flags", [(4, FEW), (80, FEW), (4, MANY)])
+def test_page_scales_far_apart(heads, flags):
     """Scales of neighbouring pages that differ by up to 2^40."""
     pr = ref.Problem(128, 16, 1, [100], [1], seed=8)
     for i, f in ((0, (0, -3, 1, -40, 2, 0, 1)), (1, (0, 20, -20, 3, -40, 10, 0))):
@@ -265,13 +268,13 @@ def test_page_scales_far_apart(heads):
             pr.scale[i][int(pr.block_table[0, block])] *= 2.0 ** e
     q = (0.3 * pr.randn(1, heads, 128)).bfloat16()
     want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, None, 16, 128 ** -0.5, 0)
-    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), q.cuda())
+    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), q.cuda(), flags=flags)
     ref.check_attention(got, want, mag)
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-@pytest.mark.parametrize("heads", [1, 3, 5, 30])
-def test_nan_reaches_only_rows_that_see_it(dim, heads):
+@pytest.mark.parametrize("heads,flags", [(1, FEW), (3, FEW), (5, FEW), (1, MANY), (30, MANY)])
+def test_nan_reaches_only_rows_that_see_it(dim, heads, flags):
     """A NaN key or value at a position that the later rows see and the
     earlier ones do not; a NaN before every window."""
     for which in (0, 1):
@@ -283,7 +286,7 @@ def test_nan_reaches_only_rows_that_see_it(dim, heads):
             q = pr.randn(6, heads, dim).bfloat16()
             want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32,
                                       dim ** -0.5, window)
-            got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), window=window).cpu()
+            got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), window=window, flags=flags).cpu()
             assert torch.equal(got.isnan(), want.isnan())
             ref.check_attention(got, want, mag)
 
@@ -311,19 +314,20 @@ def test_large_offsets():
     ref.check_attention(got, want, mag)
 
 
-def test_long_context_split_and_repeatable():
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_long_context_split_and_repeatable(flags):
     """One long sequence over the whole GPU: against the definition, and the
     same bits every time."""
     pr = ref.Problem(128, 128, 2, [20001, 300], [1, 1], seed=12)
     q = (2 * pr.randn(2, 8, 128)).bfloat16()
     want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, None, 128, 128 ** -0.5, 0)
     cache, batch = pr.cache(sgr), pr.batch(sgr, False)
-    work = sgr.kv_attention_workspace(cache, batch, 8)
+    work = sgr.kv_attention_workspace(cache, batch, 8, flags)
     work.fill_(255)  # its contents do not matter
-    first = sgr.sgr_kv_attention(cache, batch, q.cuda(), workspace=work)
+    first = sgr.sgr_kv_attention(cache, batch, q.cuda(), workspace=work, flags=flags)
     ref.check_attention(first, want, mag)
     for _ in range(5):
-        assert torch.equal(sgr.sgr_kv_attention(cache, batch, q.cuda(), workspace=work), first)
+        assert torch.equal(sgr.sgr_kv_attention(cache, batch, q.cuda(), workspace=work, flags=flags), first)
 
 
 def test_other_stream_and_graph_replay():
@@ -385,6 +389,34 @@ def test_decode_block_with_projection():
     want = want.flatten(1) @ w_out.cpu().double().T + residual.cpu().double()
     err = (y.cpu().double() - want).abs()
     assert (err <= 1e-2 * want.abs() + 2e-2).all()
+
+
+def test_library_takes_the_kernel_for_many_rows():
+    """A chunk large enough for the library's own choice: the bits of the
+    forced one."""
+    pr = ref.Problem(64, 64, 4, [1500, 700], [150, 90], seed=40)
+    q = pr.randn(pr.tokens, 32, 64).bfloat16()
+    cache, batch, x = pr.cache(sgr), pr.batch(sgr), q.cuda()
+    assert torch.equal(sgr.sgr_kv_attention(cache, batch, x), sgr.sgr_kv_attention(cache, batch, x, flags=MANY))
+    assert not torch.equal(sgr.sgr_kv_attention(cache, batch, x, flags=FEW), sgr.sgr_kv_attention(cache, batch, x, flags=MANY))
+    want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 64, 0.125, 0)
+    ref.check_attention(sgr.sgr_kv_attention(cache, batch, x), want, mag)
+
+
+def test_workspace_refusals():
+    pr = ref.Problem(128, 64, 2, [3000], [1])
+    cache, batch = pr.cache(sgr), pr.batch(sgr, False)
+    q = torch.zeros(1, 8, 128, dtype=torch.bfloat16, device="cuda")
+    work = sgr.kv_attention_workspace(cache, batch, 8)
+    for kw, status in ((dict(workspace=work[:-1]), sgr.SGR_ERR_UNSUPPORTED), (dict(workspace=work[8:]), sgr.SGR_ERR_ALIGN),
+                       (dict(flags=FEW | MANY, workspace=work), sgr.SGR_ERR_UNSUPPORTED)):
+        with pytest.raises(sgr.SgrError) as e:
+            sgr.sgr_kv_attention(cache, batch, q, **kw)
+        assert e.value.status == status
+    with pytest.raises(ValueError):
+        sgr.sgr_kv_attention(cache, batch, q, workspace=work.cpu())
+    with pytest.raises(ValueError):
+        sgr.sgr_kv_attention(cache, batch, q[:, :, :64])
 
 
 def test_empty_calls():
