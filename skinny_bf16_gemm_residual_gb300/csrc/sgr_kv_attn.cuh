@@ -408,6 +408,18 @@ __device__ __forceinline__ QuerySplit split_query(const uint4& v, float sign, fl
   return s;
 }
 
+// Whether any thread of a named barrier's says so.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t threads, bool x) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
+}
+
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }

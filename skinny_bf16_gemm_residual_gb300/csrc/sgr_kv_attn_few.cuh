@@ -369,16 +369,6 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       __syncwarp();
       named_bar_sync(1 + group, 128);
     };
-    auto any_of_group = [&](bool x) {  // of its 128 threads
-      uint32_t any;
-      __syncwarp();
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(any)
-          : "r"((uint32_t)x), "r"(1 + group)
-          : "memory");
-      return any != 0;
-    };
     const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)q0;  // tensor-memory lanes of this warp
     float o[C], l[C];
     float run = 0.f;  // R of column q0 + lane
@@ -449,7 +439,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         float top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < C; ++q) top = fmaxf(top, x[q] - c.ref[warp][q]);
-        const bool scaled = any_of_group(top > 8.8f);  // E4M3 ends at 448 = 2^8.8
+        const bool scaled = named_bar_or(1 + group, 128, top > 8.8f);  // E4M3 ends at 448 = 2^8.8
         if (__builtin_expect(scaled, 0)) {
           // R of the columns that are exceeded moves one above the tile's
           // maximum (room for the next tiles); lane q keeps column q's.

@@ -6,7 +6,7 @@
 // Per row tile (256 rows, two halves j of 128) and 128-token tile of the cache:
 //
 //     S_j [128 rows, 128 tokens] = Q_j K^T    FP8: K's codes as they are, Q = hi + lo
-//     P_j = 2^(S' - R), FP16                  one thread a row
+//     P_j = 2^(S' - R), FP16                  two threads a row, 64 tokens each
 //     O_j [128 rows, D]         += P_j V      FP16: P from tensor memory, V widened
 //
 // Q's parts hi = e4m3(b), lo = e4m3(b - hi) go into one accumulator; with the
@@ -14,30 +14,34 @@
 // 2^-9 of it and an absolute 2^-18 below.  Splitting P the same way costs
 // three conversions for two weights, and conversions share the exponential
 // unit's 16 lanes a cycle: 2560 cycles a 128 x 128 tile against 1024 for the
-// exponentials alone (measured: the products in two parts took 190 us where
-// this form takes ROWS_US).  So V is widened to FP16 instead (exact), once for
+// exponentials alone (two chunks of some 600 tokens over 6007: 190 us with the
+// weights in two parts, 129 without).  So V is widened to FP16 instead (exact), once for
 // both halves, with integer instructions, and P is an FP16 weight: 11 bits
 // down to 2^-22 of the largest.
 //
-// A row's statistics stay in its thread: R, a whole number, is the first
-// 32 scores' maximum rounded up and moves when a score exceeds it by more than
-// FP16 holds (2^7.5 times); then the sum and the row's accumulator (in tensor
-// memory) are rescaled by a power of two.  The weights overwrite the scores'
-// columns.
+// R, a whole number, is a row's first maximum rounded up and moves when a score
+// exceeds it by more than FP16 holds (2^7.5 times); then the sum and the row's
+// accumulator (in tensor memory) are rescaled by a power of two.  The row's two
+// threads agree on it by a vote of their two warps a tile.  The weights
+// overwrite the scores' columns.
 //
-// Bound: the exponential unit (16384 a half and tile).  The two halves take
-// turns: the products of one run while the other's weights are computed.
+// Bound: the tensor pipe and the softmax in turn.  An MMA of this shape takes
+// some 105 cycles wherever it was measured, 32 of them a pair of halves and
+// tile: 3360 cycles of the 4070 that a pair takes.  The two halves take turns,
+// the products of one run while the other's weights are computed.  Measured
+// for those two chunks (28 heads over 4, 74 GFLOP): 119.5 us, 620 TFLOP/s; one
+// softmax thread a row instead of two: 129.
 //
-// Roles (448 threads, one CTA an SM): warps 0-3 and 4-7 softmax of the halves
-// (and their query operands), 8-11 widen V, warp 12 walks the work and loads
-// pages, warp 13 issues the MMAs.
+// Roles (704 threads, one CTA an SM): warps 0-7 and 8-15 softmax of the halves
+// (and their query operands), 16-19 widen V, warp 20 walks the work and loads
+// pages, warp 21 issues the MMAs.
 #pragma once
 
 #include "sgr_kv_attn.cuh"
 
 namespace sgr {
 
-constexpr int kRowsNT = 256, kRowsThreads = 448;
+constexpr int kRowsNT = 256, kRowsThreads = 704;
 
 template <int D>
 struct RowsCtl {
@@ -54,6 +58,7 @@ struct RowsCtl {
   float kscale[M][8], vexp[M][8];
   int flags[M], live[M][2];
   float qf[kRowsNT];
+  float pair[2][2][128];  // of a row's two threads: maxima, sums of weights
   unsigned nan_tokens[2][4];           // of the widened tile: tokens with a NaN value
   uint32_t nan_mask[2][kAttnTile][4];  // and which of its elements
 };
@@ -138,21 +143,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&c.sfull[i]), 2);  // the product, and the thread that saw the page scales
-      mbar_init(smem_u32(&c.pfull[i]), 4);
+      mbar_init(smem_u32(&c.pfull[i]), 8);
       mbar_init(smem_u32(&c.pvdone[i]), 1);
       mbar_init(smem_u32(&c.wfull[i]), 4);
       mbar_init(smem_u32(&c.wempty[i]), 1);
-      mbar_init(smem_u32(&c.qfull[i]), 4);
+      mbar_init(smem_u32(&c.qfull[i]), 8);
     }
     mbar_init(smem_u32(&c.drain), 1);
     for (int i = 0; i < kAttnQueue; ++i) {
       mbar_init(smem_u32(&c.segfull[i]), 1);
-      mbar_init(smem_u32(&c.segempty[i]), 9);  // the softmax warps and the MMA thread
+      mbar_init(smem_u32(&c.segempty[i]), 17);  // the softmax warps and the MMA thread
     }
     c.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 13) {
+  if (warp == 21) {
     tmem_alloc(smem_u32(&c.tmem), 512);
     tmem_relinquish();
   }
@@ -178,9 +183,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     __syncwarp();
   };
 
-  if (warp == 12) {
+  if (warp == 20) {
     attn_walk<D, NT>(c, p, tmK, tmV, ring);
-  } else if (warp == 13) {
+  } else if (warp == 21) {
     // ------------------------------------------------------------- MMA issuer
     // Order: PV of half 0, next scores of half 0, PV of half 1, next scores of
     // half 1: the weights of one half are computed under the other's products.
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               const uint64_t wd = smem_desc_rows<128>(wide + (uint32_t)(y & 1) * kWide, kAttnTile * 128);
 #pragma unroll
               for (int kk = 0; kk < kAttnTile / 16; ++kk)
-                mma_bf16_tmem_a(o_cols, s_cols + (uint32_t)(kk * 8), wd + (uint64_t)(kk * (16 * 128 >> 4)), idesc_o,
+                mma_bf16_tmem_a(o_cols, s_cols + (uint32_t)(kk * 8 + (kk < 4 ? 0 : 32)), wd + (uint64_t)(kk * (16 * 128 >> 4)), idesc_o,
                                 (k > 1 || kk > 0) ? 1u : 0u);
               mma_commit(smem_u32(&c.pvdone[j]));
               if (j == halves - 1) mma_commit(smem_u32(&c.wempty[y & 1]));
@@ -245,12 +250,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       mma_commit(smem_u32(&c.drain));
       if (!mbar_wait(smem_u32(&c.drain), 0)) report_error(p.err, kErrDrain);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // --------------------------------------------------------------- widen V
     // Thread = token: its D codes to FP16, zeros where no row sees it (0 x NaN
     // must not reach the product).  In tiles whose rows see different tokens a
     // NaN becomes zero too, and the softmax threads are told.
-    const int tok = tid - 256;
+    const int tok = tid - 512;
     for (int i = 0;; ++i) {
       const int slot = i % S, meta = i % M, buf = i & 1;
       wait(&c.vfull[slot], (i / S) & 1);
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       if (flags & 2) {
         const unsigned any = __ballot_sync(0xffffffffu, nans);
-        if (lane == 0) c.nan_tokens[buf][warp - 8] = any;
+        if (lane == 0) c.nan_tokens[buf][warp - 16] = any;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -309,23 +314,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const int half = warp >> 2, row = tid & 127;
-    auto meet = [&] {  // the half's 4 warps
+    const int half = warp >> 3, sub = warp >> 2 & 1, row = tid & 127, ht = tid & 255;
+    auto meet = [&] {  // the half's 8 warps
       __syncwarp();
-      if (half == 0)
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      else
-        asm volatile("bar.sync 2, 128;" ::: "memory");
+      named_bar_sync(1 + half, 256);
     };
+    const int pair_bar = 3 + half * 4 + (warp & 3);  // the two warps of a row
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // tensor-memory lanes of this warp
     const uint32_t s_cols = tmem + lanes + (uint32_t)(half * 128), o_cols = tmem + lanes + (uint32_t)(256 + half * 128);
     int i = 0, mine = 0, sq = 0;  // tiles of the CTA, tiles of this half, segments
     while (true) {
       const int qi = sq % kAttnQueue;
-      if (row == 0) c.go[half][sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
+      if (ht == 0) c.go[half][sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
       meet();
       if (!c.go[half][sq & 1]) {
-        if (row == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
+        if (ht == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
         *abort_flag = 1;
         break;
       }
@@ -339,23 +342,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         continue;
       }
       // ------------------------------------------------------- query operand
-      // D / 8 lanes a row, D / 8 passes, two rows of a thread under way.
+      // D / 8 lanes a row, D / 16 passes, two rows of a thread under way.
       {
-        constexpr int kLanes = D / 8, kRows = 128 / kLanes;
-        const int l = row % kLanes;
+        constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+        const int l = ht % kLanes;
         auto load_row = [&](int pass) {
-          const int q = 128 * half + pass * kRows + row / kLanes;
+          const int q = 128 * half + pass * kRows + ht / kLanes;
           if (q >= g.nrows) return make_uint4(0u, 0u, 0u, 0u);
           const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
           return *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         };
         uint4 v0 = load_row(0), v1 = load_row(1);
 #pragma unroll 1
-        for (int pass = 0; pass < kLanes; ++pass) {
+        for (int pass = 0; pass < kLanes / 2; ++pass) {
           const uint4 v = v0;
           v0 = v1;
-          if (pass + 2 < kLanes) v1 = load_row(pass + 2);
-          const int q = pass * kRows + row / kLanes;
+          if (pass + 2 < kLanes / 2) v1 = load_row(pass + 2);
+          const int q = pass * kRows + ht / kLanes;
           // (a negative scale turns the queries' signs: the factor is positive)
           const QuerySplit s = split_query<kLanes>(v, p.scale_log2 < 0.f ? -1.f : 1.f, 1.f);
           const uint32_t at = qbuf + (uint32_t)(half * kHalf + (l & 1) * 8) + swizzled<D>(q, l >> 1);
@@ -381,13 +384,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         tc_fence_after();
         const int flags = c.flags[meta], ps = p.cache.page_shift;
         const int c0 = see0 - t * kAttnTile, cn = see1 - t * kAttnTile - c0;  // columns that the row sees: c0 .. c0 + cn
-        // The loops over a tile's columns stay rolled: unrolled, the body does
-        // not fit the instruction caches, and the warps of four roles then
-        // wait for instructions most of the time (236 against ROLLED_US us).
+        // The loops over a thread's columns stay rolled: unrolled, the body
+        // does not fit the instruction caches, and the warps of four roles
+        // then wait for instructions most of the time (a chunk of a prompt:
+        // 236 us unrolled, 129 rolled, both with one thread a row).
         uint32_t x[32];
         if (__builtin_expect(flags, 0)) {  // what the row does not see: no score
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 2 * sub; k < 2 * sub + 2; ++k) {
             tmem_ld32(s_cols + 32 * k, x);
             tmem_wait_ld32(x);
 #pragma unroll
@@ -402,73 +406,65 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
           tmem_wait_st();
         }
-        // Weights, 256 p in FP16, over the scores' columns [0, 64): a chunk's
-        // lie where scores were that are read already.  Where a chunk exceeds
-        // what FP16 holds, R moves, and what was written is rescaled.
+        float top = -INFINITY;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 2 * sub; k < 2 * sub + 2; ++k) {
           tmem_ld32(s_cols + 32 * k, x);
           tmem_wait_ld32(x);
-          float z[32];
-          float iv[2];  // the value scales do not count in the sum of weights
-          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (32 * k + 16 * h) >> ps;
-            const float ve = c.vexp[meta][pi], kq = c.kscale[meta][pi] * qf, add = (ve + 8.f) - R;
-            iv[h] = ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f;
+            float m[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              z[16 * h + e] = fmaf(__uint_as_float(x[16 * h + e]), kq, add);
-              top[h] = fmaxf(top[h], z[16 * h + e]);
-            }
+            for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(x[16 * h + e]));
+            top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), c.kscale[meta][pi] * qf, c.vexp[meta][pi]));
           }
-          const float most = fmaxf(top[0], top[1]);
-          const bool move = most > (unset ? -3.0e38f : 15.5f);
-          if (__any_sync(0xffffffffu, move)) {
-            const float up = move ? ceilf(most - 8.f) : 0.f, a = move && !unset ? exp2_whole(-up) : 1.f;
-            unset = unset && !move;
-            R += up;
-            l *= a;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) z[e] -= up;
-            // The product before is done: its weights' place has new scores.
-            if (t > g.ta) {
+        }
+        if (named_bar_or(pair_bar, 64, top > (unset ? -3.0e38f : R + 7.5f))) {  // (weights are 256 p: FP16 ends below 2^16)
+          c.pair[half][sub][row] = top;
+          __syncwarp();
+          named_bar_sync(pair_bar, 64);
+          top = fmaxf(top, c.pair[half][sub ^ 1][row]);
+          const bool move = top > (unset ? -3.0e38f : R + 7.5f);
+          const float now = move ? ceilf(top) : R, a = move && !unset ? exp2_whole(R - now) : 1.f;
+          unset = unset && !move;
+          R = now;
+          l *= a;
+          if (t > g.ta) {  // (the product before is done: its weights' place has new scores)
 #pragma unroll 1
-              for (int n = 0; n < D / 16; ++n) {
-                float y[16];
-                uint32_t w[16];
-                tmem_ld16(o_cols + 16 * n, y);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * a);
-                tmem_st16(o_cols + 16 * n, w);
-              }
-            }
-#pragma unroll 1
-            for (int n = 0; n < k; ++n) {
+            for (int n = 0; n < D / 32; ++n) {  // this thread's half of the accumulator
+              const uint32_t at = o_cols + (uint32_t)(sub * (D / 2) + 16 * n);
               float y[16];
               uint32_t w[16];
-              tmem_ld16(s_cols + 16 * n, y);
-              const uint32_t aa = pack_f16(a, a);
+              tmem_ld16(at, y);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(w[e]) : "r"(__float_as_uint(y[e])), "r"(aa));
-              tmem_st16(s_cols + 16 * n, w);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(y[e] * a);
+              tmem_st16(at, w);
             }
           }
+        }
+        // Weights, 256 p in FP16, over the first 32 of the thread's columns: a
+        // chunk's lie where scores were that are read already.
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          tmem_ld32(s_cols + 64 * sub + 32 * k, x);
+          tmem_wait_ld32(x);
           uint32_t w[16];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            const int pi = (64 * sub + 32 * k + 16 * h) >> ps;
+            const float ve = c.vexp[meta][pi], kq = c.kscale[meta][pi] * qf, add = (ve + 8.f) - R;
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float z0 = ex2(z[16 * h + 2 * e]), z1 = ex2(z[16 * h + 2 * e + 1]);
+              const float z0 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e]), kq, add));
+              const float z1 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e + 1]), kq, add));
               sum[0] += z0, sum[1] += z1;
               w[8 * h + e] = pack_f16(z0, z1);
             }
-            l = fmaf(sum[0] + sum[1], iv[h], l);
+            l = fmaf(sum[0] + sum[1], ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f, l);  // without the value scale
           }
-          tmem_st16(s_cols + 16 * k, w);
+          tmem_st16(s_cols + 64 * sub + 16 * k, w);
         }
         tmem_wait_st();
         if (__builtin_expect(flags & 2, 0)) {
@@ -488,13 +484,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       // ------------------------------------------------------- the segment's end
       wait(&c.pvdone[half], (mine - 1) & 1);
       tc_fence_after();
+      c.pair[half][sub][row] = l;
+      meet();
+      l = c.pair[half][0][row] + c.pair[half][1][row];
       const bool whole = (g.kind & (kSegStart | kSegEnd)) == (kSegStart | kSegEnd);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int head = g.h * p.group + r - rtok * p.group;
       __nv_bfloat16* out = p.out.p + (long long)(g.row0 + rtok) * p.out.ts + (long long)head * p.out.hs;
       float* part = p.part_o + ((long long)g.slot * NT + q) * D;
 #pragma unroll 1
-      for (int k = 0; k < D / 32; ++k) {
+      for (int k = sub * (D / 64); k < (sub + 1) * (D / 64); ++k) {  // this thread's half of the row
         uint32_t x[32];
         tmem_ld32(o_cols + 32 * k, x);
         tmem_wait_ld32(x);
@@ -519,13 +518,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             *reinterpret_cast<uint4*>(part + 32 * k + 4 * e) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
-      if (real && !whole) p.part_ml[(long long)g.slot * NT + q] = make_float2(R, l);
+      if (real && !whole && sub == 0) p.part_ml[(long long)g.slot * NT + q] = make_float2(R, l);
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == 21) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
