@@ -431,10 +431,11 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   // 24 against 34.0 in one of 32).
   a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
   // The 256-row kernel takes some 2.2 times a 32-row unit's time for eight
-  // times the rows, but 12 units' time to begin and end.  Measured, 32 rows
-  // against 256, over contexts of up to 3000: 19.5 and 21.3 us (4 sequences,
-  // 126 rows), 65.8 and 39.5 us (16 of them), 23.3 and 31.3 us (one, 700
-  // rows); for two chunks of some 600 tokens over 6007, 403 and 129 us.
+  // times the rows, but 12 units' time to begin and end.  Measured with 28
+  // heads over 4, small tiles against 256 rows: 18.1 and 20.3 us (4 sequences
+  // of 3000, 126 rows a head each), 45.0 and 33.0 (16 of them), 22.3 and 30.8
+  // (one, 700 rows), 74 and 48 (one, 4200 rows), 97.7 and 63.2 (one of 30000,
+  // 700 rows), 90 and 99 (32 of 9000, 63 rows), 145 and 108 (112 rows).
   const bool gains = rows > 64 && (double)tiles * ((double)row_tiles(32) - 2.2 * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms;
   if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
