@@ -299,7 +299,9 @@ int launch(Fn fn, dim3 grid, int threads, size_t smem, unsigned flags, void* str
 // Passes over a row's heads of one block: one while that does not fill the
 // GPU (few rows: latency), four beyond (the reads of four heads a thread are
 // then under way at once, and the row's cosines, sines and weights are read
-// once for them).
+// once for them).  32 heads of 128, one pass and four: 1.6 and 2.1 us (64
+// rows), 2.5 and 3.6 (256), 4.0 and 4.1 (700: the change-over), 8.0 and 6.9
+// (1500); 72 heads: 15.5 and 12.7 (1500), 114 and 90 (12345).
 int rope_passes(int sms, long long rows, int heads, int per_pass) {
   return rows * ((heads + per_pass - 1) / per_pass) > 16LL * sms && heads > per_pass ? 4 : 1;
 }

@@ -1,12 +1,28 @@
 // sgr_kv_append.cuh -- norm and rotation of query and key heads, and the
 // append of keys and values to the paged E4M3 cache (sgr_attention.h).
 //
-// Bound: memory (each input read once, each output written once) for prompts,
-// the chain of dependent loads for a handful of rows.  So one launch does all
-// of it: the first blocks take query rows, the others one (page, key/value
-// head, K or V) each.  A block that owns a page's head needs no atomics for
-// its scale: it holds the page's new tokens in registers, finds their largest
-// magnitude, and then writes codes and scale.
+// A head is D / 8 lanes of 8 elements: the norm is one sum of squares in FP32
+// over them, 1 / sqrt(mean + eps) and the weight multiply it, and each lane
+// holds both elements of its four pairs, so that the rotation needs no
+// exchange.  One rounding, to BF16 or E4M3, at the end.
+//
+// A scale is a power of two: x / s is then exact, and a page whose scale grows
+// has its earlier codes divided by a power of two, exact but for those that
+// become subnormal.  The price is up to one of E4M3's 15 binades of range.
+//
+// One launch does all of an append: the first blocks take query rows, the
+// others one (page, key/value head, K or V) each.  A block that owns a page's
+// head needs no atomics for its scale: it holds the page's new tokens in
+// registers, finds their largest magnitude, and then writes codes and scale.
+//
+// Bound: memory (each input read once, each output written once) and the issue
+// of instructions for prompts, the chain of dependent loads for a handful of
+// rows.  Measured: norm + rotation of 12345 rows of 72 heads (458 MB) 88 us,
+// 5.2 TB/s, issue slots 67% taken; of 16 rows of 32 heads 1.4 us.  Append of
+// 6012 prompt rows of 64 + 8 + 8 heads (237 MB) 51 us, 4.6 TB/s, issue
+// slots 73% taken; of one row 2.7 us, of 48 rows 4.9.  More blocks an SM (fewer
+// registers) or packed FP32 arithmetic (more registers) were slower for the
+// append, and within 4% for the norm.
 #pragma once
 
 #include "sgr_kv_common.cuh"

@@ -5,16 +5,18 @@
 // The unit of work is a row tile (up to NT query rows that share a key/value
 // head: the head's query group, times the new tokens of a sequence) against a
 // 128-token tile of the cache.  Every CTA takes the same number of units of
-// all sequences and heads, in order, whatever the lengths (and one more unit
-// for each row tile, which is what its beginning and end cost: without it CTAs
-// with many short sequences finish last); a row tile that spans CTAs leaves partial sums (o, R, l) in the workspace and a second kernel
-// joins them in order (the same bits on every run).  For short caches
-// (`whole`) a row tile is one unit and nothing is joined.
+// all sequences and heads, in order, whatever the lengths, and one more unit
+// for each row tile, which is what its beginning and end cost (without it CTAs
+// with many short sequences finish last: 24.2 against 18.7 us for 32 ragged
+// sequences).  A row tile that spans CTAs leaves partial sums (o, R, l) in the
+// workspace and a second kernel joins them in order (the same bits on every
+// run).  For short caches (`whole`) a row tile is one unit and nothing is
+// joined.
 //
 // Both kernels feed the FP8 tensor core (tcgen05.mma kind::f8f6f4) with the
-// cache's codes straight from TMA.  The other operands, queries and weights,
-// are brought into E4M3 as two parts, hi = e4m3(b) and lo = e4m3 of the rest,
-// each row scaled by a power of two, which holds 8 significant bits.
+// cache's codes straight from TMA.  The queries (and the few-row kernel's
+// weights) are brought into E4M3 as two parts, hi = e4m3(b) and lo = e4m3 of
+// the rest, each row scaled by a power of two, which holds 8 significant bits.
 #pragma once
 
 #include <cuda.h>
@@ -440,6 +442,11 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 // taking every kParts-th run of 8 pieces with all its reads under way at once
 // (one memory round trip for the owner, one for the pieces: few long sequences
 // have tens of pieces a row), in a fixed order.
+//
+//     o = sum_k 2^(R_k - m) o_k / sum_k 2^(R_k - m) l_k,   m = max_k R_k
+//
+// Bound: the latency of its launch and of those two round trips, some 3 us of
+// a call (two chunks of prompts, 33 MB of partial sums: 15 us from a cold L2).
 constexpr int kJoinThreads = 256;
 
 template <int NT>

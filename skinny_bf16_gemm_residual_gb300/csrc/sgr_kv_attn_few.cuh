@@ -6,7 +6,7 @@
 // Per row tile (NT = 8, 16, 24 or 32 rows) and 128-token tile of the cache:
 //
 //     S^T [128 tokens, NT] = K Q^T      codes of K as they are in the cache
-//     P^T = 2^(S' - m)                  one thread per token
+//     P^T = 2^(S' - R)                  one thread per token
 //     O^T [D, NT]          = V^T P^T    codes of V as they are, read M-major
 //
 // Both products run on the FP8 tensor core (tcgen05.mma kind::f8f6f4) with
@@ -30,11 +30,20 @@
 // exponent of P and taken out of the sum of weights again.
 //
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
-// row tile.
+// row tile, where there are enough of them: 96 sequences of up to 16384 (64
+// heads over 8, 1.63 GB) 240 us, 6.8 TB/s, a plain copy's rate; one of 200003
+// (410 MB) 68 us.  With fewer bytes the CTAs' beginning (5 us: launch, tensor
+// memory, first page, first run of the code) and the join (3 us): 32 sequences
+// of up to 4096 (28 heads over 4, 60.6 MB) 18.9 us, one of 333 7.8 us.  With
+// more rows a head the softmax: 20 rows (D = 64, 38.7 MB) 27 us, issue slots
+// 59% taken.
 //
-// Roles (two CTAs an SM, one with 24 and 32 rows): a group of 4 softmax warps for every
-// 8 rows (thread = token, then = element d), one warp that walks the work, loads pages by TMA and hands out segments, one that issues
-// the MMAs, two that bring the next segments' queries into the operand.
+// Roles: a group of 4 softmax warps for every 8 rows (thread = token, then =
+// element d), one warp that walks the work, loads pages by TMA and hands out
+// segments, one that issues the MMAs, two that bring the next segments'
+// queries into the operand.  Two CTAs an SM, so that one computes while the
+// other waits (one with 32 rows, whose registers and shared memory two would
+// not fit; three with 8 rows were slower).
 #pragma once
 
 #include "sgr_kv_attn.cuh"

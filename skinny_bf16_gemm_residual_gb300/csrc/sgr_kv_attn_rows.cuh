@@ -25,12 +25,14 @@
 // threads agree on it by a vote of their two warps a tile.  The weights
 // overwrite the scores' columns.
 //
-// Bound: the tensor pipe and the softmax in turn.  An MMA of this shape takes
-// some 105 cycles wherever it was measured, 32 of them a pair of halves and
-// tile: 3360 cycles of the 4070 that a pair takes.  The two halves take turns,
-// the products of one run while the other's weights are computed.  Measured
-// for those two chunks (28 heads over 4, 74 GFLOP): 119.5 us, 620 TFLOP/s; one
-// softmax thread a row instead of two: 129.
+// Bound: the chain of a half: its weights (2000 cycles a tile), then their
+// product, its completion and the next scores (2100; the scores' columns are
+// the weights', so these products cannot overlap), with the other half half a
+// turn behind.  Tensor memory is full (two halves of scores and outputs, 128
+// columns each), so there is no third chain.  Measured for two chunks of some
+// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 119.5 us, 620 TFLOP/s,
+// tensor pipe 32% and issue slots 58% of active cycles; with one softmax
+// thread a row instead of two 129 us.
 //
 // Roles (704 threads, one CTA an SM): warps 0-7 and 8-15 softmax of the halves
 // (and their query operands), 16-19 widen V, warp 20 walks the work and loads
