@@ -96,7 +96,8 @@ typedef struct {
  * They are the last of its seq_len[b] positions: its i-th of n rows is at
  * position seq_len[b] - n + i.  A row whose position is negative (a padding
  * row: seq_len 0) is not appended, its rotated query and its attention output
- * are zeros.  Entries of block_table beyond a sequence's length are not read.
+ * are zeros.  Rows that no sequence has (q_start[batch] below tokens) are left
+ * as they are.  Entries of block_table beyond a sequence's length are not read.
  */
 typedef struct {
   const int* block_table; /* [batch, max_pages], row stride table_stride */

@@ -21,9 +21,23 @@ import struct
 
 from .binding import (SGR_OK, SgrError, _common_device, load, sgr_heads, sgr_kv_batch, sgr_kv_cache, sgr_norm_rope)
 
+
+class _Torch:
+    """Stands for torch until its first use (importing the package does not import torch)."""
+
+    def __getattr__(self, name):
+        global torch
+        import torch
+
+        return getattr(torch, name)
+
+
+torch = _Torch()
+
 # A call of a few microseconds on the GPU should not wait for its arguments:
-# sgr_heads structures go as packed bytes, devices are compared by index and
-# the current stream is asked for as a number.
+# sgr_heads structures go as packed bytes, devices are compared by index, the
+# current stream is asked for as a number, and torch is looked up in this
+# module.
 _pack_heads = struct.Struct("@Pqqii").pack
 assert struct.calcsize("@Pqqii") == ctypes.sizeof(sgr_heads)
 
@@ -34,8 +48,6 @@ def _check(rc: int, what: str) -> None:
 
 
 def _wrong_heads(t, name: str, shape, index: int):
-    import torch
-
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if not t.is_cuda:
@@ -51,14 +63,12 @@ def _wrong_heads(t, name: str, shape, index: int):
 
 def _heads(t, name: str, shape, index: int) -> bytes:
     """The sgr_heads of a tensor of this shape on this device."""
-    import torch
-
-    tokens, heads, dim = shape
     if t.dtype is not torch.bfloat16 or t.get_device() != index or t.shape != shape:
         _wrong_heads(t, name, shape, index)
     ts, hs, es = t.stride()
     if es != 1:
         _wrong_heads(t, name, shape, index)
+    tokens, heads, dim = shape
     # Strides of axes with one element are arbitrary in torch.
     return _pack_heads(t.data_ptr(), ts if tokens > 1 else heads * dim, hs if heads > 1 else dim, heads, 0)
 
@@ -70,8 +80,6 @@ def _shape3(t, name: str):
 
 
 def _int32(t, name: str, dim: int):
-    import torch
-
     if t.dtype is not torch.int32 or not t.is_cuda or t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be a {dim}-D CUDA int32 tensor with unit inner stride")
     return t
@@ -86,8 +94,6 @@ class KvCache:
     k_scale, v_scale: [pages, heads] float32, unit inner stride."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        import torch
-
         for t, n in ((k, "k"), (v, "v")):
             if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
                 raise TypeError(f"{n} must be torch.float8_e4m3fn or torch.uint8, got {t.dtype}")
@@ -112,8 +118,6 @@ class KvCache:
     @classmethod
     def empty(cls, pages: int, heads: int, page_size: int, head_dim: int, device="cuda") -> "KvCache":
         """A cache without contents: pages count from the first append to them."""
-        import torch
-
         kv = torch.zeros(2, pages, heads, page_size, head_dim, dtype=torch.uint8, device=device)
         scale = torch.ones(2, pages, heads, dtype=torch.float32, device=device)
         kv = kv.view(torch.float8_e4m3fn)
@@ -158,8 +162,6 @@ class RopeNorm:
     [head_dim] bfloat16 (None: no norm)."""
 
     def __init__(self, table=None, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False):
-        import torch
-
         if table is not None and (table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2
                                   or not table.is_contiguous()):
             raise ValueError("table must be a contiguous 2-D CUDA float32 tensor")
@@ -179,16 +181,13 @@ class RopeNorm:
         self.ref = ctypes.addressof(self.c)
 
 
-def _on(index: int, others, what: str):
-    for o in others:
-        if o is not None and o != index:
-            raise ValueError(f"{what}: all tensors must be on one CUDA device, got cuda:{index} and cuda:{o}")
+def _on(index: int, other, what: str):
+    if other is not None and other != index:
+        raise ValueError(f"{what}: all tensors must be on one CUDA device, got cuda:{index} and cuda:{other}")
 
 
 def _launch(index: int, stream, what: str, fn, *args):
     """fn(*args, stream handle) with device `index` current."""
-    import torch
-
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     elif isinstance(stream, int):
@@ -208,8 +207,6 @@ def _launch(index: int, stream, what: str, fn, *args):
 
 def _new(index: int, stream, make):
     """A tensor allocated for use on `stream`."""
-    import torch
-
     if stream is None:
         return make()
     if isinstance(stream, int):
@@ -219,8 +216,6 @@ def _new(index: int, stream, make):
 
 
 def _like(t, stream):
-    import torch
-
     return _new(t.get_device(), stream, lambda: torch.empty(t.shape, dtype=t.dtype, device=t.device))
 
 
@@ -232,9 +227,12 @@ def sgr_qk_norm_rope(q, k, positions, rope: RopeNorm, q_out=None, k_out=None, fl
     tokens, _, dim = shape
     index = q.get_device()
     hq = _heads(q, "q", shape, index)
-    _int32(positions, "positions", 1)
-    if positions.shape[0] != tokens:
-        raise ValueError(f"positions must have {tokens} elements, got {positions.shape[0]}")
+    if (positions.dtype is not torch.int32 or positions.shape != (tokens,) or positions.get_device() != index
+            or not positions.is_contiguous()):
+        _int32(positions, "positions", 1)
+        if positions.shape[0] != tokens:
+            raise ValueError(f"positions must have {tokens} elements, got {positions.shape[0]}")
+        _on(index, positions.get_device(), "sgr_qk_norm_rope")
     if rope.head_dim is not None and rope.head_dim != dim:
         raise ValueError(f"norm weights must have {dim} elements")
     if q_out is None:
@@ -247,7 +245,8 @@ def sgr_qk_norm_rope(q, k, positions, rope: RopeNorm, q_out=None, k_out=None, fl
         if k_out is None:
             k_out = _like(k, stream)
         hko = _heads(k_out, "k_out", shape, index)
-    _on(index, (positions.get_device(), rope.index), "sgr_qk_norm_rope")
+    if rope.index != index:
+        _on(index, rope.index, "sgr_qk_norm_rope")
     _launch(index, stream, "sgr_qk_norm_rope", load().sgr_qk_norm_rope, hq, hk, hqo, hko, positions.data_ptr(), tokens,
             dim, rope.ref, flags)
     return q_out, k_out
@@ -272,15 +271,15 @@ def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, 
         hqo = _heads(q_out, "q_out", shape, index)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on(index, (batch.index, rope.index), "sgr_kv_append")
+    if batch.index != index or rope.index != index:
+        _on(index, batch.index, "sgr_kv_append")
+        _on(index, rope.index, "sgr_kv_append")
     _launch(index, stream, "sgr_kv_append", load().sgr_kv_append, cache.ref, batch.ref, hq, hk, hv, hqo, rope.ref, flags)
     return q_out
 
 
 def kv_attention_workspace(cache: KvCache, batch: KvBatch, q_heads: int, flags: int = 0):
     """A workspace for sgr_kv_attention calls of these sizes and flags (one for each call that may overlap with others on the GPU)."""
-    import torch
-
     n = ctypes.c_int64(0)
     _check(load().sgr_kv_attention_workspace(cache.index, cache.ref, batch.ref, q_heads, flags, ctypes.byref(n)),
            "sgr_kv_attention_workspace")
@@ -303,7 +302,9 @@ def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float |
         workspace = _new(index, stream, lambda: kv_attention_workspace(cache, batch, shape[1], flags))
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _on(index, (batch.index, workspace.get_device()), "sgr_kv_attention")
+    if batch.index != index or workspace.get_device() != index:
+        _on(index, batch.index, "sgr_kv_attention")
+        _on(index, workspace.get_device(), "sgr_kv_attention")
     _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention, cache.ref, batch.ref, hq, ho,
             shape[2] ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.nbytes, flags)
     return out
