@@ -428,3 +428,16 @@ def test_empty_calls():
     assert sgr.sgr_kv_append(cache, batch, x, x, sgr.RopeNorm(), q=x).shape == (0, 1, 64)
     pos = torch.empty(0, dtype=torch.int32, device="cuda")
     assert sgr.sgr_qk_norm_rope(x, x, pos, sgr.RopeNorm())[0].shape == (0, 1, 64)
+
+
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_rows_of_no_sequence_are_left(flags):
+    pr = ref.Problem(64, 16, 2, [40, 21], [3, 1])
+    cache = pr.cache(sgr)
+    batch = sgr.KvBatch(pr.block_table.cuda(), pr.seq_len.cuda(), pr.q_start.cuda(), tokens=pr.tokens + 2, max_new=3)
+    x = pr.randn(3, pr.tokens + 2, 2, 64).bfloat16().cuda()
+    q_out, out = torch.full_like(x[0], 7.0), torch.full_like(x[0], 7.0)
+    sgr.sgr_kv_append(cache, batch, x[1], x[2], sgr.RopeNorm(), q=x[0], q_out=q_out)
+    sgr.sgr_kv_attention(cache, batch, x[0], out=out, flags=flags)
+    for t in (q_out, out):
+        assert (t[pr.tokens:] == 7).all() and not (t[:pr.tokens] == 7).all(-1).any()
