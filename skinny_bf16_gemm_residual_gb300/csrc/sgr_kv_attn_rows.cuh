@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             *reinterpret_cast<uint4*>(part + 32 * k + 4 * e) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
-      if (real && !whole && sub == 0) p.part_ml[(long long)g.slot * NT + q] = make_float2(R, l);
+      if (real && !whole && sub == 0) p.part_ml[(long long)g.slot * NT + q] = make_float2(unset ? -3.0e38f : R, l);
       tc_fence_before();
     }
   }

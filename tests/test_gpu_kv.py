@@ -441,3 +441,14 @@ def test_rows_of_no_sequence_are_left(flags):
     sgr.sgr_kv_attention(cache, batch, x[0], out=out, flags=flags)
     for t in (q_out, out):
         assert (t[pr.tokens:] == 7).all() and not (t[:pr.tokens] == 7).all(-1).any()
+
+
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_join_with_pieces_that_see_nothing(flags):
+    """Rows whose few positions lie in one piece of a split cache, with scores
+    far below zero: the other pieces have no part in the maximum."""
+    pr = ref.Problem(128, 128, 2, [1035], [26], seed=3)
+    q = (8 * pr.randn(26, 16, 128)).bfloat16()
+    want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 128, 4.0, 1)
+    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), scale=4.0, window=1, flags=flags)
+    ref.check_attention(got, want, mag)
