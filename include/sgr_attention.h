@@ -160,7 +160,10 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
  * query head h reads key/value head h / (q->heads / cache->heads).  A row
  * that sees no position gets zeros.  Masked positions have no influence,
  * whatever they hold.  `scale` multiplies the scores (1/sqrt(head_dim) as a
- * rule).  workspace: device memory of sgr_kv_attention_workspace() bytes,
+ * rule).  The tensor core sees a query's elements to 2^-18 of its row's largest
+ * (with their 8 bits down to 2^-9 of it at least), so a score is good to some
+ * 2^-16 of |q| |k| scale, and weights to 8 bits down to 2^-14 of the largest and
+ * 2^-19 of it below.  workspace: device memory of sgr_kv_attention_workspace() bytes,
  * 16-byte aligned, without initial contents; calls that may overlap on the
  * GPU need one each.
  */
