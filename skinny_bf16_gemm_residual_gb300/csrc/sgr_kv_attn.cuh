@@ -439,7 +439,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 // Joins the partial sums of row tiles that span CTAs: blocks x = c take the row
 // tile that begins in CTA c and ends in a later one, if any; its pieces are
 // those of CTAs c, c + 1, ..., last.  A row is joined by kParts warps, each
-// taking every kParts-th run of 8 pieces with all its reads under way at once
+// taking every kParts-th run of pieces with all its reads under way at once
 // (one memory round trip for the owner, one for the pieces: few long sequences
 // have tens of pieces a row), in a fixed order.
 //
@@ -453,11 +453,12 @@ template <int NT>
 struct JoinShape {
   static constexpr int kParts = NT <= 16 ? 4 : 1;  // warps a row
   static constexpr int kRows = kJoinThreads / 32 / kParts;
+  static constexpr int kRun = NT <= 32 ? 8 : 2;  // pieces read at once
 };
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnParams p) {
-  constexpr int kE = D / 32, kParts = JoinShape<NT>::kParts, kRows = JoinShape<NT>::kRows;  // kE: elements a lane
+  constexpr int kE = D / 32, kParts = JoinShape<NT>::kParts, kRows = JoinShape<NT>::kRows, kRun = JoinShape<NT>::kRun;  // kE: elements a lane
   __shared__ float part_o[kRows][kParts][D];
   __shared__ float2 part_ml[kRows][kParts];
   pdl_launch_dependents();
@@ -471,10 +472,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnPa
   float m = -3.0e38f, sum = 0.f, o[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.f;
-  for (int k0 = 8 * part; k0 < n; k0 += 8 * kParts) {
-    float v[8][kE];
+  for (int k0 = kRun * part; k0 < n; k0 += kRun * kParts) {
+    float v[kRun][kE];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kRun; ++k) {
       const float* at = p.part_o + slot(min(k0 + k, n - 1)) * D + lane * kE;
       if constexpr (kE == 4) {
         const float4 u = *reinterpret_cast<const float4*>(at);
@@ -485,16 +486,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnPa
       }
     }
     float2 ml = make_float2(-3.0e38f, 0.f);  // lane k: of piece k0 + k
-    if (lane < 8 && k0 + lane < n) ml = p.part_ml[slot(k0 + lane)];
+    if (lane < kRun && k0 + lane < n) ml = p.part_ml[slot(k0 + lane)];
     const float now = fmaxf(m, warp_max(ml.x)), old = exp2_whole(m - now);
-    const float f = lane < 8 && k0 + lane < n ? exp2_whole(ml.x - now) : 0.f;
+    const float f = lane < kRun && k0 + lane < n ? exp2_whole(ml.x - now) : 0.f;
     m = now;
     sum *= old;
 #pragma unroll
     for (int e = 0; e < kE; ++e) o[e] *= old;
     const float w = ml.y * f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kRun; ++k) {
       if (k0 + k >= n) break;
       const float fk = __shfl_sync(0xffffffffu, f, k);
       sum += __shfl_sync(0xffffffffu, w, k);
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnPa
     for (int e = 0; e < kE; ++e) o[e] = 0.f;
 #pragma unroll
     for (int k = 0; k < kParts; ++k) {
-      if (8 * k >= n) break;  // (a part without pieces)
+      if (kRun * k >= n) break;  // (a part without pieces)
       const float f = exp2_whole(part_ml[row][k].x - all);
       sum = fmaf(part_ml[row][k].y, f, sum);
 #pragma unroll
