@@ -30,7 +30,7 @@
 // the weights', so these products cannot overlap), with the other half half a
 // turn behind.  Tensor memory is full (two halves of scores and outputs, 128
 // columns each), so there is no third chain.  Measured for two chunks of some
-// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 119.5 us, 620 TFLOP/s,
+// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 118 us, 627 TFLOP/s,
 // tensor pipe 32% and issue slots 58% of active cycles; with one softmax
 // thread a row instead of two 129 us.
 //
