@@ -376,7 +376,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool real = q < g.nrows;
       const int last = real ? g.first + rtok : -1;  // the row sees positions (last - window, last]
       const int see0 = max(g.tlo, last - p.window + 1), see1 = min(g.thi - 1, last);
-      const float qf = c.qf[q] == 0.f ? 1e-30f : c.qf[q];  // (a masked score, -inf, times zero is not -inf)
+      const float qf = c.qf[q];
+      // Factor of a page's scores: with the key scale it may underflow (a row of
+      // zeros has qf near 2^-129, a page of zeros the scale 2^-64), and a masked
+      // score, -inf, times zero is not -inf.  A score is below 2^24 in magnitude,
+      // so what is below 2^-100 multiplies it to nothing all the same.
+      auto score_factor = [&](float ks) {
+        const float f = ks * qf;
+        return f < 0x1p-100f ? 0x1p-100f : f;  // (a NaN stays)
+      };
       float R = 0.f, l = 0.f;
       bool unset = true;  // whether the row has seen no position yet: R is its first maximum
       unsigned nan_d[4] = {0u, 0u, 0u, 0u};  // elements of the output that saw a NaN value
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             float m[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
 #pragma unroll
             for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(x[16 * h + e]));
-            top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), c.kscale[meta][pi] * qf, c.vexp[meta][pi]));
+            top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), score_factor(c.kscale[meta][pi]), c.vexp[meta][pi]));
           }
         }
         if (named_bar_or(pair_bar, 64, top > (unset ? -3.0e38f : R + 7.5f))) {  // (weights are 256 p: FP16 ends below 2^16)
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (64 * sub + 32 * k + 16 * h) >> ps;
-            const float ve = c.vexp[meta][pi], kq = c.kscale[meta][pi] * qf, add = (ve + 8.f) - R;
+            const float ve = c.vexp[meta][pi], kq = score_factor(c.kscale[meta][pi]), add = (ve + 8.f) - R;
             float sum[2] = {0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {

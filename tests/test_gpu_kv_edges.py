@@ -1,0 +1,87 @@
+"""Attention over the paged cache where the range of its intermediate values
+ends: factors of scores that underflow."""
+import pytest
+import torch
+
+import kv_ref as ref
+import skinny_bf16_gemm_residual_gb300 as sgr
+
+pytestmark = pytest.mark.gpu
+FEW, MANY = sgr.SGR_FLAG_KV_FEW_ROWS, sgr.SGR_FLAG_KV_MANY_ROWS
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    torch.cuda.set_device(0)
+    sgr.sgr_init(0)
+    sgr.sgr_device_error(0)
+    yield
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert sgr.sgr_device_error(0) == 0
+
+
+def check(got, want, mag, grid=0.0, what=""):
+    """BF16 rounding (half a step is at most 2^-8 of the value) and, on the sum
+    p |v|, 2^-11 for the weights and 2^-11 for the scores; `grid`: what the
+    smallest step of a weight adds up to."""
+    got = got.double().cpu()
+    bad = ~((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * mag + grid)
+    bad &= ~(got.isnan() & want.isnan())
+    assert not bad.any(), (f"{what}: {int(bad.sum())} of {bad.numel()} off, first {tuple(bad.nonzero()[0].tolist())}: "
+                           f"got {got[bad][0]} want {want[bad][0]}")
+
+
+def values(cache):
+    return [c.float().double().cpu() * s.double().cpu()[:, :, None, None]
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale))]
+
+
+# ------------------------------------------------- factors of the scores near zero
+@pytest.mark.parametrize("flags", [FEW, MANY, 0])
+@pytest.mark.parametrize("window", [0, 37])
+@pytest.mark.parametrize("dim,page,heads,hk", [(128, 64, 8, 2), (64, 16, 3, 1)])
+def test_zero_queries_over_zero_keys(dim, page, heads, hk, window, flags):
+    """A prompt of zeros: the append gives its pages the least scale, every
+    position that a row sees has the same weight, and what it does not see
+    none."""
+    g = torch.Generator().manual_seed(heads)
+    lens, new = [200, 131, 3], [130, 131, 3]
+    pages = [-(-n // page) for n in lens]
+    table = torch.full((3, max(pages)), -1, dtype=torch.int32)
+    for b, n in enumerate(pages):
+        table[b, :n] = torch.arange(sum(pages[:b]), sum(pages[:b]) + n)
+    cache = sgr.KvCache.empty(sum(pages), hk, page, dim)
+    for rows in ([n - m for n, m in zip(lens, new)], new):
+        if rows is not new:  # the earlier positions of the first sequence
+            start = torch.tensor([0, rows[0], rows[0], rows[0]], dtype=torch.int32)
+            length = torch.tensor([rows[0], 0, 0], dtype=torch.int32)
+        else:
+            start = torch.tensor([0] + [sum(new[:i + 1]) for i in range(3)], dtype=torch.int32)
+            length = torch.tensor(lens, dtype=torch.int32)
+        batch = sgr.KvBatch(table.cuda(), length.cuda(), start.cuda(), tokens=int(start[-1]), max_new=max(rows))
+        zero = torch.zeros(batch.tokens, heads + hk, dim, dtype=torch.bfloat16, device="cuda")
+        v = torch.randn(batch.tokens, hk, dim, generator=g).bfloat16().cuda()
+        q = sgr.sgr_kv_append(cache, batch, zero[:, heads:], v, sgr.RopeNorm(), q=zero[:, :heads])
+    assert (cache.k_scale == 2.0 ** -64).all()
+    want, mag = ref.attention(q.cpu(), *values(cache), table, lens, start, page, dim ** -0.5, window)
+    check(sgr.sgr_kv_attention(cache, batch, q, window=window, flags=flags), want, mag)
+
+
+@pytest.mark.parametrize("flags", [FEW, MANY])
+@pytest.mark.parametrize("factor,scale", [(1.0, 0.0), (0.0, 1.0), (2.0 ** -100, -1.0)])
+def test_small_factors_over_small_scales(factor, scale, flags):
+    """Scores of nothing: a scale of zero, queries of (almost) zero, over keys
+    whose pages have the least scale, partly masked."""
+    pr = ref.Problem(128, 32, 2, [300, 40], [70, 9], seed=5)
+    pr.scale[0] = torch.where(pr.scale[0].isnan(), pr.scale[0], 2.0 ** -64)
+    q = (pr.randn(pr.tokens, 6, 128) * factor).bfloat16()
+    for window in (0, 50):
+        want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, scale, window)
+        got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), scale=scale, window=window, flags=flags)
+        check(got, want, mag)
