@@ -12,22 +12,27 @@
 // Both products run on the FP8 tensor core (tcgen05.mma kind::f8f6f4) with
 // the cache's codes as the 128-row operand straight from TMA, so that nothing
 // is converted per cached element.  The small operands are brought into E4M3
-// as two parts b = hi + lo / 32, each row (or tile) scaled by a power of two
-// that puts its largest magnitude in [128, 256]: hi = e4m3(b),
-// lo = e4m3(32 (b - hi)).  That holds 8 significant bits (all of a BF16
-// query) down to 2^-14 of the largest and an absolute 2^-22 of it below.  hi
-// and lo rows sit side by side in the operand (2 NT columns of the
-// accumulator) and are added in FP32.
+// in parts, each the code of 32 times what the one before left.  Queries, each
+// row scaled by a power of two that puts its largest magnitude in [128, 256),
+// have two, b = hi + lo / 32: 8 significant bits (all of a BF16 query) down to
+// 2^-14 of the largest and an absolute 2^-22 of it below.  Weights have three,
+// b = w0 + w1 / 32 + w2 / 1024, off by at most 2^-11 of the weight (half of it
+// from FP16 on the way) down to b = 2^-8 and by 2^-20, half a step, below.  The parts' rows sit side by side in the operand (2 NT or 3 NT
+// columns of the accumulator) and are added in FP32.
 //
 // Softmax: weights are 2^(s' - R) with a whole number R for each column that
 // only moves, up, when a score exceeds it (one vote of the four warps a tile;
 // then the tile's maxima are found), so what came before is rescaled seldom
 // and by a power of two: exactly.  The product of a tile is read back and
 // accumulated in registers (thread d holds o[.][d]); no accumulator in tensor
-// memory is ever rescaled.  Weights are 256 p in hi and lo: 8 bits down to
-// p = 2^-14, 4 bits to 2^-19, nothing below 2^-23 of the largest so far.  A
-// page's key scale multiplies the score; its value scale 2^e is added to the
-// exponent of P and taken out of the sum of weights again.
+// memory is ever rescaled.  A page's key scale multiplies the score; its value
+// scale 2^e is added to the exponent of P and taken out of the sum of weights
+// again, so a weight is p times its page's value scale.  The largest is at 2^6
+// or above once R has moved: a weight is good to 2^-11 down to 2^-14 of the
+// largest and to 2^-26 of the largest below, and n weights far below it are
+// off by n 2^-26 of it together at most, less than BF16's rounding up to some
+// 2^17 positions.  (Two parts leave 2^-21: of 131071 equal weights 2^-20
+// of the largest, an eighth of the sum, a third was lost.)
 //
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile, where there are enough of them: 96 sequences of up to 16384 (64
@@ -57,15 +62,17 @@ struct AttnShape {
   static constexpr int kSoftmax = 4 * kGroups;
   static constexpr int kThreads = 32 * (kSoftmax + 4);
   static constexpr int kCtas = NT > 24 ? 1 : 2;  // an SM
-  static constexpr int kCols = 2 * NT;  // hi and lo rows of the small operands
+  static constexpr int kCols = 2 * NT;                     // the queries' two parts
+  static constexpr int kWCols = (3 * NT + 15) / 16 * 16;  // the weights' three (the product's width is a multiple of 16)
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kStageBytes = 2 * kTileBytes;  // V, then K
   // As many stages and query buffers as kCtas an SM allow.
   static constexpr int kStages = D == 128 ? (NT == 32 ? 5 : NT == 24 ? 2 : 3) : (NT == 32 ? 8 : NT == 8 ? 6 : 5);
   static constexpr int kQBufs = D == 128 && NT == 16 ? 2 : D == 128 && NT == 32 ? 3 : D == 64 && NT == 24 ? 2 : 4;
-  static constexpr int kPBytes = kCols * kAttnTile;
+  static constexpr int kPBytes = kWCols * kAttnTile;
   static constexpr int kQBytes = kCols * D;
-  static constexpr int kTmemCols = NT == 24 ? 256 : 4 * kCols;  // S and O, two each (a power of two)
+  static constexpr int kTmemCols = NT == 8 ? 128 : NT < 32 ? 256 : 512;  // S and O, two each (a power of two)
+  static_assert(kTmemCols >= 2 * (kCols + kWCols), "two accumulators of each product");
 };
 
 template <int D, int NT>
@@ -98,7 +105,7 @@ constexpr int attn_ctl_bytes() {
 template <int D, int NT>
 constexpr int attn_smem_bytes() {
   using S = AttnShape<D, NT>;
-  return 1024 + attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + S::kQBufs * S::kQBytes;
+  return attn_ctl_bytes<D, NT>() + S::kStages * S::kStageBytes + S::kPBytes + S::kQBufs * S::kQBytes;
 }
 
 // Sums of C columns over the warp's lanes: lane l returns column l / (32 / C).
@@ -122,21 +129,24 @@ __device__ __forceinline__ float warp_column_sums(float (&x)[C]) {
 
 constexpr float kLoScale = 1.f / 32.f;
 
-// Two values in [0, 256] -> their hi codes (bytes 0, 1) and lo codes (bytes 2,
-// 3).  (FP16 holds b to 11 bits, b - hi exactly.)
-__device__ __forceinline__ uint32_t split2(float a, float b) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 x, y;\n\t"
-      "cvt.rn.f16x2.f32 x, %2, %1;\n\t"
+// Two values in [0, 256] -> their codes in three parts, one pair of bytes each:
+// b = w0 + w1 / 32 + w2 / 1024.  (FP16 holds b to 11 bits, the rests exactly.)
+__device__ __forceinline__ void split3(float a, float b, uint32_t& w01, uint32_t& w2) {
+  asm("{\n\t.reg .b16 h, l, m;\n\t.reg .b32 x, y;\n\t"
+      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 h, x;\n\t"
       "cvt.rn.f16x2.e4m3x2 y, h;\n\t"
       "sub.rn.f16x2 x, x, y;\n\t"
-      "mul.rn.f16x2 x, x, %3;\n\t"
+      "mul.rn.f16x2 x, x, %4;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n\t"
-      "mov.b32 %0, {h, l};\n\t}"
-      : "=r"(r)
+      "cvt.rn.f16x2.e4m3x2 y, l;\n\t"
+      "sub.rn.f16x2 x, x, y;\n\t"
+      "mul.rn.f16x2 x, x, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 m, x;\n\t"
+      "mov.b32 %0, {h, l};\n\t"
+      "mov.b32 %1, {m, m};\n\t}"
+      : "=r"(w01), "=r"(w2)
       : "f"(a), "f"(b), "r"(0x50005000u));  // 0x5000 = 32
-  return r;
 }
 
 // x[q] = hi[q] + lo[q] / 32 of C accumulator columns at `hi`, the lo ones
@@ -150,14 +160,34 @@ __device__ __forceinline__ void tmem_ld_sum(uint32_t hi, uint32_t apart, float (
   for (int q = 0; q < 8; ++q) x[q] = fmaf(w[q], kLoScale, v[q]);
 }
 
+// The same of three parts, w0 + w1 / 32 + w2 / 1024.
+template <int C>
+__device__ __forceinline__ void tmem_ld_sum3(uint32_t w0, uint32_t apart, float (&x)[C]) {
+  static_assert(C == 8, "the load of three runs of 8 columns");
+  float v[8], w[8];
+  tmem_ld8x3(w0, w0 + apart, w0 + 2 * apart, x, v, w);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) x[q] = fmaf(fmaf(w[q], kLoScale, v[q]), kLoScale, x[q]);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::kCtas)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Sh = AttnShape<D, NT>;
-  constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC, kCols = Sh::kCols, kSoftmax = Sh::kSoftmax;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  AttnCtl<D, NT>& c = *reinterpret_cast<AttnCtl<D, NT>*>(smem_raw + (base - raw));
+  constexpr int S = Sh::kStages, Q = Sh::kQBufs, C = Sh::kC, kCols = Sh::kCols, kWCols = Sh::kWCols, kSoftmax = Sh::kSoftmax;
+  // (aligned by its declaration: room to align it by hand would cost 16-row
+  // tiles of D = 128 their second CTA an SM)
+  extern __shared__ __align__(1024) unsigned char attn_smem[];
+  const uint32_t base = smem_u32(attn_smem);
+  if (base & 1023u) {  // swizzled operands could not be read
+    pdl_wait();
+    if (threadIdx.x == 0) {
+      report_error(p.err, kErrSmemAlign);
+      p.pieces[blockIdx.x] = AttnPiece{};  // (nothing to join)
+    }
+    return;
+  }
+  AttnCtl<D, NT>& c = *reinterpret_cast<AttnCtl<D, NT>*>(attn_smem);
   const uint32_t ring = base + attn_ctl_bytes<D, NT>();
   const uint32_t pbuf = ring + S * Sh::kStageBytes, qbuf = pbuf + Sh::kPBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -212,7 +242,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     // whose weights are written, or K Q^T of the next one.  Neither waits for
     // the other's inputs.
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(kAttnTile, kCols), idesc_o = idesc_s | (1u << 15);
+      constexpr uint32_t idesc_s = idesc_e4m3_f32(kAttnTile, kCols), idesc_o = idesc_e4m3_f32(kAttnTile, kWCols) | (1u << 15);
       const uint32_t acc_o = tmem + 2 * kCols;
       int sq = 0, filled = -1, t = 0, t_end = 0;  // segments read, query buffer in use, its tiles
       int i = 0, islot = 0, k = 0, kslot = 0;     // tiles scored, tiles weighted
@@ -230,7 +260,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           const uint64_t pd = smem_desc_rows<128>(pbuf);
 #pragma unroll
           for (int kk = 0; kk < kAttnTile / 32; ++kk)
-            mma_e4m3(acc_o + (k & 1) * kCols, vd + (uint64_t)(kk * (32 * D >> 4)), pd + (uint64_t)(kk * 2), idesc_o, kk > 0);
+            mma_e4m3(acc_o + (k & 1) * kWCols, vd + (uint64_t)(kk * (32 * D >> 4)), pd + (uint64_t)(kk * 2), idesc_o, kk > 0);
           mma_commit(smem_u32(&c.ofull[k & 1]));
           mma_commit(smem_u32(&c.empty[kslot]));
           ++k;
@@ -389,7 +419,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
     auto accumulate = [&](int k, bool scaled) {
       tc_fence_after();
       float x[C];
-      tmem_ld_sum<C>(lane_base + 2 * kCols + (k & 1) * kCols, NT, x);
+      tmem_ld_sum3<C>(lane_base + 2 * kCols + (k & 1) * kWCols, NT, x);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.oempty[k & 1]));
@@ -528,12 +558,16 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         const uint32_t col = (uint32_t)(tok & 15), chunk = tok >> 4;
 #pragma unroll
         for (int q = 0; q < C; q += 2) {
-          const uint32_t u = split2(x[q], x[q + 1]);
-          // (q0 is a multiple of 8: it does not change the swizzle)
-          sts8(pbuf + q0 * 128 + swizzled<128>(q, chunk) + col, u);
-          sts8(pbuf + q0 * 128 + swizzled<128>(q + 1, chunk) + col, u >> 8);
-          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q, chunk) + col, u >> 16);
-          sts8(pbuf + (NT + q0) * 128 + swizzled<128>(q + 1, chunk) + col, u >> 24);
+          uint32_t u, m;
+          split3(x[q], x[q + 1], u, m);
+          // (q0 and NT are multiples of 8: they do not change the swizzle)
+          const uint32_t at0 = pbuf + q0 * 128 + swizzled<128>(q, chunk) + col, at1 = pbuf + q0 * 128 + swizzled<128>(q + 1, chunk) + col;
+          sts8(at0, u);
+          sts8(at1, u >> 8);
+          sts8(at0 + NT * 128, u >> 16);
+          sts8(at1 + NT * 128, u >> 24);
+          sts8(at0 + 2 * NT * 128, m);
+          sts8(at1 + 2 * NT * 128, m >> 8);
         }
         fence_proxy_async_smem();
         __syncwarp();

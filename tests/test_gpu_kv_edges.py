@@ -1,5 +1,8 @@
 """Attention over the paged cache where the range of its intermediate values
-ends: factors of scores that underflow."""
+ends: factors of scores that underflow, weights far below the largest, errors
+of all outputs together."""
+import math
+
 import pytest
 import torch
 
@@ -85,3 +88,56 @@ def test_small_factors_over_small_scales(factor, scale, flags):
         want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, scale, window)
         got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), scale=scale, window=window, flags=flags)
         check(got, want, mag)
+
+
+# ---------------------------------------------------------------- range of the weights
+@pytest.mark.parametrize("flags", [FEW, MANY])
+@pytest.mark.parametrize("heads", [1, 20])
+def test_long_flat_tail_far_below_one_position(heads, flags):
+    """One position of no value 14 nats above 131071 others that hold an
+    eighth of the weight together, a whole sequence to each CTA: the others
+    still add up."""
+    n, dim, page = 131072, 64, 128
+    g = torch.Generator().manual_seed(1)
+    pages = n // page
+    k = torch.zeros(pages, 1, page, dim)
+    k[..., 0] = 0.375
+    k[0, 0, 0, :2] = torch.tensor([14.0, 0.25])
+    v = (1 + 0.25 * torch.randn(pages, 1, page, dim, generator=g)).to(torch.float8_e4m3fn)
+    v[0, 0, 0] = 0.0
+    scales = torch.ones(2, pages, 1)
+    cache = sgr.KvCache(k.to(torch.float8_e4m3fn).cuda(), v.cuda(), scales[0].cuda(), scales[1].cuda())
+    table = torch.arange(pages, dtype=torch.int32).view(1, pages)
+    batch = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    q = torch.zeros(batch, heads, dim)
+    q[..., :2] = 1.0
+    q = q.bfloat16()
+    want, mag = ref.attention(q[:1, :1], k.double(), v.double(), table, [n], None, page, 1.0, 0)
+    assert 0.07 < float(want.mean()) < 0.15
+    on = sgr.KvBatch(table.expand(batch, -1).contiguous().cuda(), torch.full((batch,), n, dtype=torch.int32).cuda())
+    got = sgr.sgr_kv_attention(cache, on, q.cuda(), scale=1.0, flags=flags)
+    # Weights below 2^-17 of the largest are multiples of 2^-25 of it: half of that each
+    check(got, want.expand(batch, heads, -1), mag.expand(batch, heads, -1), grid=n * 2.0 ** -26)
+
+
+# -------------------------------------------------------------- all outputs together
+@pytest.mark.parametrize("dim,page,heads,hk,lens,new,size", [
+    (128, 64, 28, 4, [3000, 1201, 77], [1, 1, 1], 1.0),
+    (128, 64, 28, 4, [3000, 1201, 77], [1, 1, 1], 0.0),
+    (64, 32, 32, 8, [2500, 640], [5, 3], 2.0),
+    (128, 32, 14, 2, [900, 1500], [100, 70], 1.0),
+])
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_root_mean_square_error(dim, page, heads, hk, lens, new, size, flags):
+    """Of all outputs of a case: that of rounding them to BF16, and 2^-11 each
+    of the outputs' own size for the weights and for the scores."""
+    pr = ref.Problem(dim, page, hk, lens, new, seed=dim + heads)
+    q = (size * pr.randn(pr.tokens, heads, dim)).bfloat16()
+    want, _ = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, page, dim ** -0.5, 0)
+    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), flags=flags).double().cpu()
+
+    def rms(x):
+        return float(x.square().mean().sqrt())
+
+    bound = math.sqrt(rms(want.bfloat16().double() - want) ** 2 + 2 * (2.0 ** -11 * rms(want)) ** 2)
+    assert rms(got - want) <= 1.02 * bound
