@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         float top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < C; ++q) top = fmaxf(top, x[q] - c.ref[warp][q]);
-        const bool scaled = named_bar_or(1 + group, 128, top > 8.8f);  // E4M3 ends at 448 = 2^8.8
+        const bool scaled = named_bar_or(1 + group, 128, top > 8.f);  // the most that the lower parts have room for: 32 times a rest of 8
         if (__builtin_expect(scaled, 0)) {
           // R of the columns that are exceeded moves one above the tile's
           // maximum (room for the next tiles); lane q keeps column q's.
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           if (lane < C) {
             const int w0 = warp & ~3;
             top = fmaxf(fmaxf(c.wmax[w0][lane], c.wmax[w0 + 1][lane]), fmaxf(c.wmax[w0 + 2][lane], c.wmax[w0 + 3][lane]));
-            const float now = top - run > 8.8f ? ceilf(top) - 7.f : run;
+            const float now = top - run > 8.f ? ceilf(top) - 7.f : run;
             c.alpha[warp][sb][lane] = exp2_whole(run - now);
             c.ref[warp][lane] = run = now;
           }

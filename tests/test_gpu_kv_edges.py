@@ -1,6 +1,6 @@
 """Attention over the paged cache where the range of its intermediate values
-ends: factors of scores that underflow, weights far below the largest, errors
-of all outputs together."""
+ends: factors of scores that underflow, weights at the top of a code's range
+and far below the largest, errors of all outputs together."""
 import math
 
 import pytest
@@ -91,6 +91,36 @@ def test_small_factors_over_small_scales(factor, scale, flags):
 
 
 # ---------------------------------------------------------------- range of the weights
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_later_score_above_the_largest_so_far(flags):
+    """A position of the second tile that takes most of the weight, 1.5 to 2.8
+    binades above the one that set the reference in the first."""
+    bits = [1.5 + 0.02 * i for i in range(64)]
+    n, dim = 129, 64
+    k, v = torch.zeros(n, 1, dim), torch.zeros(n, 1, dim)
+    k[:, 0, 2] = -224.0  # no weight
+    k[0, 0, :3] = torch.tensor([1.0, 0.0, 0.0])
+    k[n - 1, 0, :3] = torch.tensor([0.0, 1.0, 0.0])
+    v[n - 1] = 1.0 + torch.arange(dim) / 64.0
+    v[1] = v[n - 1]  # (both pages with one scale)
+    cache = sgr.KvCache.empty(2, 1, 128, dim)
+    table = torch.arange(2, dtype=torch.int32).view(1, 2)
+    whole = sgr.KvBatch(table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(),
+                        torch.tensor([0, n], dtype=torch.int32).cuda(), tokens=n, max_new=n)
+    sgr.sgr_kv_append(cache, whole, k.bfloat16().cuda(), v.bfloat16().cuda(), sgr.RopeNorm())
+    q = torch.zeros(1, len(bits), dim)
+    q[0, :, 0] = 0.01 * math.log(2)  # just above a whole number of binades
+    q[0, :, 1] = torch.tensor(bits) * math.log(2)
+    q[0, :, 2] = 1.0
+    q = q.bfloat16()
+    for heads in (1, 8, 13, 24, 64):  # row tiles of every size
+        for first in range(0, len(bits), heads):
+            x = q[:, first:first + heads].contiguous()
+            want, mag = ref.attention(x, *values(cache), table, [n], None, 128, 1.0, 0)
+            got = sgr.sgr_kv_attention(cache, sgr.KvBatch(table.cuda(), whole.seq_len), x.cuda(), scale=1.0, flags=flags)
+            check(got, want, mag, what=f"heads {first}..")
+
+
 @pytest.mark.parametrize("flags", [FEW, MANY])
 @pytest.mark.parametrize("heads", [1, 20])
 def test_long_flat_tail_far_below_one_position(heads, flags):
