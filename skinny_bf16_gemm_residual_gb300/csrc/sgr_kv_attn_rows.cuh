@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const bool real = q < g.nrows;
       const int last = real ? g.first + rtok : -1;  // the row sees positions (last - window, last]
       const int see0 = max(g.tlo, last - p.window + 1), see1 = min(g.thi - 1, last);
-      const float qf = c.qf[q];
+      // (a padding row's scores are all -inf: its query, NaN perhaps, has no part in them)
+      const float qf = see0 <= see1 ? c.qf[q] : 0.f;
       // Factor of a page's scores: with the key scale it may underflow (a row of
       // zeros has qf near 2^-129, a page of zeros the scale 2^-64), and a masked
       // score, -inf, times zero is not -inf.  A score is below 2^24 in magnitude,

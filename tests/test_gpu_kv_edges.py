@@ -1,6 +1,7 @@
 """Attention over the paged cache where the range of its intermediate values
-ends: factors of scores that underflow, weights at the top of a code's range
-and far below the largest, errors of all outputs together."""
+ends: factors of scores that underflow, rows that see nothing, weights at the
+top of a code's range and far below the largest, errors of all outputs
+together."""
 import math
 
 import pytest
@@ -88,6 +89,25 @@ def test_small_factors_over_small_scales(factor, scale, flags):
         want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, scale, window)
         got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), scale=scale, window=window, flags=flags)
         check(got, want, mag)
+
+
+# --------------------------------------------------------------- rows that see nothing
+@pytest.mark.parametrize("flags", [FEW, MANY])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, 3e38])
+def test_padding_rows_get_zeros_whatever_their_query(bad, window, flags):
+    """Rows before a sequence's first position, next to rows of the same tile
+    that see something."""
+    pr = ref.Problem(64, 32, 1, [200, 6], [220, 9], seed=7)
+    q = pr.randn(pr.tokens, 3, 64).bfloat16()
+    for first, n in ((0, 20), (220, 3)):
+        q[first:first + n, :, 5] = bad
+    clean = torch.where(q.isfinite() & (q.abs() < 1e30), q, 0.0)
+    want, mag = ref.attention(clean, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, pr.q_start, 32, 0.125, window)
+    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr), q.cuda(), window=window, flags=flags)
+    assert (want[:20] == 0).all() and (want[220:223] == 0).all()
+    assert (got[:20] == 0).all() and (got[220:223] == 0).all()
+    check(got, want, mag)
 
 
 # ---------------------------------------------------------------- range of the weights
