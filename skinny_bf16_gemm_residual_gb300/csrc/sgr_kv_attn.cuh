@@ -78,6 +78,24 @@ __device__ __forceinline__ int div_group(const AttnParams& p, int r) {
   return q + (r - q * p.group >= p.group ? 1 : 0);
 }
 
+// The last position that the tok-th row of a sequence sees, its own: -1 for any
+// padding row, so that last - window (2^31 - 1 for none) stays within 32 bits.
+__host__ __device__ __forceinline__ int row_last(int first, int tok) {
+  const int pos = first + tok;
+  return pos < -1 ? -1 : pos;
+}
+
+// Whether a row sees a position, (last - window, last].
+__host__ __device__ __forceinline__ bool row_sees(int pos, int last, int window) {
+  return pos <= last && pos > last - window;
+}
+
+// The first position that a row sees of its row tile's, from tlo on.
+__host__ __device__ __forceinline__ int row_first(int tlo, int last, int window) {
+  const int lo = last - window + 1;
+  return lo < tlo ? tlo : lo;
+}
+
 template <int NT>
 __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, const KvSeq& s, int j) {
   AttnItem it;

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         out_at = 0;
         if (q < g.nrows) {
           const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
-          pos = g.first + tok;
+          pos = row_last(g.first, tok);
           out_at = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
           v = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         }
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
 #pragma unroll
           for (int q = 0; q < C; ++q) {
             const int last = c.qpos[buf][q0 + q];
-            if (!(live && pos <= last && pos > last - p.window)) x[q] = -INFINITY;
+            if (!(live && row_sees(pos, last, p.window))) x[q] = -INFINITY;
           }
         } else if (!live) {
 #pragma unroll
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
                 if ((lds8(vt + swizzled<D>(k, tok >> 4) + (tok & 15)) & 0x7F) != 0x7F) continue;
                 for (int q = 0; q < C; ++q) {
                   const int last = c.qpos[buf][q0 + q], kp = t * kAttnTile + k;
-                  if (kp <= last && kp > last - p.window) nan_rows |= 1u << q;
+                  if (row_sees(kp, last, p.window)) nan_rows |= 1u << q;
                 }
               }
               __syncwarp();

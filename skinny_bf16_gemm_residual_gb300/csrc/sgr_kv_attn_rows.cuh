@@ -374,8 +374,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       const int q = 128 * half + row, r = g.r0 + q, rtok = div_group(p, r);
       const bool real = q < g.nrows;
-      const int last = real ? g.first + rtok : -1;  // the row sees positions (last - window, last]
-      const int see0 = max(g.tlo, last - p.window + 1), see1 = min(g.thi - 1, last);
+      const int last = real ? row_last(g.first, rtok) : -1;
+      const int see0 = row_first(g.tlo, last, p.window), see1 = min(g.thi - 1, last);
       // (a padding row's scores are all -inf: its query, NaN perhaps, has no part in them)
       const float qf = see0 <= see1 ? c.qf[q] : 0.f;
       // Factor of a page's scores: with the key scale it may underflow (a row of
