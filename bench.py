@@ -19,7 +19,8 @@ Per-M microseconds per call (median of repeats, the page's summary) are in
 each M.  `transition` times every kernel path at M = 32, 64, 128 and
 `compute_bound` the library's choice at M = 256, 512, 1024 against the BF16
 tensor peak, both with the same comparator (the page's `addmm` backend and
-`graph_samples` method).
+`graph_samples` method).  The line has each leg's microseconds only, so that
+it stays a few kilobytes; the legs in full go to stderr, one JSON line too.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 
@@ -343,6 +344,38 @@ def call_metrics(M: int, s: dict, peaks: dict) -> dict:
             "frac_of_tensor_peak_sustained": tflops / peaks["bf16_tflops_sustained"],
             "roofline_us": roof_us, "frac_of_roofline": roof_us / us,
             "bound": "tensor" if tensor_bound(M, peaks) else "hbm"}
+
+
+LEGS = ("per_m", "transition", "compute_bound", "chain", "grouped", "w8", "w4", "down_projection")
+
+
+def short_line(line: dict):
+    """The result line with its secondary legs cut to their times (us, by M),
+    and the legs in full."""
+    legs = {k: line[k] for k in LEGS if line.get(k) is not None}
+
+    def us(x):
+        return float(f"{x:.5g}")
+
+    def times(m):
+        out = {"us": us(m["us_per_call"])}
+        if "cublas_addmm" in m:
+            out["cublas_us"] = us(m["cublas_addmm"]["us_per_call"])
+        return out
+
+    def sweep(leg):
+        return {M: {"path": e["library_choice"], **times({**e["paths"]["auto"], "cublas_addmm": e["paths"]["cublas_addmm"]})}
+                for M, e in leg.items()}
+
+    cut = {"per_m": lambda leg: {M: {**times(m), "gbs": us(m["gbs"]), "path": m["path"]} for M, m in leg.items()},
+           "transition": sweep, "compute_bound": sweep,
+           "chain": lambda leg: {k: us(leg[k]) for k in ("us_per_layer", "us_per_layer_no_pdl")},
+           "grouped": lambda leg: {k: us(leg[k]) for k in ("us_grouped", "us_per_expert_calls")},
+           "w8": lambda leg: {str(m["m"]): us(m["us"]) for m in leg["per_m"]},
+           "down_projection": lambda leg: {str(m["m"]): {"us": us(m["us"]), "cublas_us": us(m["cublas_addmm_us"])}
+                                           for m in leg["per_m"]}}
+    cut["w4"] = cut["w8"]
+    return {k: cut[k](v) if k in legs else v for k, v in line.items()}, legs
 
 
 def addmm_calls(A, Ws, Rs, Ys, stream):
@@ -687,6 +720,8 @@ def run_ours(args):
         "peaks": {"hbm_gbs": peaks["hbm_gbs"], "bf16_tflops": peaks["bf16_tflops"],
                   "bf16_tflops_sustained": peaks["bf16_tflops_sustained"], "source": peak_src},
     }
+    line, legs = short_line(line)
+    print(json.dumps(legs), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
     if ws > 1:
         import torch.distributed as dist
