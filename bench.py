@@ -20,7 +20,7 @@ each M.  `transition` times every kernel path at M = 32, 64, 128 and
 `compute_bound` the library's choice at M = 256, 512, 1024 against the BF16
 tensor peak, both with the same comparator (the page's `addmm` backend and
 `graph_samples` method).  The line has each leg's microseconds only, so that
-it stays a few kilobytes; the legs in full go to stderr, one JSON line too.
+it stays a few kilobytes; the legs in full go to stderr, one line too.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
 
@@ -721,7 +721,7 @@ def run_ours(args):
                   "bf16_tflops_sustained": peaks["bf16_tflops_sustained"], "source": peak_src},
     }
     line, legs = short_line(line)
-    print(json.dumps(legs), file=sys.stderr, flush=True)
+    print("legs: " + json.dumps(legs), file=sys.stderr, flush=True)
     print(json.dumps(line), flush=True)
     if ws > 1:
         import torch.distributed as dist

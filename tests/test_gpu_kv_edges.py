@@ -191,3 +191,24 @@ def test_root_mean_square_error(dim, page, heads, hk, lens, new, size, flags):
 
     bound = math.sqrt(rms(want.bfloat16().double() - want) ** 2 + 2 * (2.0 ** -11 * rms(want)) ** 2)
     assert rms(got - want) <= 1.02 * bound
+
+
+@pytest.mark.parametrize("flags", [FEW, MANY])
+def test_one_position_takes_all_the_weight(flags):
+    """Scores of thousands: the value of the largest, wherever it is ahead by
+    more than 12 and twice a score's error (2^-16 of |q| |k| scale)."""
+    pr = ref.Problem(128, 64, 2, [3000, 500, 130], [1, 1, 1], seed=3)
+    q = (1e4 * pr.randn(3, 8, 128)).bfloat16()
+    want, mag = ref.attention(q, pr.values(0), pr.values(1), pr.block_table, pr.seq_len, None, 64, 128 ** -0.5, 0)
+    got = sgr.sgr_kv_attention(pr.cache(sgr), pr.batch(sgr, False), q.cuda(), flags=flags).double().cpu()
+    checked = 0
+    for b, n in enumerate(pr.lens):
+        t = torch.arange(n)
+        k = pr.values(0)[pr.block_table[b].long()[t // 64], :, t % 64]  # [n, heads, dim]
+        score = torch.einsum("kgd,tkd->kgt", q[b].double().view(2, 4, 128), k).reshape(8, n) * 128 ** -0.5
+        top = score.topk(2, -1).values
+        error = 2.0 ** -16 * q[b].double().norm(dim=-1) * k.norm(dim=-1).max() * 128 ** -0.5
+        ahead = top[:, 0] - top[:, 1] > 12 + 2 * error
+        check(got[b][ahead], want[b][ahead], mag[b][ahead])
+        checked += int(ahead.sum())
+    assert checked >= 12
