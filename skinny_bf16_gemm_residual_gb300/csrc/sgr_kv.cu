@@ -428,24 +428,29 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
     return c.heads * (each < all ? each : all);
   };
   // Row tiles as small as the rows of a sequence allow: the small operands and
-  // accumulators are 2 nt columns wide, and so is the softmax work a tile
-  // (five drafted tokens and four heads a key/value head: 29.6 us in a tile of
-  // 24 against 34.0 in one of 32).
+  // accumulators are 2 and 3 nt columns wide, and so is the softmax work a tile
+  // (five drafted tokens and four heads a key/value head: 29.1 us in a tile of
+  // 24 against 33.9 in one of 32).
   a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
-  // The 256-row kernel takes some 2.2 times a 32-row unit's time for eight
-  // times the rows, but 12 units' time to begin and end.  Measured with 28
-  // heads over 4, small tiles against 256 rows: 18.1 and 20.3 us (4 sequences
-  // of 3000, 126 rows a head each), 45.0 and 33.0 (16 of them), 22.3 and 30.8
-  // (one, 700 rows), 74 and 48 (one, 4200 rows), 97.7 and 63.2 (one of 30000,
-  // 700 rows), 90 and 99 (32 of 9000, 63 rows), 145 and 108 (112 rows).
-  const bool gains = rows > 64 && (double)tiles * ((double)row_tiles(32) - 2.2 * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms;
+  // The 256-row kernel takes some 1.75 times (D = 64: 2.4 times) a 32-row
+  // unit's time for eight times the rows, but 12 units' time to begin and end.
+  // Measured with 28 heads of 128 over 4, small tiles against 256 rows: 19.1
+  // and 21.4 us (8 sequences of 3000, 35 rows a head each), 122.9 and 109.8 (96
+  // of them), 19.4 and 20.4 (4 of 3000, 126 rows), 51.6 and 32.6 (16 of them),
+  // 24.1 and 30.9 (one, 700 rows), 84 and 47 (one, 4200 rows), 113.0 and 63.4
+  // (one of 30000, 700 rows), 102.8 and 99 (32 of 9000, 63 rows), 166 and 107
+  // (112 rows); 32 heads of 64 over 8: 116 and 146 (32 of 9000, 36 rows), 47.5
+  // and 36.9 (3 of 20000, 96 rows).
+  const double unit = c.head_dim == 64 ? 2.4 : 1.75;
+  const bool gains = (double)tiles * ((double)row_tiles(32) - unit * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms;
   if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);
   // Short caches are not split over CTAs: the join's launch costs more than a
-  // few tiles in turn.  28 heads over 4, split and whole: 8.5 and 8.5 us (one
-  // sequence of 4 tiles), 14.3 and 11.3 (64 of them), 9.4 and 11.9 (one of 8),
-  // 17.7 and 15.7 (64: as many row tiles as CTAs, nearly), 25.0 and 27.1 (128).
+  // few tiles in turn.  28 heads over 4, split and whole: 8.6 and 8.1 us (one
+  // sequence of 3 tiles), 8.7 and 9.0 (of 4), 14.7 and 11.5 (64 of them), 9.6
+  // and 12.6 (one of 8), 18.3 and 16.3 (64: as many row tiles as CTAs, nearly),
+  // 27.4 and 29.1 (128).
   a.split = tiles > (2 * items >= ctas && items <= ctas ? 8 : 4);
   const long long units = a.split ? items * (tiles + 1) : items;
   a.fits = units < (1LL << 31) && tiles < (1 << 24);

@@ -17,8 +17,9 @@
 // have two, b = hi + lo / 32: 8 significant bits (all of a BF16 query) down to
 // 2^-14 of the largest and an absolute 2^-22 of it below.  Weights have three,
 // b = w0 + w1 / 32 + w2 / 1024, off by at most 2^-11 of the weight (half of it
-// from FP16 on the way) down to b = 2^-8 and by 2^-20, half a step, below.  The parts' rows sit side by side in the operand (2 NT or 3 NT
-// columns of the accumulator) and are added in FP32.
+// from FP16 on the way) down to b = 2^-8 and by 2^-20, half a step, below.  The
+// parts' rows sit side by side in the operand (2 NT or 3 NT columns of the
+// accumulator) and are added in FP32.
 //
 // Softmax: weights are 2^(s' - R) with a whole number R for each column that
 // only moves, up, when a score exceeds it (one vote of the four warps a tile;
@@ -37,11 +38,11 @@
 // Bound: the cache bytes, 2 D a token and key/value head, each read once per
 // row tile, where there are enough of them: 96 sequences of up to 16384 (64
 // heads over 8, 1.63 GB) 240 us, 6.8 TB/s, a plain copy's rate; one of 200003
-// (410 MB) 68 us.  With fewer bytes the CTAs' beginning (5 us: launch, tensor
+// (410 MB) 70 us.  With fewer bytes the CTAs' beginning (5 us: launch, tensor
 // memory, first page, first run of the code) and the join (3 us): 32 sequences
-// of up to 4096 (28 heads over 4, 60.6 MB) 18.9 us, one of 333 7.8 us.  With
-// more rows a head the softmax: 20 rows (D = 64, 38.7 MB) 27 us, issue slots
-// 59% taken.
+// of up to 4096 (28 heads over 4, 60.6 MB) 19.4 us, one of 333 8.2 us.  With
+// more rows a head the softmax: 20 rows (D = 64, 38.7 MB) 29 us, issue slots
+// 61% taken.  (Of which the weights' third part 0.4 us with 8 rows, 2 with 20.)
 //
 // Roles: a group of 4 softmax warps for every 8 rows (thread = token, then =
 // element d), one warp that walks the work, loads pages by TMA and hands out
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   } else if (warp >= kSoftmax + 2) {
     // ----------------------------------------------------------- query operand
     // First a dry run over no rows: a CTA's first run of this code waits for
-    // its instructions, on the way to the first scores (8.0 against 9.6 us for
+    // its instructions, on the way to the first scores (8.2 against 9.8 us for
     // one short sequence).  Dry runs of the other roles gained nothing.
     constexpr int kLanes = D / 8, kRows = 64 / kLanes, kPass = NT / kRows;
     const int qt = tid - 32 * (kSoftmax + 2), l = qt % kLanes;

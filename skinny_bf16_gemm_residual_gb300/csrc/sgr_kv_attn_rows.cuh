@@ -29,7 +29,7 @@
 // product, its completion and the next scores (2100; the scores' columns are
 // the weights', so these products cannot overlap), with the other half half a
 // turn behind.  Tensor memory is full (two halves of scores and outputs, 128
-// columns each), so there is no third chain.  Measured for two chunks of some
+// columns each): a third chain would take scores of fewer tokens at a time.  Measured for two chunks of some
 // 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 118 us, 627 TFLOP/s,
 // tensor pipe 32% and issue slots 58% of active cycles; with one softmax
 // thread a row instead of two 129 us.
