@@ -14,8 +14,10 @@
  *   attention         o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale q.k_t),
  *                     over the positions t that the query's token may see
  *
- * All of it is computed in 32 bits (sums, norms, softmax statistics) and
- * rounded once to BF16 or E4M3.
+ * Sums, norms and softmax statistics are held in 32 bits, and results are
+ * rounded once to BF16 or E4M3.  Attention's two products run on the tensor
+ * core, which sees queries and weights in fewer bits: sgr_kv_attention says how
+ * many.
  *
  * Pointers are device pointers owned by the caller; structures are host
  * memory, read during the call only.  Calls enqueue work on `stream`, return
@@ -31,7 +33,8 @@
  * a length beyond the block table, a position beyond the rotation table, row
  * offsets that run backwards or past `tokens` -- is never followed: the
  * kernel clamps or skips it and records code 7 in the device error word
- * (sgr_device_error).
+ * (sgr_device_error).  (Code 8: a block's shared memory did not begin where the
+ * kernel needs it; nothing was computed.)
  */
 #ifndef SGR_ATTENTION_H
 #define SGR_ATTENTION_H
@@ -98,6 +101,8 @@ typedef struct {
  * row: seq_len 0) is not appended, its rotated query and its attention output
  * are zeros.  Rows that no sequence has (q_start[batch] below tokens) are left
  * as they are.  Entries of block_table beyond a sequence's length are not read.
+ * The kernel and split of sgr_kv_attention are chosen by max_pages and max_new:
+ * any upper bounds are right, close ones fast.
  */
 typedef struct {
   const int* block_table; /* [batch, max_pages], row stride table_stride */
@@ -162,8 +167,11 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
  * whatever they hold.  `scale` multiplies the scores (1/sqrt(head_dim) as a
  * rule).  The tensor core sees a query's elements to 2^-18 of its row's largest
  * (with their 8 bits down to 2^-9 of it at least), so a score is good to some
- * 2^-16 of |q| |k| scale, and weights to 8 bits down to 2^-14 of the largest and
- * 2^-19 of it below.  workspace: device memory of sgr_kv_attention_workspace() bytes,
+ * 2^-16 of |q| |k| scale.  Weights, each times the value scale of its page, are
+ * good to 2^-11 of themselves down to 2^-14 of the row's largest so far, and to
+ * 2^-26 of the largest below: n weights far below it are off by n 2^-26 of it
+ * together at most.  The sum that divides is of the weights before they are
+ * rounded.  workspace: device memory of sgr_kv_attention_workspace() bytes,
  * 16-byte aligned, without initial contents; calls that may overlap on the
  * GPU need one each.
  */

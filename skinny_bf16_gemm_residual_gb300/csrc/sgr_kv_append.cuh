@@ -15,14 +15,14 @@
 // head needs no atomics for its scale: it holds the page's new tokens in
 // registers, finds their largest magnitude, and then writes codes and scale.
 //
-// Bound: memory (each input read once, each output written once) and the issue
-// of instructions for prompts, the chain of dependent loads for a handful of
-// rows.  Measured: norm + rotation of 12345 rows of 72 heads (458 MB) 88 us,
-// 5.2 TB/s, issue slots 67% taken; of 16 rows of 32 heads 1.4 us.  Append of
-// 6012 prompt rows of 64 + 8 + 8 heads (237 MB) 51 us, 4.6 TB/s, issue
-// slots 73% taken; of one row 2.7 us, of 48 rows 4.9.  More blocks an SM (fewer
-// registers) or packed FP32 arithmetic (more registers) were slower for the
-// append, and within 4% for the norm.
+// Bound: for prompts neither memory (each input read once, each output written
+// once) nor issue slots are full, both are used for most of the time; for a
+// handful of rows the chain of dependent loads.  Measured: norm + rotation of
+// 12345 rows of 72 heads (458 MB) 88-90 us, 5.1 TB/s, issue slots 67% taken; of
+// 16 rows of 32 heads 1.4 us.  Append of 6012 prompt rows of 64 + 8 + 8 heads
+// (237 MB) 51 us, 4.6 TB/s, issue slots 73% taken; of one row 2.7 us, of 48
+// rows 4.9.  More blocks an SM (fewer registers) or packed FP32 arithmetic
+// (more registers) were slower for the append, and within 4% for the norm.
 #pragma once
 
 #include "sgr_kv_common.cuh"

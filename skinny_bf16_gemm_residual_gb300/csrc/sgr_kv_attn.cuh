@@ -8,15 +8,16 @@
 // all sequences and heads, in order, whatever the lengths, and one more unit
 // for each row tile, which is what its beginning and end cost (without it CTAs
 // with many short sequences finish last: 24.2 against 18.7 us for 32 ragged
-// sequences).  A row tile that spans CTAs leaves partial sums (o, R, l) in the
+// sequences, with weights in two parts).  A row tile that spans CTAs leaves partial sums (o, R, l) in the
 // workspace and a second kernel joins them in order (the same bits on every
 // run).  For short caches (`whole`) a row tile is one unit and nothing is
 // joined.
 //
 // Both kernels feed the FP8 tensor core (tcgen05.mma kind::f8f6f4) with the
-// cache's codes straight from TMA.  The queries (and the few-row kernel's
-// weights) are brought into E4M3 as two parts, hi = e4m3(b) and lo = e4m3 of
-// the rest, each row scaled by a power of two, which holds 8 significant bits.
+// cache's codes straight from TMA.  The queries are brought into E4M3 as two
+// parts, hi = e4m3(b) and lo = e4m3 of the rest, each row scaled by a power of
+// two, which holds 8 significant bits; the weights into three (few rows) or
+// into FP16 (many).
 #pragma once
 
 #include <cuda.h>
@@ -464,7 +465,7 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
 //     o = sum_k 2^(R_k - m) o_k / sum_k 2^(R_k - m) l_k,   m = max_k R_k
 //
 // Bound: the latency of its launch and of those two round trips, some 3 us of
-// a call (two chunks of prompts, 33 MB of partial sums: 15 us from a cold L2).
+// a call (two chunks of prompts, 33 MB of partial sums: 12 us from a cold L2).
 constexpr int kJoinThreads = 256;
 
 template <int NT>

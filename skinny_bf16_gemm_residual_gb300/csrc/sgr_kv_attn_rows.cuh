@@ -30,8 +30,8 @@
 // the weights', so these products cannot overlap), with the other half half a
 // turn behind.  Tensor memory is full (two halves of scores and outputs, 128
 // columns each): a third chain would take scores of fewer tokens at a time.  Measured for two chunks of some
-// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 118 us, 627 TFLOP/s,
-// tensor pipe 32% and issue slots 58% of active cycles; with one softmax
+// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 118 us, 625 TFLOP/s,
+// tensor pipe 31% and issue slots 58% of active cycles; with one softmax
 // thread a row instead of two 129 us.
 //
 // Roles (704 threads, one CTA an SM): warps 0-7 and 8-15 softmax of the halves
