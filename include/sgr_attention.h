@@ -13,6 +13,12 @@
  *                     token of the page saturates
  *   attention         o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale q.k_t),
  *                     over the positions t that the query's token may see
+ *                     (sgr_kv_mask: a window, sinks, a tree of drafted tokens)
+ *   mass              mass_t += sum over rows and a group's heads of
+ *                     p_t / sum_t p_t: the attention weight that a cached
+ *                     position has got
+ *   eviction          the positions with the largest mass stay, and move to
+ *                     new pages
  *
  * Sums, norms and softmax statistics are held in 32 bits, and results are
  * rounded once to BF16 or E4M3.  Attention's two products run on the tensor
@@ -133,6 +139,60 @@ typedef struct {
 } sgr_norm_rope;
 
 /*
+ * What a row sees.  Its position is its place in the sequence, p; without a
+ * mask it sees the positions t <= p.
+ *   window  > 0: only t > p - window of them, and
+ *   sinks   the first positions of the sequence, t < sinks, all the same
+ *           (t <= p as ever; without a window they make no difference).
+ *   tree    rows are drafted tokens: of the n new tokens of its sequence a row
+ *           sees those whose bits are set, bit j % 64 of
+ *           tree[row * tree_stride + j / 64] for the j-th (itself among them
+ *           only if set; a window does not count between them), and of the
+ *           positions before the new ones those that a row at position
+ *           seq_len - n + (bits set) - 1 sees.  Bits from n on are not looked
+ *           at.  NULL: not a tree.  tree_words: words of a row, at least
+ *           max_new / 64 rounded up.
+ * A padding row (its place negative) sees nothing, and no row sees one.
+ */
+typedef struct {
+  const uint64_t* tree; /* [tokens, tree_words], 8-byte aligned */
+  int64_t tree_stride;  /* words from row to row */
+  int tree_words;
+  int window;
+  int sinks;
+  int reserved; /* must be zero */
+} sgr_kv_mask;
+
+/*
+ * The attention weight that each position of a cache has got, FP32: position t
+ * of a sequence, head h at data + page * page_stride + h * head_stride +
+ * t % page_size (elements), page as in sgr_kv_cache.
+ */
+typedef struct {
+  float* data;
+  int64_t page_stride;
+  int64_t head_stride;
+} sgr_kv_masses;
+
+/*
+ * What stays of each sequence.  n = min(keep[b], seq_len[b]) positions: the
+ * first min(first, n), the last min(recent, what is left of n), and of those
+ * between the ones with the largest mass (of equal ones the first; a NaN
+ * counts as larger than all).  table: the pages that they move to.
+ */
+typedef struct {
+  const int* keep;  /* [batch], not negative */
+  const int* table; /* [batch, max_pages], row stride table_stride */
+  int* kept;        /* [batch, heads, max_pages * page_size]: the positions that stay, ascending; entries from n on are left */
+  int* new_len;     /* [batch]: n */
+  int64_t table_stride;
+  int max_pages;
+  int first;
+  int recent;
+  int reserved; /* must be zero */
+} sgr_kv_eviction;
+
+/*
  * Queries and keys of `tokens` rows normalised per head and rotated to
  * positions[row], in one pass: q_out = rope(norm(q)), k_out likewise.  In
  * place where out and in are the same (pointer and strides); any other
@@ -160,6 +220,17 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
                   const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, unsigned flags, void* stream);
 
 /*
+ * The same, with row r's query and key rotated to positions[r] instead of its
+ * place in the cache: drafted tokens of a tree stand at their depth, and new
+ * tokens of a sequence that has lost positions (sgr_kv_evict) behind all that
+ * it ever had.  A negative position counts as 0 and records code 7.  positions
+ * NULL: as sgr_kv_append.
+ */
+int sgr_kv_append_at(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* k,
+                     const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, const int* positions,
+                     unsigned flags, void* stream);
+
+/*
  * out[row, head] = attention of the row's query over the cached positions
  * t <= position (and t > position - window where window > 0) of its sequence;
  * query head h reads key/value head h / (q->heads / cache->heads).  A row
@@ -178,6 +249,60 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
 int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* out,
                      float scale, int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream);
 
+/*
+ * The same over the positions that `mask` says (NULL: all up to a row's own),
+ * and, with lse not NULL, lse[row * q->heads + head] = log sum_t p_t, FP32
+ * (-infinity for a row that sees no position; rows of no sequence are left).
+ * Takes sgr_kv_attention's workspace.
+ */
+int sgr_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                            const sgr_heads* out, float* lse, float scale, const sgr_kv_mask* mask, void* workspace,
+                            int64_t workspace_bytes, unsigned flags, void* stream);
+
+/*
+ * Adds to every cached position's mass, for each key/value head, the attention
+ * weight that the batch's rows give it with the heads of its group:
+ *
+ *   mass[t, h] += sum_{rows, heads of h} exp(scale q.k_t - lse[row, head])
+ *
+ * over the rows that see t (mask: as sgr_kv_attention_masked; lse: what that
+ * call wrote for the same q, scale and mask).  The new tokens' own positions
+ * are set, not added to: a page needs no clearing before it is used.  Masked
+ * weights have no part, whatever the position holds; positions that no row sees
+ * keep their mass.  Scores as in sgr_kv_attention for few rows (queries to
+ * 2^-22 of the row's largest), sums in FP32 in a fixed order.  batch->max_new has
+ * to be an upper bound (a sequence with more rows is recorded, code 7, and its
+ * later rows may be missing).  No two sequences of a call may share a page.
+ * workspace: sgr_kv_mass_workspace() bytes, 16-byte aligned, without initial
+ * contents, one for each call that may overlap; NULL where 0 bytes are needed.
+ */
+int sgr_kv_mass(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const float* lse,
+                const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask, void* workspace,
+                int64_t workspace_bytes, unsigned flags, void* stream);
+
+/* Workspace that sgr_kv_mass needs for this batch and `q_heads` query heads, in
+ * bytes: 0 where a key/value head has at most 256 rows of a sequence (max_new
+ * times the group), 4 bytes a position and key/value head for every 256 rows
+ * beyond.  Depends on the sizes in the structures alone. */
+int sgr_kv_mass_workspace(const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads, int64_t* bytes);
+
+/*
+ * Evicts positions by their mass: for each sequence (its block table and
+ * seq_len; q_start and the rows do not matter) and key/value head chooses what
+ * stays and moves it, in order, to the positions 0 .. n - 1 of the pages of
+ * `eviction->table`: codes, rounded to new page scales (as sgr_kv_append
+ * chooses them), and mass.  Heads keep positions of their own, the same number
+ * each.  The old pages are read only; a new page may be none of them, nor
+ * occur twice (undefined contents otherwise).  Entries of the table beyond n
+ * positions are not read; positions of a new page behind them are not written.
+ * Keys stay rotated to the positions that they had: go on with
+ * sgr_kv_append_at.  A bad old page's positions count as the smallest mass and
+ * move as zeros; n beyond the new table's room is cut to it; both are recorded
+ * (code 7).  Cached values that are NaN do not count for the scale and stay NaN.
+ */
+int sgr_kv_evict(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_kv_masses* mass,
+                 const sgr_kv_eviction* eviction, unsigned flags, void* stream);
+
 /* Workspace that sgr_kv_attention needs for this batch, `q_heads` query heads
  * and these flags on `device`, in bytes (a smaller one is
  * SGR_ERR_UNSUPPORTED there).  Depends on the sizes in the structures, not on
@@ -185,14 +310,23 @@ int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const
 int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
                                unsigned flags, int64_t* bytes);
 
-/* Host-only argument checks of the three operators (their exact rules, but
- * for the size of the workspace). */
+/* Host-only argument checks of the operators (their exact rules, but for the
+ * size of the workspace). */
 int sgr_validate_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* q_out, const sgr_heads* k_out,
                               const int* positions, int tokens, int head_dim, const sgr_norm_rope* nr);
 int sgr_validate_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
                            const sgr_heads* k, const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr);
 int sgr_validate_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
                               const sgr_heads* out, float scale, int window);
+int sgr_validate_kv_append_at(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                              const sgr_heads* k, const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr,
+                              const int* positions);
+int sgr_validate_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                                     const sgr_heads* out, const float* lse, float scale, const sgr_kv_mask* mask);
+int sgr_validate_kv_mass(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const float* lse,
+                         const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask);
+int sgr_validate_kv_evict(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_kv_masses* mass,
+                          const sgr_kv_eviction* eviction);
 
 #ifdef __cplusplus
 }

@@ -80,7 +80,7 @@
 extern "C" {
 #endif
 
-#define SGR_ABI_VERSION 10
+#define SGR_ABI_VERSION 11
 
 typedef enum {
   SGR_OK = 0,

@@ -75,7 +75,10 @@ from .attention import (  # noqa: F401
     KvCache,
     RopeNorm,
     kv_attention_workspace,
+    kv_mass_workspace,
     sgr_kv_append,
     sgr_kv_attention,
+    sgr_kv_evict,
+    sgr_kv_mass,
     sgr_qk_norm_rope,
 )

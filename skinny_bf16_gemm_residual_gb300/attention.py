@@ -8,6 +8,13 @@ step; its tensors are updated in place from step to step) and a ``RopeNorm``
     o = sgr_kv_attention(cache, batch, q)                # attention over the cache
     y = skinny_gemm_residual(o.flatten(1), w_out, residual)
 
+Drafted tokens that form trees pass ``tree=`` to the attention and their depths
+as ``positions=`` to the append; ``window=`` and ``sinks=`` limit what a token
+sees.  A program that bounds its caches by attention weight keeps a mass for
+each (``KvCache.zero_mass``), adds to it after the attention (``sgr_kv_mass``)
+and evicts what has the least of it when a sequence has outgrown its pages
+(``sgr_kv_evict``).
+
 Rows of heads (q, k, v and outputs) are CUDA bfloat16 tensors
 [tokens, heads, head_dim] with unit inner stride and token and head strides
 that are multiples of 8 elements: slices of a packed projection output fit as
@@ -19,7 +26,8 @@ from __future__ import annotations
 import ctypes
 import struct
 
-from .binding import (SGR_OK, SgrError, _common_device, load, sgr_heads, sgr_kv_batch, sgr_kv_cache, sgr_norm_rope)
+from .binding import (SGR_OK, SgrError, _common_device, load, sgr_heads, sgr_kv_batch, sgr_kv_cache, sgr_kv_eviction,
+                      sgr_kv_mask, sgr_kv_masses, sgr_norm_rope)
 
 
 class _Torch:
@@ -40,6 +48,12 @@ torch = _Torch()
 # module.
 _pack_heads = struct.Struct("@Pqqii").pack
 assert struct.calcsize("@Pqqii") == ctypes.sizeof(sgr_heads)
+_pack_mask = struct.Struct("@Pqiiii").pack
+assert struct.calcsize("@Pqiiii") == ctypes.sizeof(sgr_kv_mask)
+_pack_masses = struct.Struct("@Pqq").pack
+assert struct.calcsize("@Pqq") == ctypes.sizeof(sgr_kv_masses)
+_pack_eviction = struct.Struct("@PPPPqiiii").pack
+assert struct.calcsize("@PPPPqiiii") == ctypes.sizeof(sgr_kv_eviction)
 
 
 def _check(rc: int, what: str) -> None:
@@ -122,6 +136,11 @@ class KvCache:
         scale = torch.ones(2, pages, heads, dtype=torch.float32, device=device)
         kv = kv.view(torch.float8_e4m3fn)
         return cls(kv[0], kv[1], scale[0], scale[1])
+
+
+    def zero_mass(self):
+        """Accumulated attention weights for this cache: float32 [pages, heads, page_size], zeros."""
+        return torch.zeros(self.k.shape[:3], dtype=torch.float32, device=self.device)
 
 
 class KvBatch:
@@ -252,11 +271,28 @@ def sgr_qk_norm_rope(q, k, positions, rope: RopeNorm, q_out=None, k_out=None, fl
     return q_out, k_out
 
 
+def _mask(batch, window: int, sinks: int, tree, index: int) -> bytes:
+    """The sgr_kv_mask of these arguments."""
+    if tree is None:
+        return _pack_mask(0, 0, 0, window, sinks, 0)
+    if tree.dtype is not torch.int64 or tree.dim() != 2 or (tree.shape[1] > 1 and tree.stride(1) != 1):
+        raise ValueError("tree must be a 2-D int64 tensor [tokens, words] with unit inner stride")
+    if tree.get_device() != index:
+        raise ValueError(f"tree: all tensors must be on one CUDA device, got {tree.device} and cuda:{index}")
+    tokens, words = tree.shape
+    if tokens != batch.tokens or 64 * words < batch.max_new:
+        raise ValueError(f"tree must be [{batch.tokens}, at least {-(-batch.max_new // 64)}], got {list(tree.shape)}")
+    return _pack_mask(tree.data_ptr(), tree.stride(0) if tokens > 1 else words, words, window, sinks, 0)
+
+
 def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, q_out=None, flags: int = 0,
-                  stream=None):
+                  stream=None, positions=None):
     """Append the new tokens' keys (normalised, rotated to their positions)
     and values [tokens, heads, head_dim] to the cache; with q, also normalise
-    and rotate their queries into q_out (which may be q).  Returns q_out."""
+    and rotate their queries into q_out (which may be q).  positions [tokens]
+    (int32) are what they are rotated to where that is not their place in the
+    cache: drafted tokens of a tree (the positions of their depths), tokens of
+    a sequence of which positions were evicted.  Returns q_out."""
     index = cache.index
     shape = (batch.tokens, cache.heads, cache.head_dim)
     hk, hv = _heads(k, "k", shape, index), _heads(v, "v", shape, index)
@@ -274,7 +310,16 @@ def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, 
     if batch.index != index or rope.index != index:
         _on(index, batch.index, "sgr_kv_append")
         _on(index, rope.index, "sgr_kv_append")
-    _launch(index, stream, "sgr_kv_append", load().sgr_kv_append, cache.ref, batch.ref, hq, hk, hv, hqo, rope.ref, flags)
+    if positions is None:
+        _launch(index, stream, "sgr_kv_append", load().sgr_kv_append, cache.ref, batch.ref, hq, hk, hv, hqo, rope.ref, flags)
+        return q_out
+    _int32(positions, "positions", 1)
+    if positions.shape[0] != batch.tokens:
+        raise ValueError(f"positions must have {batch.tokens} elements, got {positions.shape[0]}")
+    if positions.get_device() != index:
+        _on(index, positions.get_device(), "sgr_kv_append")
+    _launch(index, stream, "sgr_kv_append", load().sgr_kv_append_at, cache.ref, batch.ref, hq, hk, hv, hqo, rope.ref,
+            positions.data_ptr(), flags)
     return q_out
 
 
@@ -287,11 +332,14 @@ def kv_attention_workspace(cache: KvCache, batch: KvBatch, q_heads: int, flags: 
 
 
 def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float | None = None, window: int = 0,
-                     workspace=None, flags: int = 0, stream=None):
+                     workspace=None, flags: int = 0, stream=None, sinks: int = 0, tree=None, lse=None):
     """Attention of the new tokens' queries [tokens, q_heads, head_dim] over
-    the cached positions up to their own (the last `window` of them where
-    window > 0), scores times `scale` (1/sqrt(head_dim) by default).
-    Returns out."""
+    the cached positions up to their own (where window > 0 the last `window` of
+    them, and the sequence's first `sinks`), scores times `scale`
+    (1/sqrt(head_dim) by default).  tree [tokens, words] (int64): bit j % 64 of
+    word j / 64 says whether a row sees the j-th new token of its sequence,
+    itself among them.  lse [tokens, q_heads] (contiguous float32) gets the
+    logarithm of each row's sum of exponentials.  Returns out."""
     index = cache.index
     shape = (batch.tokens, _shape3(q, "q")[1], cache.head_dim)
     hq = _heads(q, "q", shape, index)
@@ -305,6 +353,94 @@ def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float |
     if batch.index != index or workspace.get_device() != index:
         _on(index, batch.index, "sgr_kv_attention")
         _on(index, workspace.get_device(), "sgr_kv_attention")
-    _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention, cache.ref, batch.ref, hq, ho,
-            shape[2] ** -0.5 if scale is None else scale, window, workspace.data_ptr(), workspace.nbytes, flags)
+    if scale is None:
+        scale = shape[2] ** -0.5
+    if sinks == 0 and tree is None and lse is None:
+        _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention, cache.ref, batch.ref, hq, ho, scale, window,
+                workspace.data_ptr(), workspace.nbytes, flags)
+        return out
+    _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention_masked, cache.ref, batch.ref, hq, ho,
+            None if lse is None else _row_stats(lse, "lse", shape[:2], index), scale,
+            _mask(batch, window, sinks, tree, index), workspace.data_ptr(), workspace.nbytes, flags)
     return out
+
+
+def _masses(mass, cache: KvCache) -> bytes:
+    """The sgr_kv_masses of a tensor."""
+    shape = cache.k.shape[:3]
+    if mass.dtype is not torch.float32 or mass.shape != shape or mass.get_device() != cache.index or mass.stride(2) != 1:
+        raise ValueError(f"mass must be a float32 tensor {list(shape)} with unit inner stride on cuda:{cache.index}")
+    pages, heads, size = shape
+    hs = mass.stride(1) if heads > 1 else size
+    return _pack_masses(mass.data_ptr(), mass.stride(0) if pages > 1 else heads * hs, hs)
+
+
+def kv_mass_workspace(cache: KvCache, batch: KvBatch, q_heads: int):
+    """A workspace for sgr_kv_mass calls of these sizes (one for each call that may overlap with others on the GPU)."""
+    n = ctypes.c_int64(0)
+    _check(load().sgr_kv_mass_workspace(cache.ref, batch.ref, q_heads, ctypes.byref(n)), "sgr_kv_mass_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=cache.device)
+
+
+def sgr_kv_mass(cache: KvCache, batch: KvBatch, q, lse, mass, scale: float | None = None, window: int = 0,
+                sinks: int = 0, tree=None, workspace=None, flags: int = 0, stream=None):
+    """Add to mass [pages, heads, page_size] (float32) the attention weight that
+    the new tokens' queries [tokens, q_heads, head_dim] give each cached
+    position, summed over the heads of its key/value head; the new tokens' own
+    positions are set.  lse: what sgr_kv_attention wrote for the same queries,
+    scale and masks.  Returns mass."""
+    index = cache.index
+    shape = (batch.tokens, _shape3(q, "q")[1], cache.head_dim)
+    hq = _heads(q, "q", shape, index)
+    lse_at = _row_stats(lse, "lse", shape[:2], index)
+    if workspace is None:
+        workspace = _new(index, stream, lambda: kv_mass_workspace(cache, batch, shape[1]))
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if batch.index != index or workspace.get_device() != index:
+        _on(index, batch.index, "sgr_kv_mass")
+        _on(index, workspace.get_device(), "sgr_kv_mass")
+    _launch(index, stream, "sgr_kv_mass", load().sgr_kv_mass, cache.ref, batch.ref, hq, lse_at, _masses(mass, cache),
+            shape[2] ** -0.5 if scale is None else scale, _mask(batch, window, sinks, tree, index),
+            workspace.data_ptr(), workspace.nbytes, flags)
+    return mass
+
+
+def sgr_kv_evict(cache: KvCache, batch: KvBatch, mass, keep, new_table, first: int = 0, recent: int = 0, new_len=None,
+                 kept=None, flags: int = 0, stream=None):
+    """Of each sequence keep the first `first` and the last `recent` positions
+    and, head by head, the others with the largest mass, `keep` [batch] (int32)
+    in all, and move them in order, with their mass, to the pages of new_table
+    [batch, pages] (int32; none of them in use).  Returns (new_len, kept): the
+    new lengths [batch], and the positions that stayed [batch, heads, room]
+    (room: what the new pages hold; entries beyond a length are not written).
+
+    Go on with the new table and lengths, and with sgr_kv_append(positions=):
+    the keys keep the rotation of the positions that they had."""
+    index = cache.index
+    for t, name, dim in ((keep, "keep", 1), (new_table, "new_table", 2)):
+        _int32(t, name, dim)
+        if t.shape[0] != batch.batch:
+            raise ValueError(f"{name} must have {batch.batch} rows, got {t.shape[0]}")
+        _on(index, t.get_device(), "sgr_kv_evict")
+    pages = new_table.shape[1]
+    shapes = {"new_len": (batch.batch,), "kept": (batch.batch, cache.heads, pages * cache.page_size)}
+    given = {"new_len": new_len, "kept": kept}
+    for name, t in given.items():
+        if t is None:
+            given[name] = _new(index, stream, lambda: torch.empty(shapes[name], dtype=torch.int32, device=cache.device))
+        elif t.dtype is not torch.int32 or t.shape != shapes[name] or t.get_device() != index or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor {list(shapes[name])} on cuda:{index}")
+    new_len, kept = given["new_len"], given["kept"]
+    _on(index, batch.index, "sgr_kv_evict")
+    ev = _pack_eviction(keep.data_ptr(), new_table.data_ptr(), kept.data_ptr(), new_len.data_ptr(),
+                        new_table.stride(0) if batch.batch > 1 else pages, pages, first, recent, 0)
+    _launch(index, stream, "sgr_kv_evict", load().sgr_kv_evict, cache.ref, batch.ref, _masses(mass, cache), ev, flags)
+    return new_len, kept
+
+
+def _row_stats(t, name: str, shape, index: int) -> int:
+    """The address of one float32 a row and query head."""
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)} on cuda:{index}")
+    return t.data_ptr()

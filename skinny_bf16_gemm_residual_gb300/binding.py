@@ -15,7 +15,7 @@ import threading
 
 from . import build as _build
 
-ABI_VERSION = 10  # must equal SGR_ABI_VERSION of the loaded library
+ABI_VERSION = 11  # must equal SGR_ABI_VERSION of the loaded library
 
 SGR_OK = 0
 SGR_ERR_NULL = 1
@@ -70,6 +70,21 @@ class sgr_norm_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int)]
 
 
+class sgr_kv_mask(ctypes.Structure):
+    _fields_ = [("tree", ctypes.c_void_p), ("tree_stride", ctypes.c_int64), ("tree_words", ctypes.c_int),
+                ("window", ctypes.c_int), ("sinks", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
+class sgr_kv_masses(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class sgr_kv_eviction(ctypes.Structure):
+    _fields_ = [("keep", ctypes.c_void_p), ("table", ctypes.c_void_p), ("kept", ctypes.c_void_p),
+                ("new_len", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int),
+                ("first", ctypes.c_int), ("recent", ctypes.c_int), ("reserved", ctypes.c_int)]
+
+
 class SgrError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -117,11 +132,20 @@ EXPORTS = (
     "sgr_selftest_streamk_abort",
     "sgr_qk_norm_rope",
     "sgr_kv_append",
+    "sgr_kv_append_at",
     "sgr_kv_attention",
+    "sgr_kv_attention_masked",
     "sgr_kv_attention_workspace",
+    "sgr_kv_mass",
+    "sgr_kv_mass_workspace",
+    "sgr_kv_evict",
     "sgr_validate_qk_norm_rope",
     "sgr_validate_kv_append",
+    "sgr_validate_kv_append_at",
     "sgr_validate_kv_attention",
+    "sgr_validate_kv_attention_masked",
+    "sgr_validate_kv_mass",
+    "sgr_validate_kv_evict",
 )
 
 
@@ -173,10 +197,19 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         # Structures go as addresses (byref() or a structure's own address).
         lib.sgr_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp, U, vp]
         lib.sgr_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, U, vp]
+        lib.sgr_kv_append_at.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, U, vp]
+        lib.sgr_kv_attention_masked.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, i64, U, vp]
+        lib.sgr_kv_mass.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, i64, U, vp]
+        lib.sgr_kv_mass_workspace.argtypes = [vp, vp, I, ctypes.POINTER(i64)]
+        lib.sgr_kv_evict.argtypes = [vp, vp, vp, vp, U, vp]
+        lib.sgr_validate_kv_mass.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, vp]
+        lib.sgr_validate_kv_evict.argtypes = [vp, vp, vp, vp]
         lib.sgr_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I, vp, i64, U, vp]
         lib.sgr_kv_attention_workspace.argtypes = [I, vp, vp, I, U, ctypes.POINTER(i64)]
         lib.sgr_validate_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, I, I, vp]
         lib.sgr_validate_kv_append.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+        lib.sgr_validate_kv_append_at.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
+        lib.sgr_validate_kv_attention_masked.argtypes = [vp, vp, vp, vp, vp, ctypes.c_float, vp]
         lib.sgr_validate_kv_attention.argtypes = [vp, vp, vp, vp, ctypes.c_float, I]
         for name in EXPORTS:
             if name != "sgr_status_string":

@@ -1,7 +1,7 @@
 """Build step for the CUDA library (in-tree, sm_103a only).
 
 ``build_library()`` compiles ``csrc/sgr_api.cu`` (the projections) and
-``csrc/sgr_kv.cu`` (the attention operators), each with the kernels that it
+``csrc/sgr_kv*.cu`` (the attention operators), each with the kernels that it
 includes, with nvcc side by side, links them into
 ``_build/libskinny_gemm_residual.so`` next to this file and returns its path.
 Rebuilds when any source or public header is newer than the library.
@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
-UNITS = ("sgr_api.cu", "sgr_kv.cu")
+UNITS = ("sgr_api.cu", "sgr_kv.cu", "sgr_kv_masked.cu", "sgr_kv_mass.cu")
 
 
 def _nvcc() -> str:

@@ -13,8 +13,8 @@
 #include "sgr_attention.h"
 #include "sgr_internal.h"
 #include "sgr_kv_append.cuh"
-#include "sgr_kv_attn_few.cuh"
-#include "sgr_kv_attn_rows.cuh"
+#include "sgr_kv_evict.cuh"
+#include "sgr_kv_kernels.h"
 
 namespace {
 
@@ -182,10 +182,9 @@ int check_batch(const sgr_kv_batch* b) {
 
 bool empty(const sgr_kv_batch& b) { return b.batch == 0 || b.tokens == 0; }
 
-// Whether rows of heads and the cache (codes or scales) share memory.
-bool touches_cache(const sgr_heads& x, const sgr_kv_cache& c, long long tokens) {
+// Whether memory and the cache (codes or scales) share bytes.
+bool touches_cache(Extent e, const sgr_kv_cache& c) {
   if (c.num_pages == 0) return false;
-  const Extent e = heads_extent(x, tokens, c.head_dim);
   for (const void* p : {(const void*)c.k, (const void*)c.v}) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
     if (overlap(e, {lo, lo + (uintptr_t)cache_bytes(c)})) return true;
@@ -197,13 +196,19 @@ bool touches_cache(const sgr_heads& x, const sgr_kv_cache& c, long long tokens) 
   return false;
 }
 
+// Whether rows of heads and the cache (codes or scales) share memory.
+bool touches_cache(const sgr_heads& x, const sgr_kv_cache& c, long long tokens) {
+  return touches_cache(heads_extent(x, tokens, c.head_dim), c);
+}
+
 int validate_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* k,
-                    const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr) {
+                    const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr, const int* positions) {
   int rc;
   if ((rc = check_cache(c)) != SGR_OK || (rc = check_batch(b)) != SGR_OK) return rc;
   if ((q == nullptr) != (qo == nullptr)) return SGR_ERR_NULL;
   if (empty(*b)) return SGR_OK;
   const int dim = c->head_dim;
+  if (!aligned(positions, 4)) return SGR_ERR_ALIGN;
   if ((rc = check_norm_rope(nr, dim)) != SGR_OK) return rc;
   if ((rc = check_heads(k, c->heads, dim, false)) != SGR_OK) return rc;
   if ((rc = check_heads(v, c->heads, dim, false)) != SGR_OK) return rc;
@@ -219,11 +224,24 @@ int validate_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_head
   return SGR_OK;
 }
 
+// (NULL: no mask)
+int check_mask(const sgr_kv_mask* m, const sgr_kv_batch& b) {
+  if (!m) return SGR_OK;
+  if (m->reserved != 0) return SGR_ERR_UNSUPPORTED;
+  if (m->window < 0 || m->sinks < 0) return SGR_ERR_SHAPE;
+  if (!m->tree || empty(b)) return SGR_OK;
+  if (!aligned(m->tree, 8)) return SGR_ERR_ALIGN;
+  if (m->tree_words < 1 || 64LL * m->tree_words < b.max_new || m->tree_stride < m->tree_words) return SGR_ERR_SHAPE;
+  if (m->tree_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  return SGR_OK;
+}
+
 int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out,
-                       float scale, int window) {
+                       const float* lse, float scale, const sgr_kv_mask* mask) {
   int rc;
   if ((rc = check_cache(c)) != SGR_OK || (rc = check_batch(b)) != SGR_OK) return rc;
-  if (!std::isfinite(scale) || window < 0) return SGR_ERR_SHAPE;
+  if (!std::isfinite(scale)) return SGR_ERR_SHAPE;
+  if ((rc = check_mask(mask, *b)) != SGR_OK) return rc;
   if (empty(*b)) return SGR_OK;
   if (!q || !out) return SGR_ERR_NULL;
   if ((rc = check_heads(q, q->heads, c->head_dim, false)) != SGR_OK) return rc;
@@ -233,6 +251,103 @@ int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_h
   if ((rc = check_rows(*out, b->tokens, c->head_dim)) != SGR_OK) return rc;
   if (heads_overlap(*q, *out, b->tokens, c->head_dim)) return SGR_ERR_ALIAS;
   if (touches_cache(*out, *c, b->tokens)) return SGR_ERR_ALIAS;
+  if (lse) {
+    if (!aligned(lse, 4)) return SGR_ERR_ALIGN;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
+    const Extent e{lo, lo + 4 * (uintptr_t)b->tokens * q->heads};
+    if (overlap(e, heads_extent(*q, b->tokens, c->head_dim)) || overlap(e, heads_extent(*out, b->tokens, c->head_dim)) ||
+        touches_cache(e, *c))
+      return SGR_ERR_ALIAS;
+  }
+  return SGR_OK;
+}
+
+// A mass for each position of a cache: positions must not overlap, nor share
+// memory with the cache.
+int check_masses(const sgr_kv_masses* m, const sgr_kv_cache& c, Extent* extent) {
+  if (!m) return SGR_ERR_NULL;
+  *extent = {0, 0};
+  if (c.num_pages == 0) return SGR_OK;
+  if (!m->data) return SGR_ERR_NULL;
+  if (!aligned(m->data, 4)) return SGR_ERR_ALIGN;
+  struct Dim {
+    long long stride, count;
+  } d[2] = {{m->head_stride, c.heads}, {m->page_stride, c.num_pages}};
+  for (const Dim& x : d) {
+    if (x.count > 1 && x.stride < 0) return SGR_ERR_SHAPE;
+    if (x.stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  }
+  if (d[0].stride > d[1].stride) std::swap(d[0], d[1]);
+  long long span = c.page_size;
+  for (const Dim& x : d)
+    if (x.count > 1) {
+      if (x.stride < span) return SGR_ERR_SHAPE;
+      span += (x.count - 1) * x.stride;
+    }
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(m->data);
+  *extent = {lo, lo + 4 * (uintptr_t)span};
+  return touches_cache(*extent, c) ? SGR_ERR_ALIAS : SGR_OK;
+}
+
+int validate_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const float* lse,
+                  const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask) {
+  int rc;
+  if ((rc = check_cache(c)) != SGR_OK || (rc = check_batch(b)) != SGR_OK) return rc;
+  if (!std::isfinite(scale)) return SGR_ERR_SHAPE;
+  if ((rc = check_mask(mask, *b)) != SGR_OK) return rc;
+  if (empty(*b)) return SGR_OK;
+  if (!q || !lse) return SGR_ERR_NULL;
+  if ((rc = check_heads(q, q->heads, c->head_dim, false)) != SGR_OK) return rc;
+  if (q->heads % c->heads) return SGR_ERR_SHAPE;
+  if (q->heads / c->heads > kMaxGroup) return SGR_ERR_UNSUPPORTED;
+  if (!aligned(lse, 4)) return SGR_ERR_ALIGN;
+  Extent e;
+  if ((rc = check_masses(mass, *c, &e)) != SGR_OK) return rc;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
+  if (overlap(e, heads_extent(*q, b->tokens, c->head_dim)) || overlap(e, {lo, lo + 4 * (uintptr_t)b->tokens * q->heads}))
+    return SGR_ERR_ALIAS;
+  return SGR_OK;
+}
+
+int validate_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses* mass, const sgr_kv_eviction* ev) {
+  int rc;
+  if ((rc = check_cache(c)) != SGR_OK) return rc;
+  if (!b || !ev) return SGR_ERR_NULL;
+  sgr_kv_batch only = *b;  // (its rows do not matter)
+  only.q_start = nullptr;
+  only.tokens = only.batch;
+  only.max_new = 1;
+  if ((rc = check_batch(&only)) != SGR_OK) return rc;
+  if (ev->reserved != 0) return SGR_ERR_UNSUPPORTED;
+  if (ev->first < 0 || ev->recent < 0 || ev->max_pages < 0) return SGR_ERR_SHAPE;
+  if (ev->max_pages > (1 << 24)) return SGR_ERR_UNSUPPORTED;
+  if (b->batch == 0) return SGR_OK;
+  if (!ev->keep || !ev->new_len || (ev->max_pages > 0 && (!ev->table || !ev->kept))) return SGR_ERR_NULL;
+  if (!aligned(ev->keep, 4) || !aligned(ev->new_len, 4) || !aligned(ev->table, 4) || !aligned(ev->kept, 4))
+    return SGR_ERR_ALIGN;
+  if (ev->table_stride < ev->max_pages) return SGR_ERR_SHAPE;
+  if (ev->table_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
+  Extent e[3];  // what is written: masses, positions, lengths
+  if ((rc = check_masses(mass, *c, &e[0])) != SGR_OK) return rc;
+  auto of = [](const void* p, long long n) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Extent{lo, lo + 4 * (uintptr_t)(n > 0 ? n : 0)};
+  };
+  const long long rows = b->batch - 1;
+  e[1] = of(ev->kept, (long long)b->batch * c->heads * ev->max_pages * c->page_size);
+  e[2] = of(ev->new_len, b->batch);
+  const Extent in[4] = {of(b->seq_len, b->batch), of(ev->keep, b->batch),
+                        of(b->block_table, b->max_pages > 0 ? rows * b->table_stride + b->max_pages : 0),
+                        of(ev->table, ev->max_pages > 0 ? rows * ev->table_stride + ev->max_pages : 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Extent& x : in)
+      if (overlap(e[i], x)) return SGR_ERR_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (overlap(e[i], e[j])) return SGR_ERR_ALIAS;
+    if (touches_cache(e[i], *c)) return SGR_ERR_ALIAS;
+  }
+  for (const Extent& x : in)
+    if (touches_cache(x, *c)) return SGR_ERR_ALIAS;
   return SGR_OK;
 }
 
@@ -349,8 +464,9 @@ AppendFn append_fn(int dim, int page_size, int most, int q_passes) {
 }
 
 int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* k,
-               const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr, unsigned flags, void* stream) {
-  int rc = validate_append(c, b, q, k, v, qo, nr);
+               const sgr_heads* v, const sgr_heads* qo, const sgr_norm_rope* nr, const int* positions, unsigned flags,
+               void* stream) {
+  int rc = validate_append(c, b, q, k, v, qo, nr, positions);
   if (rc != SGR_OK || empty(*b)) return rc;
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
@@ -362,6 +478,7 @@ int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q,
   p.cache = cache_of(*c);
   p.batch = batch_of(*b);
   p.nr = norm_rope_of(*nr);
+  p.positions = nr->table ? positions : nullptr;
   p.err = dev->err;
   // Pages written to: at most one per row; a sequence of n rows reaches at
   // most (n - 1) / page_size + 2 of them.
@@ -379,35 +496,25 @@ int run_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q,
 }
 
 // ------------------------------------------------------------ attention
-using AttnFn = void (*)(const CUtensorMap, const CUtensorMap, const sgr::AttnParams);
-using JoinFn = void (*)(const sgr::AttnParams);
+sgr::AttnKernel attn_kernel(int dim, int nt, bool masked) {
+  if (masked) return sgr::attn_kernel_masked(dim, nt);
+  return dim == 64 ? sgr::attn_kernel_of<64, false>(nt) : sgr::attn_kernel_of<128, false>(nt);
+}
 
-struct AttnKernel {
-  AttnFn fn;
-  JoinFn join;
-  int smem, threads, join_rows;
+struct Join {
+  sgr::JoinFn fn;
+  int rows;  // of a block
 };
 
-template <int D, int NT>
-AttnKernel attn_kernel_of() {
-  return {sgr::kv_attn_kernel<D, NT>, sgr::kv_attn_join_kernel<D, NT>, sgr::attn_smem_bytes<D, NT>(),
-          sgr::AttnShape<D, NT>::kThreads, sgr::JoinShape<NT>::kRows};
-}
-
 template <int D>
-AttnKernel attn_rows_kernel_of() {
-  return {sgr::kv_attn_rows_kernel<D>, sgr::kv_attn_join_kernel<D, sgr::kRowsNT>, sgr::rows_attn_smem_bytes<D>(),
-          sgr::kRowsThreads, sgr::JoinShape<sgr::kRowsNT>::kRows};
-}
-
-template <int D>
-AttnKernel attn_few_kernel(int nt) {
-  return nt == 8 ? attn_kernel_of<D, 8>() : nt == 16 ? attn_kernel_of<D, 16>() : nt == 24 ? attn_kernel_of<D, 24>() : attn_kernel_of<D, 32>();
-}
-
-AttnKernel attn_kernel(int dim, int nt) {
-  if (nt == sgr::kRowsNT) return dim == 64 ? attn_rows_kernel_of<64>() : attn_rows_kernel_of<128>();
-  return dim == 64 ? attn_few_kernel<64>(nt) : attn_few_kernel<128>(nt);
+Join join_kernel(int nt) {
+  switch (nt) {
+    case 8: return {sgr::kv_attn_join_kernel<D, 8>, sgr::JoinShape<8>::kRows};
+    case 16: return {sgr::kv_attn_join_kernel<D, 16>, sgr::JoinShape<16>::kRows};
+    case 24: return {sgr::kv_attn_join_kernel<D, 24>, sgr::JoinShape<24>::kRows};
+    case 32: return {sgr::kv_attn_join_kernel<D, 32>, sgr::JoinShape<32>::kRows};
+    default: return {sgr::kv_attn_join_kernel<D, sgr::kRowsNT>, sgr::JoinShape<sgr::kRowsNT>::kRows};
+  }
 }
 
 struct AttnPlan {
@@ -476,9 +583,34 @@ bool make_cache_tmap(CUtensorMap* m, const void* codes, const sgr_kv_cache& c) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out, float scale,
-                  int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
-  int rc = validate_attention(c, b, q, out, scale, window);
+// What the walk of the work and the masks need, of any operator over the cache.
+void attn_params(sgr::AttnParams* p, const sgr_kv_cache& c, const sgr_kv_batch& b, const sgr_heads& q, float scale,
+                 const sgr_kv_mask* mask, unsigned* err) {
+  p->q = heads_of(&q);
+  p->cache = cache_of(c);
+  p->batch = batch_of(b);
+  p->scale_log2 = scale * 1.4426950408889634f;
+  const sgr_kv_mask m = mask ? *mask : sgr_kv_mask{};
+  p->window = m.window > 0 ? m.window : INT_MAX;
+  p->sinks = m.window > 0 ? m.sinks : 0;
+  p->tree = reinterpret_cast<const unsigned long long*>(m.tree);
+  p->tree_stride = m.tree_stride;
+  p->tree_words = m.tree_words;
+  p->group = q.heads / c.heads;
+  p->group_inv = p->group > 1 ? (unsigned)((1ULL << 32) / p->group) : 0xffffffffu;
+  p->err = err;
+}
+
+sgr_kv_mask windowed(int window) {
+  sgr_kv_mask m = {};
+  m.window = window;
+  return m;
+}
+
+int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out, float* lse,
+                  float scale, const sgr_kv_mask* mask, void* workspace, int64_t workspace_bytes, unsigned flags,
+                  void* stream) {
+  int rc = validate_attention(c, b, q, out, lse, scale, mask);
   if (rc != SGR_OK || empty(*b)) return rc;
   if ((flags & SGR_FLAG_KV_FEW_ROWS) && (flags & SGR_FLAG_KV_MANY_ROWS)) return SGR_ERR_UNSUPPORTED;
   if (!workspace) return SGR_ERR_NULL;
@@ -492,24 +624,137 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   if (!make_cache_tmap(&tk, c->num_pages ? c->k : workspace, *c) || !make_cache_tmap(&tv, c->num_pages ? c->v : workspace, *c))
     return SGR_ERR_LAUNCH;
   sgr::AttnParams p;
-  p.q = heads_of(q);
+  attn_params(&p, *c, *b, *q, scale, mask, dev->err);
   p.out = heads_of(out);
-  p.cache = cache_of(*c);
-  p.batch = batch_of(*b);
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.window = window > 0 ? window : INT_MAX;
-  p.group = q->heads / c->heads;
-  p.group_inv = p.group > 1 ? (unsigned)((1ULL << 32) / p.group) : 0xffffffffu;
+  p.lse = lse;
   p.reuse = a.reuse ? 1 : 0;
   p.whole = a.split ? 0 : 1;
-  p.err = dev->err;
   p.part_o = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2LL * a.grid * a.nt * c->head_dim);
   p.pieces = reinterpret_cast<sgr::AttnPiece*>(p.part_ml + 2LL * a.grid * a.nt);
-  const AttnKernel k = attn_kernel(c->head_dim, a.nt);
+  const sgr::AttnKernel k = attn_kernel(c->head_dim, a.nt, p.sinks > 0 || p.tree || p.lse);
   rc = launch(k.fn, dim3(a.grid), k.threads, k.smem, flags, stream, tk, tv, p);
   if (rc != SGR_OK || !a.split) return rc;
-  return launch(k.join, dim3(a.grid, a.nt / k.join_rows), sgr::kJoinThreads, 0, flags, stream, p);
+  const Join join = c->head_dim == 64 ? join_kernel<64>(a.nt) : join_kernel<128>(a.nt);
+  return launch(join.fn, dim3(a.grid, a.nt / join.rows), sgr::kJoinThreads, 0, flags, stream, p);
+}
+
+// ------------------------------------------------------------ mass
+struct MassPlan {
+  int nt;         // rows of a row tile
+  int grid;
+  int tiles;      // of keys, of a sequence
+  bool part;      // whether a sequence may have several row tiles
+  bool fits;
+  int64_t bytes;  // workspace
+};
+
+MassPlan mass_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads) {
+  MassPlan m;
+  const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
+  m.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : sgr::kMassRows;
+  m.part = rows > m.nt;
+  const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  const long long row_tiles = m.part ? (long long)b.tokens * group / m.nt + b.batch : b.batch;  // at most
+  const long long units = c.heads * row_tiles * (tiles + 1);
+  m.fits = units < (1LL << 31) && tiles < (1 << 24) && c.heads * row_tiles * tiles < (1LL << 31);
+  m.tiles = (int)tiles;
+  m.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
+  m.bytes = m.part ? row_tiles * c.heads * tiles * sgr::kAttnTile * 4LL : 0;
+  return m;
+}
+
+int run_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const float* lse,
+             const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask, void* workspace, int64_t workspace_bytes,
+             unsigned flags, void* stream) {
+  int rc = validate_mass(c, b, q, lse, mass, scale, mask);
+  if (rc != SGR_OK || empty(*b)) return rc;
+  KvDevice* dev;
+  if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  const MassPlan m = mass_plan(dev->sms, *c, *b, q->heads);
+  if (!m.fits || (m.part && b->batch > 65535)) return SGR_ERR_UNSUPPORTED;
+  if (m.part) {
+    if (!workspace) return SGR_ERR_NULL;
+    if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
+    if (workspace_bytes < m.bytes) return SGR_ERR_UNSUPPORTED;
+  }
+  if (c->num_pages == 0 || m.tiles == 0) return SGR_OK;  // (no position has a place)
+  CUtensorMap tk;
+  if (!make_cache_tmap(&tk, c->k, *c)) return SGR_ERR_LAUNCH;
+  sgr::MassParams p = {};
+  attn_params(&p.a, *c, *b, *q, scale, mask, dev->err);
+  p.a.lse = const_cast<float*>(lse);
+  p.a.reuse = m.part ? 1 : 0;
+  p.mass = mass->data;
+  p.page_stride = mass->page_stride;
+  p.head_stride = mass->head_stride;
+  p.part = m.part ? static_cast<float*>(workspace) : nullptr;
+  p.tiles = m.tiles;
+  const sgr::MassKernel k = sgr::mass_kernel(c->head_dim, m.nt);
+  rc = launch(k.fn, dim3(m.grid), sgr::kMassThreads, k.smem, flags, stream, tk, p);
+  if (rc != SGR_OK || !m.part) return rc;
+  return launch(sgr::mass_join_kernel(), dim3(m.tiles, c->heads, b->batch), sgr::kAttnTile, 0, flags, stream, p);
+}
+
+// ------------------------------------------------------------ eviction
+using MoveFn = void (*)(const sgr::EvictParams);
+
+template <int D>
+MoveFn move_fn(int page_size) {
+  const int pass = page_size / (sgr::kMoveThreads / (D / 16));
+  return pass >= 4 && D == 128 ? sgr::kv_move_kernel<D, D == 128 ? 4 : 2> : pass >= 2 ? sgr::kv_move_kernel<D, 2> : sgr::kv_move_kernel<D, 1>;
+}
+
+int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses* mass, const sgr_kv_eviction* ev,
+              unsigned flags, void* stream) {
+  int rc = validate_evict(c, b, mass, ev);
+  if (rc != SGR_OK || b->batch == 0) return rc;
+  KvDevice* dev;
+  if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
+  // CTAs of a cluster: as many as hold a sequence's keys in shared memory, and
+  // more while the clusters do not fill the GPU.
+  const long long items = (long long)b->batch * c->heads, longest = (long long)b->max_pages * c->page_size;
+  int cluster = 1;
+  while (cluster < sgr::kSelectCluster &&
+         (longest > (long long)cluster * sgr::kSelectCached || (items * cluster < dev->sms && longest > cluster * 2048LL)))
+    cluster *= 2;
+  const long long moves = items * ev->max_pages;
+  if (items * cluster > 0x7fffffffLL || moves > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
+  sgr::EvictParams p;
+  p.cache = cache_of(*c);
+  p.batch = batch_of(*b);
+  p.mass = mass->data;
+  p.page_stride = mass->page_stride;
+  p.head_stride = mass->head_stride;
+  p.keep = ev->keep;
+  p.new_table = ev->table;
+  p.new_stride = ev->table_stride;
+  p.new_pages = ev->max_pages;
+  p.first = ev->first;
+  p.recent = ev->recent;
+  p.kept = ev->kept;
+  p.new_len = ev->new_len;
+  p.err = dev->err;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)(items * cluster));
+  lc.blockDim = dim3(sgr::kSelectThreads);
+  lc.dynamicSmemBytes = sizeof(sgr::SelectCtl);
+  lc.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = (flags & SGR_FLAG_NO_PDL) ? 1 : 2;
+  if (cudaLaunchKernelEx(&lc, sgr::kv_select_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SGR_ERR_LAUNCH;
+  }
+  if (moves == 0) return SGR_OK;
+  return launch(c->head_dim == 64 ? move_fn<64>(c->page_size) : move_fn<128>(c->page_size), dim3((unsigned)moves),
+                sgr::kMoveThreads, 0, flags, stream, p);
 }
 
 }  // namespace
@@ -532,7 +777,12 @@ int kv_init_device(int dev) {
     bool ok = true;
     for (int dim : {64, 128})
       for (int nt : {8, 16, 24, 32, sgr::kRowsNT})
-        ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(attn_kernel(dim, nt).fn)) == cudaSuccess;
+        for (bool masked : {false, true})
+          ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(attn_kernel(dim, nt, masked).fn)) == cudaSuccess;
+    for (int dim : {64, 128})
+      for (int nt : {8, 16, 32, sgr::kMassRows})
+        ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(mass_kernel(dim, nt).fn)) == cudaSuccess;
+    ok = ok && set_kernel_smem_attrs(reinterpret_cast<const void*>(kv_select_kernel)) == cudaSuccess;
     if (prev != dev) cudaSetDevice(prev);
     if (ok)
       d.status = device_error_word(dev, &d.err);
@@ -554,12 +804,25 @@ int sgr_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* q_
 
 int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* k,
                   const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, unsigned flags, void* stream) {
-  return run_append(cache, batch, q, k, v, q_out, nr, flags, stream);
+  return run_append(cache, batch, q, k, v, q_out, nr, nullptr, flags, stream);
+}
+
+int sgr_kv_append_at(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* k,
+                     const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, const int* positions,
+                     unsigned flags, void* stream) {
+  return run_append(cache, batch, q, k, v, q_out, nr, positions, flags, stream);
 }
 
 int sgr_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* out,
                      float scale, int window, void* workspace, int64_t workspace_bytes, unsigned flags, void* stream) {
-  return run_attention(cache, batch, q, out, scale, window, workspace, workspace_bytes, flags, stream);
+  const sgr_kv_mask mask = windowed(window);
+  return run_attention(cache, batch, q, out, nullptr, scale, &mask, workspace, workspace_bytes, flags, stream);
+}
+
+int sgr_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                            const sgr_heads* out, float* lse, float scale, const sgr_kv_mask* mask, void* workspace,
+                            int64_t workspace_bytes, unsigned flags, void* stream) {
+  return run_attention(cache, batch, q, out, lse, scale, mask, workspace, workspace_bytes, flags, stream);
 }
 
 int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads,
@@ -573,6 +836,36 @@ int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_
   return SGR_OK;
 }
 
+int sgr_kv_mass(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const float* lse,
+                const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask, void* workspace,
+                int64_t workspace_bytes, unsigned flags, void* stream) {
+  return run_mass(cache, batch, q, lse, mass, scale, mask, workspace, workspace_bytes, flags, stream);
+}
+
+int sgr_kv_mass_workspace(const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads, int64_t* bytes) {
+  if (!bytes) return SGR_ERR_NULL;
+  int rc;
+  if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
+  if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
+  *bytes = mass_plan(1, *cache, *batch, q_heads).bytes;
+  return SGR_OK;
+}
+
+int sgr_kv_evict(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_kv_masses* mass,
+                 const sgr_kv_eviction* eviction, unsigned flags, void* stream) {
+  return run_evict(cache, batch, mass, eviction, flags, stream);
+}
+
+int sgr_validate_kv_mass(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const float* lse,
+                         const sgr_kv_masses* mass, float scale, const sgr_kv_mask* mask) {
+  return validate_mass(cache, batch, q, lse, mass, scale, mask);
+}
+
+int sgr_validate_kv_evict(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_kv_masses* mass,
+                          const sgr_kv_eviction* eviction) {
+  return validate_evict(cache, batch, mass, eviction);
+}
+
 int sgr_validate_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_heads* q_out, const sgr_heads* k_out,
                               const int* positions, int tokens, int head_dim, const sgr_norm_rope* nr) {
   return validate_rope(q, k, q_out, k_out, positions, tokens, head_dim, nr);
@@ -580,12 +873,24 @@ int sgr_validate_qk_norm_rope(const sgr_heads* q, const sgr_heads* k, const sgr_
 
 int sgr_validate_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
                            const sgr_heads* k, const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr) {
-  return validate_append(cache, batch, q, k, v, q_out, nr);
+  return validate_append(cache, batch, q, k, v, q_out, nr, nullptr);
+}
+
+int sgr_validate_kv_append_at(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                              const sgr_heads* k, const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr,
+                              const int* positions) {
+  return validate_append(cache, batch, q, k, v, q_out, nr, positions);
 }
 
 int sgr_validate_kv_attention(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
                               const sgr_heads* out, float scale, int window) {
-  return validate_attention(cache, batch, q, out, scale, window);
+  const sgr_kv_mask mask = windowed(window);
+  return validate_attention(cache, batch, q, out, nullptr, scale, &mask);
+}
+
+int sgr_validate_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q,
+                                     const sgr_heads* out, const float* lse, float scale, const sgr_kv_mask* mask) {
+  return validate_attention(cache, batch, q, out, lse, scale, mask);
 }
 
 }  // extern "C"

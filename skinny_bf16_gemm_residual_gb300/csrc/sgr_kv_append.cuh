@@ -131,11 +131,20 @@ struct AppendParams {
   KvCacheRef cache;
   KvBatch batch;
   NormRope nr;
+  const int* positions;  // that rows are rotated to; NULL: their places in the cache
   unsigned* err;
   int q_blocks;         // blocks that take query rows: rows * q_chunks
   int q_chunks;         // blocks a query row
   int heads_per_block;  // query heads of such a block
 };
+
+// The position that a row is rotated to, from its place in the cache.
+__device__ __forceinline__ int append_position(const AppendParams& p, int row, int place) {
+  if (!p.positions || place < 0) return place;
+  const int pos = p.positions[row];
+  if (pos < 0) report_error(p.err, kErrIndex);
+  return max(pos, 0);
+}
 
 // The sequence of row `row` (-1: none), found by each warp in one pass over
 // the row offsets.
@@ -210,7 +219,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     const int b = find_row(p.batch, row);
     if (b < 0) return;  // a row of no sequence
     const KvSeq s = kv_seq(p.batch, p.cache.page_shift, b, p.err);
-    rope_row<D, kQPass>(p.q, p.qo, p.nr.q_weight, p.nr, row, s.len - s.n + row - s.row0, h0, p.err);
+    rope_row<D, kQPass>(p.q, p.qo, p.nr.q_weight, p.nr, row,
+                        append_position(p, row, s.len - s.n + row - s.row0), h0, p.err);
     return;
   }
   // ------------------------------------------------- one page's K or V of a head
@@ -253,7 +263,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     unpack8(v[i], x[i]);
     if (!is_v) {
       float4 cs, sn;
-      hl.angles(p.nr, min(t0 + i * kTok + tok, t1 - 1), cs, sn, p.err);
+      const int t = min(t0 + i * kTok + tok, t1 - 1);
+      hl.angles(p.nr, append_position(p, s.row0 + t - first, t), cs, sn, p.err);
       if (norm) head_norm<D>(x[i], w, p.nr.eps);
       hl.rotate(x[i], cs, sn);
     }

@@ -40,7 +40,7 @@ struct AttnSeg {
   int ta, tb;
   int tlo, thi;  // positions that some row of the tile sees
   int slot;      // of its partial sums
-  int pad;
+  int n, b;      // new tokens of the sequence, its number
 };
 
 // Owner of the partial sums of a row tile that begins in a CTA and ends in
@@ -57,20 +57,38 @@ struct AttnParams {
   KvBatch batch;
   float scale_log2;  // scale * log2(e)
   int window;        // INT_MAX: none
+  int sinks;         // first positions that stay visible (0 without a window)
   int group;         // query heads a key/value head
   unsigned group_inv;  // floor(2^32 / group), at most 2^32 - 1
   int reuse;         // row tiles of a sequence share the cache's bytes
   int whole;         // a row tile is one unit
+  const unsigned long long* tree;  // bits of the new tokens that a row sees, tree_words of them; NULL: those up to its own
+  long long tree_stride;
+  int tree_words;
+  float* lse;  // [rows][query heads], or NULL
   unsigned* err;
   float* part_o;      // [2 grid][NT][D]
   float2* part_ml;    // [2 grid][NT]  maximum, sum
   AttnPiece* pieces;  // [grid]
 };
 
-// Row tile j of a sequence: its rows, the positions they see, its tiles, its
-// units (a row tile that sees nothing is one unit: its zeros).
+// Row tile j of a sequence: its rows, the positions they see from the first
+// window on (tlo, below it the sinks alone), its tiles, its units (a row tile
+// that sees nothing is one unit: its zeros).  Tiles are numbered by position
+// from the windows' first on; the sinks' come right before it (TileMap).
 struct AttnItem {
   int r0, nrows, tlo, thi, ta, tb, units;
+};
+
+// Tile numbers of a row tile -> tiles by position: the tiles between the sinks
+// and the windows, `gap` of them, are left out.
+struct TileMap {
+  int tw, gap;
+
+  // (sinks = 0: the identity)
+  __device__ __forceinline__ TileMap(int tlo, int sinks)
+      : tw(tlo / kAttnTile), gap(tw - min((int)(((unsigned)sinks + kAttnTile - 1) / kAttnTile), tw)) {}
+  __device__ __forceinline__ int at(int t) const { return t < tw ? t - gap : t; }
 };
 
 // r / group for 0 <= r < 2^31: the product is at most one too small.
@@ -97,35 +115,95 @@ __host__ __device__ __forceinline__ int row_first(int tlo, int last, int window)
   return lo < tlo ? tlo : lo;
 }
 
-template <int NT>
+// Whether a row sees a position: in its window, or a sink up to its own.
+__host__ __device__ __forceinline__ bool row_sees(int pos, int last, int window, int sinks) {
+  return row_sees(pos, last, window) || (pos < sinks && pos <= last);
+}
+
+// ------------------------------------------------------------ drafted trees
+// A row's bits from the j-th new token on, 32 of them (bits past the last word
+// are zeros).
+__device__ __forceinline__ uint32_t tree_bits(const unsigned long long* row, int words, int j) {
+  const int w = j >> 6, s = j & 63;
+  const unsigned long long lo = w < words ? row[w] : 0ULL, hi = s > 32 && w + 1 < words ? row[w + 1] : 0ULL;
+  return (uint32_t)(lo >> s) | (s > 32 ? (uint32_t)(hi << (64 - s)) : 0u);
+}
+
+// A row of a tree, the tok-th of n of a sequence: the position that it stands
+// for, behind as many as it sees of the new ones but itself (-1: a padding row),
+// and whether it sees any of the new ones.
+struct TreeRow {
+  int last;
+  bool drafts;
+};
+
+__device__ __forceinline__ TreeRow tree_row(const AttnParams& p, int row0, int n, int first, int tok) {
+  if (first + tok < 0) return {-1, false};
+  const unsigned long long* bits = p.tree + (long long)(row0 + tok) * p.tree_stride;
+  const int j0 = first < 0 ? -first : 0;  // new tokens before the first position are not there
+  int count = 0;
+  for (int w = 0; w < p.tree_words && 64 * w < n; ++w) {
+    unsigned long long x = bits[w];
+    if (n - 64 * w < 64) x &= (1ULL << (n - 64 * w)) - 1;
+    if (j0 > 64 * w) x = j0 - 64 * w < 64 ? x >> (j0 - 64 * w) << (j0 - 64 * w) : 0ULL;
+    count += __popcll(x);
+  }
+  return {max(first, 0) + max(count - 1, 0), count > 0};
+}
+
+// Bits of the positions x .. x + 31 that lie in [lo, hi].
+__device__ __forceinline__ uint32_t span_bits(int x, int lo, int hi) {
+  const int a = max(lo - x, 0), b = min(hi - x, 31);
+  return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
+}
+
+// Bits of the positions x .. x + 31 (x >= 0) that a row with this `last` sees;
+// thi: behind the sequence's last position, first: its first new one.
+__device__ __forceinline__ uint32_t row_bits(const AttnParams& p, int x, int last, int thi, int first, int row) {
+  uint32_t m = span_bits(x, max(last - p.window + 1, 0), last) | span_bits(x, 0, min(last, p.sinks - 1));
+  if (p.tree && x + 31 >= first) {
+    m &= span_bits(x, 0, first - 1);
+    if (last >= 0) {
+      const unsigned long long* bits = p.tree + (long long)row * p.tree_stride;
+      const int j = x - first;
+      const uint32_t t = j >= 0 ? tree_bits(bits, p.tree_words, j) : tree_bits(bits, p.tree_words, 0) << -j;
+      m |= t & span_bits(x, 0, thi - 1);
+    }
+  }
+  return m;
+}
+
+template <int NT, bool kMasked>
 __device__ __forceinline__ AttnItem attn_item(const AttnParams& p, const KvSeq& s, int j) {
   AttnItem it;
   it.r0 = j * NT;
   it.nrows = min(NT, s.n * p.group - it.r0);
-  const int first = s.len - s.n, p0 = first + div_group(p, it.r0);
-  it.thi = max(first + div_group(p, max(it.r0 + it.nrows - 1, 0)) + 1, 0);
+  // (every row of a tree may see all of its new tokens, and stands for the first one's position at least)
+  const int first = s.len - s.n, p0 = kMasked && p.tree ? first : first + div_group(p, it.r0);
+  it.thi = max(kMasked && p.tree ? s.len : first + div_group(p, max(it.r0 + it.nrows - 1, 0)) + 1, 0);
   it.tlo = p.window > p0 ? 0 : p0 - p.window + 1;
-  it.ta = it.thi > 0 ? it.tlo / kAttnTile : 0;
+  it.ta = it.thi <= 0 ? 0 : kMasked ? TileMap(it.tlo, p.sinks).gap : it.tlo / kAttnTile;
   it.tb = (it.thi + kAttnTile - 1) / kAttnTile;
   it.units = p.whole || it.tb <= it.ta ? 1 : it.tb - it.ta + 1;  // the first for its beginning and end
   return it;
 }
 
-template <int NT>
+template <int NT, bool kMasked>
 __device__ __forceinline__ int attn_seq_units(const AttnParams& p, const KvSeq& s) {
   int u = 0;
-  for (int j = 0; j * NT < s.n * p.group; ++j) u += attn_item<NT>(p, s, j).units;
+  for (int j = 0; j * NT < s.n * p.group; ++j) u += attn_item<NT, kMasked>(p, s, j).units;
   return u;
 }
 
 // The warp that walks a CTA's share of the work: finds it, hands out its
 // segments, loads the pages of its tiles by TMA (V, then K, of a stage of the
-// ring) and writes their scales beside them.  Rows that see nothing get their
-// zeros here.  Executed by one whole warp.
-template <int D, int NT, class Ctl>
+// ring; without Ctl::kValues K alone) and writes their scales beside them.  Rows
+// that see nothing get their zeros here.  Executed by one whole warp.
+template <int D, int NT, bool kMasked, class Ctl>
 __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUtensorMap& tmK, const CUtensorMap& tmV,
                                           uint32_t ring) {
-  constexpr int S = Ctl::kStages, M = Ctl::kMeta, kTile = kAttnTile * D, kStage = 2 * kTile;
+  constexpr bool kValues = Ctl::kValues;
+  constexpr int S = Ctl::kStages, M = Ctl::kMeta, kTile = kAttnTile * D, kStage = (kValues ? 2 : 1) * kTile;
   const int lane = threadIdx.x & 31;
   volatile int* abort_flag = &c.abort;
   // ------------------------------------------------ this CTA's share of the work
@@ -143,7 +221,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
 #pragma unroll 4
     for (int x = b_first; x < b_last; ++x) {
       s = kv_seq(p.batch, ps, x, p.err);
-      units = attn_seq_units<NT>(p, s);
+      units = attn_seq_units<NT, kMasked>(p, s);
       mine += units * hk;
     }
     int upto = mine;
@@ -176,7 +254,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
           if (b >= p.batch.batch) found = false;
           if (!found) break;
           s = kv_seq(p.batch, ps, b, nullptr);
-          units = attn_seq_units<NT>(p, s);
+          units = attn_seq_units<NT, kMasked>(p, s);
           if (off < units * hk) break;
           off -= units * hk;
         }
@@ -184,7 +262,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       if (!found) u1 = u, off = 0, units = 1;
       h = off / units;
       off -= h * units;
-      for (int x; found && off >= (x = attn_item<NT>(p, s, j).units); ++j) off -= x;
+      for (int x; found && off >= (x = attn_item<NT, kMasked>(p, s, j).units); ++j) off -= x;
       skip = off;
     }
   }
@@ -198,7 +276,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   AttnItem it{};
   bool ok = true;
   AttnPiece piece{};  // of the row tile that goes on in the next CTA
-  if (u < u1) it = attn_item<NT>(p, s, j);
+  if (u < u1) it = attn_item<NT, kMasked>(p, s, j);
   int t = 0, t_end = 0;  // tiles of the segment handed out last
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok && !mbar_wait_nap<kNap>(smem_u32(bar), parity, abort_flag)) {
@@ -239,18 +317,20 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
             s = kv_seq(p.batch, ps, b, nullptr);
           } while (s.n == 0);
         }
-        it = attn_item<NT>(p, s, 0);
+        it = attn_item<NT, kMasked>(p, s, 0);
       }
       const int units = it.units, take = min(u1 - u, units - skip);
       u += take;
       if (it.tb <= it.ta) {  // rows that see nothing: zeros
-        for (int e = lane; e < it.nrows * (D / 8); e += 32) {
+        for (int e = lane; kValues && e < it.nrows * (D / 8); e += 32) {
           const int r = it.r0 + e / (D / 8), tok = div_group(p, r);
           *reinterpret_cast<uint4*>(p.out.p + (long long)(s.row0 + tok) * p.out.ts +
                                     (long long)(h * p.group + r - tok * p.group) * p.out.hs + e % (D / 8) * 8) =
               make_uint4(0u, 0u, 0u, 0u);
+          if (kMasked && p.lse && e % (D / 8) == 0)
+            p.lse[(long long)(s.row0 + tok) * p.q.heads + h * p.group + r - tok * p.group] = -INFINITY;
         }
-        it = attn_item<NT>(p, s, ++j);
+        it = attn_item<NT, kMasked>(p, s, ++j);
         continue;
       }
       AttnSeg g;
@@ -266,31 +346,44 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       g.tlo = it.tlo;
       g.thi = it.thi;
       g.slot = 2 * (int)blockIdx.x + (g.kind & kSegStart ? 1 : 0);
-      g.pad = 0;
+      g.n = s.n;
+      g.b = b;
       hand_out(g);
       if (!ok) return false;
-      if (g.kind == kSegStart) piece = {cta_of(u + units - skip - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
+      if (kValues && g.kind == kSegStart) piece = {cta_of(u + units - skip - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
       t = g.ta;
       t_end = g.tb;
       cur = it;
       cur_h = h;
       cur_b = b;
-      cur_p0 = g.first + div_group(p, it.r0);
+      cur_p0 = kMasked && p.tree ? g.first - 1 : g.first + div_group(p, it.r0);  // rows see the same up to it, but for windows
       cur_p1 = it.thi - 1;
       skip = 0;
-      if (g.kind & kSegEnd) it = attn_item<NT>(p, s, ++j);
+      if (g.kind & kSegEnd) it = attn_item<NT, kMasked>(p, s, ++j);
     }
-    const int x0 = t * kAttnTile, x1 = x0 + kAttnTile;
+    const TileMap tm(cur.tlo, kMasked ? p.sinks : 0);
+    const bool sink = kMasked && t < tm.tw;  // a tile before the windows: rows see its sinks alone
+    const int x0 = (kMasked ? tm.at(t) : t) * kAttnTile, x1 = x0 + kAttnTile;
     ++t;
     x.h = cur_h;
-    x.live0 = max(cur.tlo - x0, 0);
-    x.live1 = min(cur.thi - x0, kAttnTile);
-    x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
-    if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
+    if (sink) {
+      x.live0 = 0;
+      x.live1 = min(p.sinks - x0, kAttnTile);
+      x.flags = x.live1 < kAttnTile ? 1 : 0;
+    } else {
+      x.live0 = max(cur.tlo - x0, 0);
+      x.live1 = min(cur.thi - x0, kAttnTile);
+      x.flags = (x0 < cur.tlo || x1 > cur.thi) ? 1 : 0;
+      if (min(x1, cur.thi) - 1 > max(cur_p0, -1) || max(x0, cur.tlo) < (long long)cur_p1 - p.window + 1) x.flags |= 2;
+      if (kMasked && x.live0 > 0 && p.sinks > x0) {  // sinks and windows in one tile, perhaps with a gap
+        x.live0 = 0;
+        x.flags |= 2;
+      }
+    }
     // This lane's page of the tile, where some row sees a position of it.
     const int block = (x0 >> ps) + lane, at = block << ps;
     x.page = -1;
-    if (lane < (kAttnTile >> ps) && at < cur.thi && at + (1 << ps) > cur.tlo) {
+    if (lane < (kAttnTile >> ps) && at < cur.thi && (at + (1 << ps) > cur.tlo || (kMasked && at < p.sinks))) {
       x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
       x.flags |= 4;
     }
@@ -306,7 +399,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     if (x.page >= 0) {
       const long long at = (long long)x.page * p.cache.scale_stride + x.h;
       x.ks = p.cache.k_scale[at];
-      x.vs = p.cache.v_scale[at];
+      if (kValues) x.vs = p.cache.v_scale[at];
     }
   };
   // One tile ahead of the copies: its table entries are asked for before
@@ -322,23 +415,26 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     if (i >= S) wait(&c.empty[slot], par ^ 1u);
     if (!ok) break;
     const unsigned live = __ballot_sync(0xffffffffu, a.page >= 0);
-    const uint32_t kb = smem_u32(&c.kfull[slot]), vb = smem_u32(&c.vfull[slot]);
+    const uint32_t kb = smem_u32(&c.kfull[slot]);
     if (lane == 0) {
       mbar_expect_tx(kb, (uint32_t)__popc(live) * page_bytes);
-      mbar_arrive_expect_tx(vb, (uint32_t)__popc(live) * page_bytes);
+      if constexpr (kValues) mbar_arrive_expect_tx(smem_u32(&c.vfull[slot]), (uint32_t)__popc(live) * page_bytes);
     }
     __syncwarp();
     if (a.page >= 0) {
       const uint32_t dst = ring + (uint32_t)slot * kStage + (uint32_t)lane * page_bytes;
-      tma_load_4d(dst + kTile, &tmK, 0, 0, a.h, a.page, kb, policy);
-      tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, vb, policy);
+      tma_load_4d(dst + kStage - kTile, &tmK, 0, 0, a.h, a.page, kb, policy);
+      if constexpr (kValues) tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, smem_u32(&c.vfull[slot]), policy);
     }
     has = next_tile(next);
     const int meta = i % M;
     if (lane < per_tile) {
       c.kscale[meta][lane] = a.ks;
       // (an exponent of -inf marks a page that is not there)
-      c.vexp[meta][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
+      if constexpr (kValues)
+        c.vexp[meta][lane] = a.page >= 0 ? (float)((int)((__float_as_uint(a.vs) >> 23) & 0xFF) - 127) : -INFINITY;
+      else
+        c.page[meta][lane] = a.page;
     }
     if (lane == 0) {
       c.flags[meta] = (a.flags & 3) | (__popc(live) < per_tile ? 1 : 0);
@@ -356,7 +452,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     if (has) load_scales(a);
   }
   bool stopped = false;
-  if (Ctl::kStopStage && ok) {  // a stage that ends the sequence
+  if constexpr (Ctl::kStopStage) if (ok) {  // a stage that ends the sequence
     if (i >= S) wait(&c.empty[slot], par ^ 1u);
     stopped = ok;
     if (ok && lane == 0) {
@@ -368,12 +464,14 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   AttnSeg stop{};
   stop.kind = kSegStop;
   hand_out(stop);
-  if (lane == 0) p.pieces[blockIdx.x] = piece;
+  if (kValues && lane == 0) p.pieces[blockIdx.x] = piece;
   // Every copy that this warp issued lands before the CTA may exit.  (The
   // stage that the stop took was empty: its copies have landed.)
   bool landed = true;
-  for (int k = max(i - S + (stopped ? 1 : 0), 0); k < i && landed; ++k)
-    landed = mbar_wait(smem_u32(&c.kfull[k % S]), (k / S) & 1) && mbar_wait(smem_u32(&c.vfull[k % S]), (k / S) & 1);
+  for (int k = max(i - S + (stopped ? 1 : 0), 0); k < i && landed; ++k) {
+    landed = mbar_wait(smem_u32(&c.kfull[k % S]), (k / S) & 1);
+    if constexpr (kValues) landed = landed && mbar_wait(smem_u32(&c.vfull[k % S]), (k / S) & 1);
+  }
   if (!landed) report_error(p.err, kErrDrain);
 }
 
@@ -453,6 +551,13 @@ __device__ __forceinline__ uint32_t lds8(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
+}
+
+// Logarithm of the sum of a row's exponentials, from its R and the sum of its
+// weights (256 p: the 8).  The sum has 24 bits and R is whole, so it is good to
+// some 2^-23 of the larger of itself and 1.
+__device__ __forceinline__ float log_sum_exp(float R, float sum) {
+  return sum == 0.f ? -INFINITY : (R - 8.f + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Joins the partial sums of row tiles that span CTAs: blocks x = c take the row
@@ -549,6 +654,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attn_join_kernel(const AttnPa
   }
   const float f = sum == 0.f ? 0.f : 1.f / sum;
   const int r = own.r0 + q, tok = div_group(p, r);
+  if (p.lse && lane == 0) {
+    if constexpr (kParts > 1) {
+      m = part_ml[row][0].x;
+#pragma unroll
+      for (int k = 1; k < kParts; ++k) m = fmaxf(m, part_ml[row][k].x);
+    }
+    p.lse[(long long)(own.row0 + tok) * p.q.heads + own.h * p.group + r - tok * p.group] = log_sum_exp(m, sum);
+  }
   __nv_bfloat16* out = p.out.p + (long long)(own.row0 + tok) * p.out.ts +
                        (long long)(own.h * p.group + r - tok * p.group) * p.out.hs + lane * kE;
   if constexpr (kE == 4)

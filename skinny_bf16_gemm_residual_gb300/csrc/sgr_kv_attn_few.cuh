@@ -83,7 +83,7 @@ struct AttnShape {
 template <int D, int NT>
 struct AttnCtl {
   using Sh = AttnShape<D, NT>;
-  static constexpr bool kStopStage = false;
+  static constexpr bool kStopStage = false, kValues = true;
   static constexpr int kStages = Sh::kStages, kMeta = kStages, S = kStages, Q = Sh::kQBufs, C = Sh::kC;
   uint64_t kfull[S], vfull[S], empty[S];
   uint64_t sfull[2], sempty[2], ofull[2], oempty[2], qfull[Q], qempty[Q], pfull, drain;
@@ -97,7 +97,9 @@ struct AttnCtl {
   int flags[S], live[S][2];        // flags: 1: some token is not live, 2: rows see different tokens; live tokens
   long long qout[Q][NT];           // a row's place in the output
   alignas(16) float qf[Q][NT];     // its score factor
-  int qpos[Q][NT];                 // the last position that it sees
+  int qpos[Q][NT];                 // the last position that it sees, by itself
+  int qrow[Q][NT];                 // the row (of a tree's bits)
+  int qspan[Q][2];                 // the segment's first new position, and where its windows begin
   alignas(16) float wmax[Sh::kSoftmax][C], wsum[Sh::kSoftmax][C];
   alignas(16) float ref[Sh::kSoftmax][C], alpha[Sh::kSoftmax][2][C];  // a warp's own copies
 };
@@ -205,7 +207,7 @@ __device__ __forceinline__ void tmem_ld_sum3(uint32_t w0, uint32_t apart, float 
   for (int q = 0; q < 8; ++q) x[q] = fmaf(fmaf(w[q], kLoScale, v[q]), kLoScale, x[q]);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kMasked>
 __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::kCtas)
     kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
   using Sh = AttnShape<D, NT>;
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
   if (warp < kSoftmax + 2) pdl_wait();  // (the query warps do after their dry run)
 
   if (warp == kSoftmax) {
-    attn_walk<D, NT>(c, p, tmK, tmV, ring);
+    attn_walk<D, NT, kMasked>(c, p, tmK, tmV, ring);
   } else if (warp == kSoftmax + 1) {
     // ------------------------------------------------------------- MMA issuer
     // Issues whichever of the two products can go: V^T P^T of the oldest tile
@@ -378,32 +380,34 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         if (g.kind & kSegStop) break;
       }
       // Row `pass` of this thread's: two are under way while one is converted.
-      auto load_row = [&](int pass, long long& out_at, int& pos) {
+      auto load_row = [&](int pass, long long& out_at, int& pos, int& row) {
         const int q = pass * kRows + qt / kLanes;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         pos = -1;  // a row that is none sees nothing
         out_at = 0;
+        row = 0;
         if (q < g.nrows) {
           const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
-          pos = row_last(g.first, tok);
+          pos = kMasked && p.tree ? tree_row(p, g.row0, g.n, g.first, tok).last : row_last(g.first, tok);
+          row = g.row0 + tok;
           out_at = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
           v = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         }
         return v;
       };
       long long out0, out1 = 0;
-      int pos0, pos1 = -1;
-      uint4 v0 = load_row(0, out0, pos0), v1 = v0;
-      if (kPass > 1) v1 = load_row(1, out1, pos1);
+      int pos0, pos1 = -1, row0, row1 = 0;
+      uint4 v0 = load_row(0, out0, pos0, row0), v1 = v0;
+      if (kPass > 1) v1 = load_row(1, out1, pos1, row1);
       if (lane == 0 && !dry) ok = mbar_wait_nap<kNap>(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll 1
       for (int i = 0; i < kPass; ++i) {
-        const int q = i * kRows + qt / kLanes, pos = pos0;
+        const int q = i * kRows + qt / kLanes, pos = pos0, row = row0;
         const long long out_at = out0;
         const uint4 v = v0;
-        v0 = v1, out0 = out1, pos0 = pos1;
-        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1);
+        v0 = v1, out0 = out1, pos0 = pos1, row0 = row1;
+        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1, row1);
         const QuerySplit s = split_query<kLanes>(v, 1.f, 32.f);
         const uint32_t qb = qbuf + (uint32_t)(buf * Sh::kQBytes) + (uint32_t)((l & 1) * 8);
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(s.hi.x), "r"(s.hi.y) : "memory");
@@ -412,6 +416,11 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
           c.qf[buf][q] = s.factor * p.scale_log2;
           c.qpos[buf][q] = pos;
           c.qout[buf][q] = out_at;
+          if (kMasked) c.qrow[buf][q] = row;
+        }
+        if (kMasked && qt == 0 && i == 0) {
+          c.qspan[buf][0] = g.first;
+          c.qspan[buf][1] = g.tlo;
         }
       }
       fence_proxy_async_smem();
@@ -482,6 +491,18 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
       wait(&c.qfull[buf], qpar);
 #pragma unroll
       for (int q = 0; q < C; ++q) o[q] = l[q] = 0.f;
+      auto tile_at = [&](int t) { return kMasked ? TileMap(c.qspan[buf][1], p.sinks).at(t) : t; };
+      // Whether column q0 + q sees a position.  (What only tiles with masks need
+      // is read from shared memory there: registers are full.)
+      auto sees = [&](int pos, int q) {
+        const int last = c.qpos[buf][q0 + q], j = pos - c.qspan[buf][0];
+        if (!kMasked) return row_sees(pos, last, p.window);
+        if (p.tree && j >= 0) {
+          if (last < 0 || (j >> 6) >= p.tree_words) return false;
+          return (p.tree[c.qrow[buf][q0 + q] * p.tree_stride + (j >> 6)] >> (j & 63) & 1) != 0;
+        }
+        return row_sees(pos, last, p.window, p.sinks);
+      };
       run = -3.0e38f;
       if (lane < C) c.ref[warp][lane] = run;
       nan_rows = 0;
@@ -495,16 +516,27 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.sempty[sb]));
-        const int pi = tok >> p.cache.page_shift, flags = c.flags[slot], pos = t * kAttnTile + tok;
+        const int pi = tok >> p.cache.page_shift, flags = c.flags[slot];
         const float ks = c.kscale[slot][pi], ve = c.vexp[slot][pi];
         const bool live = !(flags & 1) || (tok >= c.live[slot][0] && tok < c.live[slot][1] && ve > -INFINITY);
 #pragma unroll
         for (int q = 0; q < C; ++q) x[q] = fmaf(x[q], ks * c.qf[buf][q0 + q], ve + 8.f);  // weights come as 256 p
         if (__builtin_expect(flags & 2, 0)) {
+          if constexpr (kMasked) {
+            const int pos = tile_at(t) * kAttnTile + tok;
+            unsigned seen = 0;  // (a rolled loop: unrolled it would cost registers)
+#pragma unroll 1
+            for (int q = 0; live && q < C; ++q) seen |= sees(pos, q) ? 1u << q : 0u;
 #pragma unroll
-          for (int q = 0; q < C; ++q) {
-            const int last = c.qpos[buf][q0 + q];
-            if (!(live && row_sees(pos, last, p.window))) x[q] = -INFINITY;
+            for (int q = 0; q < C; ++q)
+              if (!(seen >> q & 1)) x[q] = -INFINITY;
+          } else {
+            const int pos = t * kAttnTile + tok;
+#pragma unroll
+            for (int q = 0; q < C; ++q) {
+              const int last = c.qpos[buf][q0 + q];
+              if (!(live && row_sees(pos, last, p.window))) x[q] = -INFINITY;
+            }
           }
         } else if (!live) {
 #pragma unroll
@@ -576,8 +608,7 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
                 if (!(c.nan_tokens[k >> 5] >> (k & 31) & 1) || tok >= D) continue;
                 if ((lds8(vt + swizzled<D>(k, tok >> 4) + (tok & 15)) & 0x7F) != 0x7F) continue;
                 for (int q = 0; q < C; ++q) {
-                  const int last = c.qpos[buf][q0 + q], kp = t * kAttnTile + k;
-                  if (row_sees(kp, last, p.window)) nan_rows |= 1u << q;
+                  if (sees(tile_at(t) * kAttnTile + k, q)) nan_rows |= 1u << q;
                 }
               }
               __syncwarp();
@@ -628,6 +659,10 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         c.ref[warp][lane] = sum == 0.f ? 0.f : 1.f / sum;  // (R is not needed any more)
         if (!whole && (warp & 3) == 0 && q0 + lane < g.nrows)
           p.part_ml[(long long)g.slot * NT + q0 + lane] = make_float2(run, sum);
+        if (kMasked && p.lse && whole && (warp & 3) == 0 && q0 + lane < g.nrows) {
+          const int r = g.r0 + q0 + lane, row_tok = div_group(p, r);
+          p.lse[(long long)(g.row0 + row_tok) * p.q.heads + g.h * p.group + r - row_tok * p.group] = log_sum_exp(run, sum);
+        }
       }
       __syncwarp();
       if (tok < D) {

@@ -48,7 +48,7 @@ constexpr int kRowsNT = 256, kRowsThreads = 704;
 template <int D>
 struct RowsCtl {
   static constexpr int kStages = 2, kMeta = 4, S = kStages, M = kMeta;
-  static constexpr bool kStopStage = true;
+  static constexpr bool kStopStage = true, kValues = true;
   uint64_t kfull[S], vfull[S], empty[S];
   uint64_t sfull[2], pfull[2], pvdone[2], wfull[2], wempty[2], qfull[2], drain;
   uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
@@ -123,7 +123,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return r;
 }
 
-template <int D>
+template <int D, bool kMasked>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     kv_attn_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const AttnParams p) {
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   };
 
   if (warp == 20) {
-    attn_walk<D, NT>(c, p, tmK, tmV, ring);
+    attn_walk<D, NT, kMasked>(c, p, tmK, tmV, ring);
   } else if (warp == 21) {
     // ------------------------------------------------------------- MMA issuer
     // Order: PV of half 0, next scores of half 0, PV of half 1, next scores of
@@ -374,10 +374,18 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       }
       const int q = 128 * half + row, r = g.r0 + q, rtok = div_group(p, r);
       const bool real = q < g.nrows;
-      const int last = real ? row_last(g.first, rtok) : -1;
-      const int see0 = row_first(g.tlo, last, p.window), see1 = min(g.thi - 1, last);
+      int last = real ? row_last(g.first, rtok) : -1;
+      bool sees = last >= 0;
+      if (kMasked && p.tree && real) {
+        const TreeRow tr = tree_row(p, g.row0, g.n, g.first, rtok);
+        last = tr.last;
+        // (a row without a new one sees the positions before them, where its window or the sinks reach there)
+        sees = tr.drafts || (last >= 0 && g.first > 0 && (p.window > 1 || p.sinks > 0));
+      }
+      auto tile_at = [&](int t) { return kMasked ? TileMap(g.tlo, p.sinks).at(t) : t; };
+      const int see0 = row_first(g.tlo, last, p.window), see1 = min(g.thi - 1, last);  // (without a mask beyond the window)
       // (a padding row's scores are all -inf: its query, NaN perhaps, has no part in them)
-      const float qf = see0 <= see1 ? c.qf[q] : 0.f;
+      const float qf = sees ? c.qf[q] : 0.f;
       // Factor of a page's scores: with the key scale it may underflow (a row of
       // zeros has qf near 2^-129, a page of zeros the scale 2^-64), and a masked
       // score, -inf, times zero is not -inf.  A score is below 2^24 in magnitude,
@@ -395,6 +403,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         tc_fence_after();
         const int flags = c.flags[meta], ps = p.cache.page_shift;
         const int c0 = see0 - t * kAttnTile, cn = see1 - t * kAttnTile - c0;  // columns that the row sees: c0 .. c0 + cn
+        // Bits of columns 32 k on that the row sees.
+        auto seen = [&](int k) { return row_bits(p, tile_at(t) * kAttnTile + 32 * k, last, g.thi, g.first, g.row0 + rtok); };
         // The loops over a thread's columns stay rolled: unrolled, the body
         // does not fit the instruction caches, and the warps of four roles
         // then wait for instructions most of the time (a chunk of a prompt:
@@ -405,13 +415,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           for (int k = 2 * sub; k < 2 * sub + 2; ++k) {
             tmem_ld32(s_cols + 32 * k, x);
             tmem_wait_ld32(x);
+            const uint32_t bits = kMasked ? seen(k) : 0u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const bool there = cn >= 0 && c.vexp[meta][(32 * k + 16 * h) >> ps] > -INFINITY;
+              const bool page = c.vexp[meta][(32 * k + 16 * h) >> ps] > -INFINITY, there = page && cn >= 0;
+              const uint32_t mine = page ? bits >> (16 * h) : 0u;
               uint32_t w[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                w[e] = there && (unsigned)(32 * k + 16 * h + e - c0) <= (unsigned)cn ? x[16 * h + e] : 0xFF800000u;
+              for (int e = 0; e < 16; ++e) {
+                const bool sees_it = kMasked ? (mine >> e & 1) != 0 : there && (unsigned)(32 * k + 16 * h + e - c0) <= (unsigned)cn;
+                w[e] = sees_it ? x[16 * h + e] : 0xFF800000u;
+              }
               tmem_st16(s_cols + 32 * k + 16 * h, w);
             }
           }
@@ -483,7 +497,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           for (int m = 0; m < 4; ++m)
             for (unsigned left = c.nan_tokens[i & 1][m]; left; left &= left - 1) {
               const int k = 32 * m + __ffs(left) - 1;
-              if (cn < 0 || (unsigned)(k - c0) > (unsigned)cn) continue;
+              if (kMasked ? !(seen(m) >> (k & 31) & 1) : cn < 0 || (unsigned)(k - c0) > (unsigned)cn) continue;
 #pragma unroll
               for (int e = 0; e < 4; ++e) nan_d[e] |= c.nan_mask[i & 1][k][e];
             }
@@ -529,6 +543,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             *reinterpret_cast<uint4*>(part + 32 * k + 4 * e) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
+      if (kMasked && p.lse && real && whole && sub == 0) p.lse[(long long)(g.row0 + rtok) * p.q.heads + head] = log_sum_exp(R, l);
       if (real && !whole && sub == 0) p.part_ml[(long long)g.slot * NT + q] = make_float2(unset ? -3.0e38f : R, l);
       tc_fence_before();
     }

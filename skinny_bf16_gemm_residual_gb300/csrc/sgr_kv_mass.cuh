@@ -1,0 +1,432 @@
+// sgr_kv_mass.cuh -- the attention weight that cached positions get from the
+// new tokens' rows, added to what they have (sgr_attention.h):
+//
+//     mass[t, h] += sum over rows r and heads of h's group of 2^(s_rt - L_r)
+//     s = scale log2(e) q.k,   L = log2(e) lse
+//
+// With the rows' log-sum-exp known a position's sum needs its own key alone:
+// one pass over K, no maxima, and every sum within one thread.  As in the
+// attention kernel (sgr_kv_attn_few.cuh) the codes of 128 keys are the 128-row
+// operand of the FP8 tensor core as they are,
+//
+//     S^T [128 keys, 2 rows] = K Q^T
+//
+// with the rows' queries in two E4M3 parts b = hi + lo / 32 side by side (8
+// significant bits, all of a BF16 query, down to 2^-14 of its row's largest
+// and an absolute 2^-22 of it below).  Thread = key: it reads its lane of the
+// accumulator, adds the parts in FP32, and sums 2^(s - L) over the columns.
+//
+// Rows that share a key/value head go in products of up to 32.  Up to 256 of
+// them, their queries all in shared memory, meet a tile of keys while it is
+// there (it is read once); more are several row tiles, whose sums go to the
+// workspace and are added in order by a second kernel: no atomics on one
+// address from two places, the same bits on every run.  Every CTA takes the
+// same number of (row tile, key tile) units (attn_walk).
+//
+// Roles: warps 0-3 weigh (thread = key), warp 4 walks the work and loads
+// pages, warp 5 issues the MMAs, warps 6-7 bring queries into the operand, a
+// ring of products' worth of rows.
+#pragma once
+
+#include "sgr_kv_attn_few.cuh"
+
+namespace sgr {
+
+struct MassParams {
+  AttnParams a;  // (lse: input; out, partial sums and pieces unused)
+  float* mass;
+  long long page_stride, head_stride;  // elements
+  float* part;  // [row tile][key/value head][128 tiles positions], NULL: one row tile a sequence
+  int tiles;    // of a sequence, at most
+};
+
+constexpr int kMassThreads = 256, kMassAcc = 4;
+constexpr int kMassRows = 256;  // of the largest row tile
+
+template <int D, int NT>
+struct MassShape {
+  static constexpr int kRows = NT < 32 ? NT : 32;  // of a product
+  static constexpr int kCols = 2 * kRows;
+  static constexpr int kTileBytes = kAttnTile * D;
+  static constexpr int kSlotBytes = kCols * D;
+  // As many stages of keys and slots of queries as two CTAs an SM allow.
+  static constexpr int kStages = D == 128 ? (NT <= 16 ? 6 : NT == 32 ? 5 : 2) : (NT <= 16 ? 10 : NT == 32 ? 8 : 4);
+  static constexpr int kSlots = NT == 256 ? 8 : NT == 32 ? 3 : 4;
+  static constexpr int kTmemCols = kMassAcc * kCols;
+};
+
+template <int D, int NT>
+struct MassCtl {
+  using Sh = MassShape<D, NT>;
+  static constexpr bool kStopStage = false, kValues = false;
+  static constexpr int kStages = Sh::kStages, kMeta = kStages, S = kStages, Q = Sh::kSlots;
+  uint64_t kfull[S], empty[S];
+  uint64_t sfull[kMassAcc], sempty[kMassAcc], qfull[Q], qempty[Q], drain;
+  uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
+  uint32_t tmem;
+  int abort;
+  int go[2];
+  AttnSeg seg[kAttnQueue];
+  float kscale[S][8];  // of a stage's pages
+  int page[S][8];      // (-1: not there)
+  int flags[S], live[S][2];
+  alignas(16) float qf[Q][Sh::kRows];  // a row's score factor
+  alignas(16) float ql[Q][Sh::kRows];  // and -L (-inf: a row that counts for nothing)
+  int qpos[Q][Sh::kRows];              // the last position that it sees, by itself
+  int qrow[Q][Sh::kRows];              // the row (of a tree's bits)
+};
+
+template <int D, int NT>
+constexpr int mass_ctl_bytes() {
+  return (int)((sizeof(MassCtl<D, NT>) + 1023) / 1024 * 1024);
+}
+
+template <int D, int NT>
+constexpr int mass_smem_bytes() {
+  using S = MassShape<D, NT>;
+  return mass_ctl_bytes<D, NT>() + S::kStages * S::kTileBytes + S::kSlots * S::kSlotBytes;
+}
+
+// Where a row tile's sums of a key/value head go in `part`: a sequence's row
+// tiles are numbered from one for every NT rows before it and one a sequence.
+template <int NT>
+__device__ __forceinline__ long long mass_part(const MassParams& p, int b, int row0, int j, int h) {
+  const long long tile = (long long)row0 * p.a.group / NT + b + j;
+  return (tile * p.a.cache.heads + h) * p.tiles * kAttnTile;
+}
+
+// Pairs of FP32 values, one instruction for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_parts(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// Whether a row sees a position (`last`, `row`: MassCtl's).
+__device__ __forceinline__ bool mass_sees(const AttnParams& p, int pos, int first, int last, int row) {
+  const int j = pos - first;
+  if (p.tree && j >= 0) {
+    if (last < 0 || (j >> 6) >= p.tree_words) return false;
+    return (p.tree[row * p.tree_stride + (j >> 6)] >> (j & 63) & 1) != 0;
+  }
+  return row_sees(pos, last, p.window, p.sinks);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kMassThreads, 2)
+    kv_mass_kernel(const __grid_constant__ CUtensorMap tmK, const MassParams mp) {
+  using Sh = MassShape<D, NT>;
+  constexpr int S = Sh::kStages, Q = Sh::kSlots, R = Sh::kRows, kCols = Sh::kCols, A = kMassAcc;
+  const AttnParams& p = mp.a;
+  extern __shared__ __align__(1024) unsigned char mass_smem[];
+  const uint32_t base = smem_u32(mass_smem);
+  if (base & 1023u) {  // swizzled operands could not be read
+    pdl_wait();
+    if (threadIdx.x == 0) report_error(p.err, kErrSmemAlign);
+    return;
+  }
+  MassCtl<D, NT>& c = *reinterpret_cast<MassCtl<D, NT>*>(mass_smem);
+  const uint32_t ring = base + mass_ctl_bytes<D, NT>(), qbuf = ring + S * Sh::kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort_flag = &c.abort;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&c.kfull[i]), 1);
+      mbar_init(smem_u32(&c.empty[i]), 5);  // the last product, the weighing warps
+    }
+    for (int i = 0; i < A; ++i) {
+      mbar_init(smem_u32(&c.sfull[i]), 2);  // the product, and the thread that saw the page scales
+      mbar_init(smem_u32(&c.sempty[i]), 4);
+    }
+    for (int i = 0; i < Q; ++i) {
+      mbar_init(smem_u32(&c.qfull[i]), 2);
+      mbar_init(smem_u32(&c.qempty[i]), 5);
+    }
+    mbar_init(smem_u32(&c.drain), 1);
+    for (int i = 0; i < kAttnQueue; ++i) {
+      mbar_init(smem_u32(&c.segfull[i]), 1);
+      mbar_init(smem_u32(&c.segempty[i]), 7);  // the weighing and query warps, the MMA thread
+    }
+    c.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(&c.tmem), Sh::kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 32) prefetch_tmap(&tmK);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  // (only now: a dependent that allocates tensor memory must not come first)
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 4) {
+    attn_walk<D, NT, true>(c, p, tmK, tmK, ring);
+  } else if (warp == 5) {
+    // ------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(kAttnTile, kCols);
+      bool ok = true;
+      auto need = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
+          if (!*abort_flag) report_error(p.err, kErrWaitFull);
+          *abort_flag = 1;
+          ok = false;
+        }
+        return ok;
+      };
+      int sq = 0, i = 0, x = 0, q0 = 0;  // segments, tiles, products, slots of queries before the segment's
+      while (ok) {
+        const int qi = sq % kAttnQueue;
+        if (!need(&c.segfull[qi], (sq / kAttnQueue) & 1)) break;
+        const int kind = c.seg[qi].kind, n = c.seg[qi].tb - c.seg[qi].ta, chunks = (c.seg[qi].nrows + R - 1) / R;
+        mbar_arrive(smem_u32(&c.segempty[qi]));
+        if (kind & kSegStop) break;
+        ++sq;
+        for (int t = 0; t < n && ok; ++t, ++i) {
+          if (!need(&c.kfull[i % S], (i / S) & 1)) break;
+          for (int k = 0; k < chunks; ++k, ++x) {
+            const int q = (q0 + k) % Q;
+            if (t == 0 && !need(&c.qfull[q], ((q0 + k) / Q) & 1)) break;
+            if (!need(&c.sempty[x % A], ((x / A) & 1) ^ 1)) break;
+            tc_fence_after();
+            const uint64_t kd = smem_desc_rows<D>(ring + (uint32_t)(i % S) * Sh::kTileBytes);
+            const uint64_t qd = smem_desc_rows<D>(qbuf + (uint32_t)q * Sh::kSlotBytes);
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              mma_e4m3(tmem + (uint32_t)(x % A) * kCols, kd + (uint64_t)(kk * 2), qd + (uint64_t)(kk * 2), idesc, kk > 0);
+            mma_commit(smem_u32(&c.sfull[x % A]));
+            mbar_arrive(smem_u32(&c.sfull[x % A]));
+            if (k == chunks - 1) mma_commit(smem_u32(&c.empty[i % S]));
+            if (t == n - 1) mma_commit(smem_u32(&c.qempty[q]));
+          }
+        }
+        q0 += chunks;
+      }
+      mma_commit(smem_u32(&c.drain));
+      if (!mbar_wait(smem_u32(&c.drain), 0)) report_error(p.err, kErrDrain);
+    }
+  } else if (warp >= 6) {
+    // ----------------------------------------------------------- query operand
+    constexpr int kLanes = D / 8, kStep = 64 / kLanes, kPass = R / kStep;
+    const int qt = tid - 192, l = qt % kLanes;
+    int sq = 0, slot = 0;
+    uint32_t par = 0;
+    bool ok = true;
+    while (ok) {
+      const int qi = sq % kAttnQueue;
+      if (lane == 0) ok = mbar_wait_nap<kNap>(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      const AttnSeg g = c.seg[qi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
+      ++sq;
+      if (g.kind & kSegStop) break;
+      for (int k = 0; k * R < g.nrows && ok; ++k) {
+        struct Row {
+          uint4 v;
+          float lse;
+          int last, row;
+        };
+        // Row `pass` of this thread's: two are under way while one is converted.
+        auto load_row = [&](int pass) {
+          Row r{make_uint4(0u, 0u, 0u, 0u), -INFINITY, -1, 0};  // a row that is none sees nothing
+          const int q = k * R + pass * kStep + qt / kLanes;
+          if (q < g.nrows) {
+            const int at = g.r0 + q, tok = div_group(p, at), head = g.h * p.group + at - tok * p.group;
+            r.row = g.row0 + tok;
+            r.last = p.tree ? tree_row(p, g.row0, g.n, g.first, tok).last : row_last(g.first, tok);
+            r.v = *reinterpret_cast<const uint4*>(p.q.p + (long long)r.row * p.q.ts + (long long)head * p.q.hs + 8 * l);
+            r.lse = p.lse[(long long)r.row * p.q.heads + head];
+          }
+          return r;
+        };
+        Row r0 = load_row(0), r1 = r0;
+        if (kPass > 1) r1 = load_row(1);
+        if (lane == 0) ok = mbar_wait_nap<kNap>(smem_u32(&c.qempty[slot]), par ^ 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+#pragma unroll 1
+        for (int i = 0; i < kPass; ++i) {
+          const int q = i * kStep + qt / kLanes;
+          const Row r = r0;
+          r0 = r1;
+          if (i + 2 < kPass) r1 = load_row(i + 2);
+          const QuerySplit s = split_query<kLanes>(r.v, 1.f, 32.f);
+          const uint32_t qb = qbuf + (uint32_t)(slot * Sh::kSlotBytes) + (uint32_t)((l & 1) * 8);
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(s.hi.x), "r"(s.hi.y) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(R + q, l >> 1)), "r"(s.lo.x), "r"(s.lo.y) : "memory");
+          if (l == 0) {
+            c.qf[slot][q] = s.factor * p.scale_log2;
+            c.ql[slot][q] = r.lse == -INFINITY ? -INFINITY : -1.4426950408889634f * r.lse;
+            c.qpos[slot][q] = r.last;
+            c.qrow[slot][q] = r.row;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.qfull[slot]));
+        if (++slot == Q) {
+          slot = 0;
+          par ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- weights
+    // After a wait that ran out (abort) the waits fall through, so that the
+    // warps keep meeting at their barriers until the segments end.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!mbar_wait_or_abort(smem_u32(bar), parity, abort_flag)) {
+        if (!*abort_flag) report_error(p.err, kErrWaitMma);
+        *abort_flag = 1;
+      }
+      __syncwarp();
+    };
+    const uint32_t lanes = tmem + ((uint32_t)warp << 21);  // tensor-memory lanes of this warp
+    const int ps = p.cache.page_shift;
+    int sq = 0, i = 0, x = 0, q0 = 0;
+    while (true) {
+      const int qi = sq % kAttnQueue;
+      if (tid == 0) c.go[sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
+      __syncwarp();
+      named_bar_sync(1, 128);
+      if (!c.go[sq & 1]) {
+        if (tid == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
+        *abort_flag = 1;
+        break;
+      }
+      const AttnSeg g = c.seg[qi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.segempty[qi]));
+      ++sq;
+      if (g.kind & kSegStop) break;
+      const TileMap tm(g.tlo, p.sinks);
+      const int chunks = (g.nrows + R - 1) / R;
+      for (int t = g.ta; t < g.tb; ++t, ++i) {
+        const int slot = i % S, pos = tm.at(t) * kAttnTile + tid;
+        int flags = 0, page = -1;
+        float ks = 0.f;
+        bool live = false;
+        F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+        for (int k = 0; k < chunks; ++k, ++x) {
+          const int q = (q0 + k) % Q, a = x % A;
+          if (t == g.ta) wait(&c.qfull[q], ((q0 + k) / Q) & 1);
+          wait(&c.sfull[a], (x / A) & 1);
+          tc_fence_after();
+          if (k == 0) {
+            flags = c.flags[slot];
+            page = c.page[slot][tid >> ps];
+            ks = c.kscale[slot][tid >> ps];
+            live = page >= 0 && tid >= c.live[slot][0] && tid < c.live[slot][1];
+          }
+          uint32_t seen = live ? 0xffffffffu : 0u;
+          if (__builtin_expect(flags & 2, 0)) {
+            seen = 0u;
+#pragma unroll 1
+            for (int e = 0; live && e < R; ++e)
+              seen |= mass_sees(p, pos, g.first, c.qpos[q][e], c.qrow[q][e]) ? 1u << e : 0u;
+          }
+          const F2 third = f2(kLoScale, kLoScale), key = f2(ks, ks);
+#pragma unroll
+          for (int e0 = 0; e0 < R; e0 += 8) {
+            float hi[8], lo[8];
+            tmem_ld8x2(lanes + (uint32_t)(a * kCols + e0), lanes + (uint32_t)(a * kCols + R + e0), hi, lo);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float2 f = *reinterpret_cast<const float2*>(&c.qf[q][e0 + e]);
+              const float2 l = *reinterpret_cast<const float2*>(&c.ql[q][e0 + e]);
+              const F2 s = f2_fma(f2(lo[e], lo[e + 1]), third, f2(hi[e], hi[e + 1]));
+              float2 w = f2_parts(f2_fma(s, f2_mul(f2(f.x, f.y), key), f2(l.x, l.y)));
+              w.x = seen >> (e0 + e) & 1 ? ex2(w.x) : 0.f;
+              w.y = seen >> (e0 + e + 1) & 1 ? ex2(w.y) : 0.f;
+              sum[e >> 1 & 1] = f2_add(sum[e >> 1 & 1], f2(w.x, w.y));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c.sempty[a]));
+        }
+        const float2 s2 = f2_parts(f2_add(sum[0], sum[1]));
+        const float w = s2.x + s2.y;
+        if (!mp.part && g.r0 > 0) {  // more rows than the batch's max_new says
+          if (tid == 0) report_error(p.err, kErrIndex);
+        } else if (mp.part) {
+          mp.part[mass_part<NT>(mp, g.b, g.row0, g.r0 / NT, g.h) + pos] = w;
+        } else if (live) {
+          float* at = mp.mass + (long long)page * mp.page_stride + (long long)g.h * mp.head_stride + (pos & ((1 << ps) - 1));
+          if (pos >= g.first)
+            *at = w;
+          else
+            atomicAdd(at, w);  // (the only one to this address: no read to wait for)
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&c.empty[slot]));
+      }
+      for (int k = 0; k < chunks; ++k)
+        if (lane == 0) mbar_arrive(smem_u32(&c.qempty[(q0 + k) % Q]));
+      q0 += chunks;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Sh::kTmemCols);
+  }
+}
+
+// Adds the row tiles' sums of a position, in order: block (x, y, z) takes tile x
+// of sequence z and key/value head y, thread = position.
+template <int NT>
+__global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParams mp) {
+  const AttnParams& p = mp.a;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z, pos = t * kAttnTile + threadIdx.x;
+  const KvSeq s = kv_seq(p.batch, p.cache.page_shift, b, nullptr);
+  if (s.n == 0 || pos >= s.len) return;
+  const long long at = mass_part<NT>(mp, b, s.row0, 0, h) + pos, step = (long long)p.cache.heads * mp.tiles * kAttnTile;
+  float w = 0.f;
+  bool any = false;
+  for (int j = 0; j * NT < s.n * p.group; ++j) {
+    const AttnItem it = attn_item<NT, true>(p, s, j);
+    const TileMap tm(it.tlo, p.sinks);
+    if (t >= it.tb || (t < tm.tw && t >= tm.tw - tm.gap)) continue;  // a tile that its rows do not see
+    w += mp.part[at + j * step];
+    any = true;
+  }
+  const int page = any ? p.batch.table[(long long)b * p.batch.table_stride + (pos >> p.cache.page_shift)] : -1;
+  if (page < 0 || page >= p.cache.num_pages) return;  // (recorded by the kernel before)
+  float* to = mp.mass + (long long)page * mp.page_stride + (long long)h * mp.head_stride + (pos & ((1 << p.cache.page_shift) - 1));
+  *to = pos >= s.len - s.n ? w : *to + w;
+}
+
+}  // namespace sgr
