@@ -294,7 +294,7 @@ int sgr_kv_mass_workspace(const sgr_kv_cache* cache, const sgr_kv_batch* batch, 
  * chooses them), and mass.  Heads keep positions of their own, the same number
  * each.  The old pages are read only; a new page may be none of them, nor
  * occur twice (undefined contents otherwise).  Entries of the table beyond n
- * positions are not read; positions of a new page behind them are not written.
+ * positions do not matter; positions of a new page behind them are not written.
  * Keys stay rotated to the positions that they had: go on with
  * sgr_kv_append_at.  A bad old page's positions count as the smallest mass and
  * move as zeros; n beyond the new table's room is cut to it; both are recorded

@@ -697,14 +697,6 @@ int run_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, c
 }
 
 // ------------------------------------------------------------ eviction
-using MoveFn = void (*)(const sgr::EvictParams);
-
-template <int D>
-MoveFn move_fn(int page_size) {
-  const int pass = page_size / (sgr::kMoveThreads / (D / 16));
-  return pass >= 4 && D == 128 ? sgr::kv_move_kernel<D, D == 128 ? 4 : 2> : pass >= 2 ? sgr::kv_move_kernel<D, 2> : sgr::kv_move_kernel<D, 1>;
-}
-
 int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses* mass, const sgr_kv_eviction* ev,
               unsigned flags, void* stream) {
   int rc = validate_evict(c, b, mass, ev);
@@ -718,11 +710,16 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
   while (cluster < sgr::kSelectCluster &&
          (longest > (long long)cluster * sgr::kSelectCached || (items * cluster < dev->sms && longest > cluster * 2048LL)))
     cluster *= 2;
-  const long long moves = items * ev->max_pages;
-  if (items * cluster > 0x7fffffffLL || moves > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
+  // Warps of the move: 16-byte runs of a page's head, two (the smallest) or four
+  // a lane, eight warps a block.
+  const int runs = c->page_size * c->head_dim / 16, vec = runs / 32 < 4 ? 2 : 4, warps = runs / (32 * vec);
+  const int per_block = sgr::kMoveThreads / 32 / warps;
+  const long long moves = (items * ev->max_pages + per_block - 1) / per_block;
+  if (items * cluster > 0x7fffffffLL || moves > 0x7fffffffLL || items > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
   sgr::EvictParams p;
   p.cache = cache_of(*c);
   p.batch = batch_of(*b);
+  if (c->num_pages == 0) p.batch.max_pages = 0;  // (no position has a place)
   p.mass = mass->data;
   p.page_stride = mass->page_stride;
   p.head_stride = mass->head_stride;
@@ -734,11 +731,14 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
   p.recent = ev->recent;
   p.kept = ev->kept;
   p.new_len = ev->new_len;
+  const long long run = ((longest + cluster - 1) / cluster + 3) & ~3LL;  // of a CTA, at most
+  p.cached = (int)(run < sgr::kSelectCached ? run : sgr::kSelectCached);
+  p.wide = aligned(mass->data, 16) && mass->page_stride % 4 == 0 && mass->head_stride % 4 == 0;
   p.err = dev->err;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(items * cluster));
   lc.blockDim = dim3(sgr::kSelectThreads);
-  lc.dynamicSmemBytes = sizeof(sgr::SelectCtl);
+  lc.dynamicSmemBytes = sizeof(sgr::SelectCtl) + 4 * (size_t)p.cached;
   lc.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -753,8 +753,10 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
     return SGR_ERR_LAUNCH;
   }
   if (moves == 0) return SGR_OK;
-  return launch(c->head_dim == 64 ? move_fn<64>(c->page_size) : move_fn<128>(c->page_size), dim3((unsigned)moves),
-                sgr::kMoveThreads, 0, flags, stream, p);
+  void (*move)(const sgr::EvictParams) = c->head_dim == 128 ? sgr::kv_move_kernel<128, 4>
+                                         : vec == 2         ? sgr::kv_move_kernel<64, 2>
+                                                            : sgr::kv_move_kernel<64, 4>;
+  return launch(move, dim3((unsigned)moves), sgr::kMoveThreads, 0, flags, stream, p);
 }
 
 }  // namespace
