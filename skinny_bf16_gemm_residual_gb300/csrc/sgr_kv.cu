@@ -690,8 +690,9 @@ int run_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, c
   p.head_stride = mass->head_stride;
   p.part = m.part ? static_cast<float*>(workspace) : nullptr;
   p.tiles = m.tiles;
+  p.max_new = b->max_new;
   const sgr::MassKernel k = sgr::mass_kernel(c->head_dim, m.nt);
-  rc = launch(k.fn, dim3(m.grid), sgr::kMassThreads, k.smem, flags, stream, tk, p);
+  rc = launch(k.fn, dim3(m.grid), k.threads, k.smem, flags, stream, tk, p);
   if (rc != SGR_OK || !m.part) return rc;
   return launch(sgr::mass_join_kernel(), dim3(m.tiles, c->heads, b->batch), sgr::kAttnTile, 0, flags, stream, p);
 }

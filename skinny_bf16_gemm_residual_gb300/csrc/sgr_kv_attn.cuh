@@ -214,15 +214,36 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   int b = 0, h = 0, j = 0, skip = 0, u = 0, u1 = 0, per = 0, rest = 0;
   KvSeq s{0, 0, 0};
   {
-    // Each lane counts its (consecutive) sequences.
+    // Each lane counts its (consecutive) sequences; or, where few sequences have
+    // many row tiles, the lanes count a sequence's together, one sequence after
+    // another (two chunks of 16 row tiles a head: 3 us less to the first tile).
     const int per_lane = (p.batch.batch + 31) / 32, b_first = lane * per_lane;
     const int b_last = min(b_first + per_lane, p.batch.batch);
     int mine = 0, units = 0;
+    int tiles = 0;  // row tiles of a sequence, the most of any
+    constexpr bool kSeveral = NT >= 32;  // (rows that fit a smaller tile are in one)
+    if (kSeveral && p.reuse && per_lane == 1) {
+      if (b_first < b_last) s = kv_seq(p.batch, ps, b_first, p.err);
+      tiles = __reduce_max_sync(0xffffffffu, (s.n * p.group + NT - 1) / NT);
+    }
+    if (kSeveral && tiles > 2 * p.batch.batch * ((tiles + 31) / 32)) {
+      for (int x = 0; x < p.batch.batch; ++x) {
+        const KvSeq sx{__shfl_sync(0xffffffffu, s.row0, x), __shfl_sync(0xffffffffu, s.n, x), __shfl_sync(0xffffffffu, s.len, x)};
+        int part = 0;
+        for (int k = lane; k * NT < sx.n * p.group; k += 32) part += attn_item<NT, kMasked>(p, sx, k).units;
+        part = __reduce_add_sync(0xffffffffu, part);
+        if (lane == x) {
+          units = part;
+          mine = units * hk;
+        }
+      }
+    } else {
 #pragma unroll 4
-    for (int x = b_first; x < b_last; ++x) {
-      s = kv_seq(p.batch, ps, x, p.err);
-      units = attn_seq_units<NT, kMasked>(p, s);
-      mine += units * hk;
+      for (int x = b_first; x < b_last; ++x) {
+        s = kv_seq(p.batch, ps, x, p.err);
+        units = attn_seq_units<NT, kMasked>(p, s);
+        mine += units * hk;
+      }
     }
     int upto = mine;
 #pragma unroll
@@ -262,7 +283,29 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       if (!found) u1 = u, off = 0, units = 1;
       h = off / units;
       off -= h * units;
-      for (int x; found && off >= (x = attn_item<NT, kMasked>(p, s, j).units); ++j) off -= x;
+      // The row tile: the lanes look at 32 of them at once.
+      if (kSeveral && p.reuse) {
+        while (found && j * NT < s.n * p.group) {
+          const int each = (j + lane) * NT < s.n * p.group ? attn_item<NT, kMasked>(p, s, j + lane).units : 0;
+          int upto_j = each;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, upto_j, o);
+            if (lane >= o) upto_j += up;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, upto_j > off);
+          if (past) {
+            const int at = __ffs(past) - 1;
+            off -= __shfl_sync(0xffffffffu, upto_j - each, at);
+            j += at;
+            break;
+          }
+          off -= __shfl_sync(0xffffffffu, upto_j, 31);
+          j += 32;
+        }
+      } else {
+        for (int x; found && off >= (x = attn_item<NT, kMasked>(p, s, j).units); ++j) off -= x;
+      }
       skip = off;
     }
   }

@@ -45,7 +45,7 @@ using MassJoinFn = void (*)(const MassParams);
 
 struct MassKernel {
   MassFn fn;
-  int smem;
+  int smem, threads;
 };
 
 MassKernel mass_kernel(int dim, int nt);  // nt: 8, 16, 32 or kMassRows

@@ -7,7 +7,7 @@ namespace {
 
 template <int D, int NT>
 MassKernel kernel_of() {
-  return {kv_mass_kernel<D, NT>, mass_smem_bytes<D, NT>()};
+  return {kv_mass_kernel<D, NT>, mass_smem_bytes<D, NT>(), MassShape<D, NT>::kThreads};
 }
 
 template <int D>

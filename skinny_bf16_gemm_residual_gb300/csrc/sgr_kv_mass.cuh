@@ -16,19 +16,23 @@
 // and an absolute 2^-22 of it below).  Thread = key: it reads its lane of the
 // accumulator, adds the parts in FP32, and sums 2^(s - L) over the columns.
 //
-// Rows that share a key/value head go in products of up to 32.  Up to 256 of
+// Rows that share a key/value head go in products of up to 64.  Up to 128 of
 // them, their queries all in shared memory, meet a tile of keys while it is
 // there (it is read once); more are several row tiles, whose sums go to the
 // workspace and are added in order by a second kernel: no atomics on one
 // address from two places, the same bits on every run.  Every CTA takes the
 // same number of (row tile, key tile) units (attn_walk).
 //
-// Roles: warps 0-3 weigh (thread = key), warp 4 walks the work and loads
-// pages, warp 5 issues the MMAs, warps 6-7 bring queries into the operand, a
-// ring of products' worth of rows.
+// Roles: four warps weigh (thread = key; eight for products of 32 rows or more,
+// half of the columns each), one walks the work and loads pages, one issues the
+// MMAs, two (four for 128 rows) bring queries into the operand, a ring of products' worth of
+// rows.
 #pragma once
 
+#include <type_traits>
+
 #include "sgr_kv_attn_few.cuh"
+#include "sgr_kv_attn_rows.cuh"
 
 namespace sgr {
 
@@ -38,21 +42,25 @@ struct MassParams {
   long long page_stride, head_stride;  // elements
   float* part;  // [row tile][key/value head][128 tiles positions], NULL: one row tile a sequence
   int tiles;    // of a sequence, at most
+  int max_new;  // rows of a sequence, at most
 };
 
-constexpr int kMassThreads = 256, kMassAcc = 4;
-constexpr int kMassRows = 256;  // of the largest row tile
+constexpr int kMassRows = 128;  // of the largest row tile
 
 template <int D, int NT>
 struct MassShape {
-  static constexpr int kRows = NT < 32 ? NT : 32;  // of a product
+  static constexpr int kRows = NT < 64 ? NT : 64;  // of a product
   static constexpr int kCols = 2 * kRows;
+  static constexpr int kAcc = kRows == 64 ? 2 : 4;  // accumulators
+  static constexpr int kGroups = kRows >= 32 ? 2 : 1;  // of 4 weighing warps, each a part of a product's columns
+  static constexpr int kWeigh = 4 * kGroups, kQuery = NT > 32 ? 4 : 2;  // warps
+  static constexpr int kThreads = 32 * (kWeigh + 2 + kQuery);
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kSlotBytes = kCols * D;
   // As many stages of keys and slots of queries as two CTAs an SM allow.
-  static constexpr int kStages = D == 128 ? (NT <= 16 ? 6 : NT == 32 ? 5 : 2) : (NT <= 16 ? 10 : NT == 32 ? 8 : 4);
-  static constexpr int kSlots = NT == 256 ? 8 : NT == 32 ? 3 : 4;
-  static constexpr int kTmemCols = kMassAcc * kCols;
+  static constexpr int kStages = D == 128 ? (NT <= 16 ? 6 : NT == 32 ? 5 : 2) : (NT <= 16 ? 10 : NT == 32 ? 8 : 5);
+  static constexpr int kSlots = NT == 16 || NT == 32 ? 3 : 4;
+  static constexpr int kTmemCols = kAcc * kCols;
 };
 
 template <int D, int NT>
@@ -61,7 +69,7 @@ struct MassCtl {
   static constexpr bool kStopStage = false, kValues = false;
   static constexpr int kStages = Sh::kStages, kMeta = kStages, S = kStages, Q = Sh::kSlots;
   uint64_t kfull[S], empty[S];
-  uint64_t sfull[kMassAcc], sempty[kMassAcc], qfull[Q], qempty[Q], drain;
+  uint64_t sfull[Sh::kAcc], sempty[Sh::kAcc], qfull[Q], qempty[Q], drain;
   uint64_t segfull[kAttnQueue], segempty[kAttnQueue];
   uint32_t tmem;
   int abort;
@@ -70,6 +78,7 @@ struct MassCtl {
   float kscale[S][8];  // of a stage's pages
   int page[S][8];      // (-1: not there)
   int flags[S], live[S][2];
+  float sum[Sh::kGroups][kAttnTile];  // of the groups but the first
   alignas(16) float qf[Q][Sh::kRows];  // a row's score factor
   alignas(16) float ql[Q][Sh::kRows];  // and -L (-inf: a row that counts for nothing)
   int qpos[Q][Sh::kRows];              // the last position that it sees, by itself
@@ -125,6 +134,35 @@ __device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
   return r;
 }
 
+// hi and lo parts of C accumulator columns, the lo ones `apart` columns on.
+template <int C>
+__device__ __forceinline__ void tmem_ld_parts(uint32_t hi_at, uint32_t apart, float (&hi)[C], float (&lo)[C]) {
+  static_assert(C == 8 || C == 16, "one load of each part");
+  if constexpr (C == 8) {
+    tmem_ld8x2(hi_at, hi_at + apart, hi, lo);
+  } else {
+    uint32_t r[32];
+#define SGR_LD16(AT, O)                                                                                               \
+  asm volatile(                                                                                                       \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "                                                                       \
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"                                \
+      : "=r"(r[O]), "=r"(r[O + 1]), "=r"(r[O + 2]), "=r"(r[O + 3]), "=r"(r[O + 4]), "=r"(r[O + 5]), "=r"(r[O + 6]),   \
+        "=r"(r[O + 7]), "=r"(r[O + 8]), "=r"(r[O + 9]), "=r"(r[O + 10]), "=r"(r[O + 11]), "=r"(r[O + 12]),            \
+        "=r"(r[O + 13]), "=r"(r[O + 14]), "=r"(r[O + 15])                                                             \
+      : "r"(AT)                                                                                                       \
+      : "memory")
+    SGR_LD16(hi_at, 0);
+    SGR_LD16(hi_at + apart, 16);
+#undef SGR_LD16
+    tmem_wait_ld32(r);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      hi[e] = __uint_as_float(r[e]);
+      lo[e] = __uint_as_float(r[16 + e]);
+    }
+  }
+}
+
 // Whether a row sees a position (`last`, `row`: MassCtl's).
 __device__ __forceinline__ bool mass_sees(const AttnParams& p, int pos, int first, int last, int row) {
   const int j = pos - first;
@@ -136,10 +174,10 @@ __device__ __forceinline__ bool mass_sees(const AttnParams& p, int pos, int firs
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kMassThreads, 2)
+__global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
     kv_mass_kernel(const __grid_constant__ CUtensorMap tmK, const MassParams mp) {
   using Sh = MassShape<D, NT>;
-  constexpr int S = Sh::kStages, Q = Sh::kSlots, R = Sh::kRows, kCols = Sh::kCols, A = kMassAcc;
+  constexpr int S = Sh::kStages, Q = Sh::kSlots, R = Sh::kRows, kCols = Sh::kCols, A = Sh::kAcc, kWeigh = Sh::kWeigh, kQuery = Sh::kQuery;
   const AttnParams& p = mp.a;
   extern __shared__ __align__(1024) unsigned char mass_smem[];
   const uint32_t base = smem_u32(mass_smem);
@@ -156,25 +194,25 @@ __global__ void __launch_bounds__(kMassThreads, 2)
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(smem_u32(&c.kfull[i]), 1);
-      mbar_init(smem_u32(&c.empty[i]), 5);  // the last product, the weighing warps
+      mbar_init(smem_u32(&c.empty[i]), 1 + kWeigh);  // the last product, the weighing warps
     }
     for (int i = 0; i < A; ++i) {
       mbar_init(smem_u32(&c.sfull[i]), 2);  // the product, and the thread that saw the page scales
-      mbar_init(smem_u32(&c.sempty[i]), 4);
+      mbar_init(smem_u32(&c.sempty[i]), kWeigh);
     }
     for (int i = 0; i < Q; ++i) {
-      mbar_init(smem_u32(&c.qfull[i]), 2);
-      mbar_init(smem_u32(&c.qempty[i]), 5);
+      mbar_init(smem_u32(&c.qfull[i]), kQuery);
+      mbar_init(smem_u32(&c.qempty[i]), 1 + kWeigh);
     }
     mbar_init(smem_u32(&c.drain), 1);
     for (int i = 0; i < kAttnQueue; ++i) {
       mbar_init(smem_u32(&c.segfull[i]), 1);
-      mbar_init(smem_u32(&c.segempty[i]), 7);  // the weighing and query warps, the MMA thread
+      mbar_init(smem_u32(&c.segempty[i]), kWeigh + kQuery + 1);  // the weighing and query warps, the MMA thread
     }
     c.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == kWeigh + 1) {
     tmem_alloc(smem_u32(&c.tmem), Sh::kTmemCols);
     tmem_relinquish();
   }
@@ -187,9 +225,9 @@ __global__ void __launch_bounds__(kMassThreads, 2)
   pdl_launch_dependents();
   pdl_wait();
 
-  if (warp == 4) {
+  if (warp == kWeigh) {
     attn_walk<D, NT, true>(c, p, tmK, tmK, ring);
-  } else if (warp == 5) {
+  } else if (warp == kWeigh + 1) {
     // ------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(kAttnTile, kCols);
@@ -233,10 +271,10 @@ __global__ void __launch_bounds__(kMassThreads, 2)
       mma_commit(smem_u32(&c.drain));
       if (!mbar_wait(smem_u32(&c.drain), 0)) report_error(p.err, kErrDrain);
     }
-  } else if (warp >= 6) {
+  } else if (warp >= kWeigh + 2) {
     // ----------------------------------------------------------- query operand
-    constexpr int kLanes = D / 8, kStep = 64 / kLanes, kPass = R / kStep;
-    const int qt = tid - 192, l = qt % kLanes;
+    constexpr int kLanes = D / 8, kStep = 32 * kQuery / kLanes, kPass = R / kStep;
+    const int qt = tid - 32 * (kWeigh + 2), l = qt % kLanes;
     int sq = 0, slot = 0;
     uint32_t par = 0;
     bool ok = true;
@@ -310,14 +348,17 @@ __global__ void __launch_bounds__(kMassThreads, 2)
       }
       __syncwarp();
     };
-    const uint32_t lanes = tmem + ((uint32_t)warp << 21);  // tensor-memory lanes of this warp
+    // Group g of four warps takes columns C g .. C g + C - 1 of every product.
+    constexpr int C = R / Sh::kGroups;
+    const int group = warp >> 2, tok = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21) + (uint32_t)(group * C);  // tensor-memory lanes of this warp
     const int ps = p.cache.page_shift;
     int sq = 0, i = 0, x = 0, q0 = 0;
     while (true) {
       const int qi = sq % kAttnQueue;
       if (tid == 0) c.go[sq & 1] = mbar_wait_or_abort(smem_u32(&c.segfull[qi]), (sq / kAttnQueue) & 1, abort_flag) ? 1 : 0;
       __syncwarp();
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 32 * kWeigh);
       if (!c.go[sq & 1]) {
         if (tid == 0 && !*abort_flag) report_error(p.err, kErrWaitFull);
         *abort_flag = 1;
@@ -330,10 +371,12 @@ __global__ void __launch_bounds__(kMassThreads, 2)
       if (g.kind & kSegStop) break;
       const TileMap tm(g.tlo, p.sinks);
       const int chunks = (g.nrows + R - 1) / R;
+      if (g.n > mp.max_new && tid == 0) report_error(p.err, kErrIndex);
+      const bool stray = !mp.part && g.r0 > 0;  // (rows that there is no room for)
       for (int t = g.ta; t < g.tb; ++t, ++i) {
-        const int slot = i % S, pos = tm.at(t) * kAttnTile + tid;
+        const int slot = i % S, pos = tm.at(t) * kAttnTile + tok;
         int flags = 0, page = -1;
-        float ks = 0.f;
+        F2 key = f2(0.f, 0.f);
         bool live = false;
         F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
         for (int k = 0; k < chunks; ++k, ++x) {
@@ -343,41 +386,61 @@ __global__ void __launch_bounds__(kMassThreads, 2)
           tc_fence_after();
           if (k == 0) {
             flags = c.flags[slot];
-            page = c.page[slot][tid >> ps];
-            ks = c.kscale[slot][tid >> ps];
-            live = page >= 0 && tid >= c.live[slot][0] && tid < c.live[slot][1];
+            page = c.page[slot][tok >> ps];
+            key = f2(c.kscale[slot][tok >> ps], c.kscale[slot][tok >> ps]);
+            live = page >= 0 && tok >= c.live[slot][0] && tok < c.live[slot][1];
           }
-          uint32_t seen = live ? 0xffffffffu : 0u;
-          if (__builtin_expect(flags & 2, 0)) {
-            seen = 0u;
+          const F2 third = f2(kLoScale, kLoScale);
+          // P columns at a time, from c0 on.
+          constexpr int P = C < 16 ? C : 16;
+          float hi[P], lo[P];
+          auto weigh = [&](auto masked, int c0, uint32_t seen) {
+            constexpr bool kHide = decltype(masked)::value;
+#pragma unroll
+            for (int e = 0; e < P; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&c.qf[q][c0 + e]);
+              const float4 l = *reinterpret_cast<const float4*>(&c.ql[q][c0 + e]);
+              const F2 s0 = f2_fma(f2(lo[e], lo[e + 1]), third, f2(hi[e], hi[e + 1]));
+              const F2 s1 = f2_fma(f2(lo[e + 2], lo[e + 3]), third, f2(hi[e + 2], hi[e + 3]));
+              const float2 w0 = f2_parts(f2_fma(s0, f2_mul(f2(f.x, f.y), key), f2(l.x, l.y)));
+              const float2 w1 = f2_parts(f2_fma(s1, f2_mul(f2(f.z, f.w), key), f2(l.z, l.w)));
+              float w[4] = {w0.x, w0.y, w1.x, w1.y};
+#pragma unroll
+              for (int m = 0; m < 4; ++m) w[m] = ex2(!kHide || (seen >> (e + m) & 1) ? w[m] : -INFINITY);
+              sum[0] = f2_add(sum[0], f2(w[0], w[1]));
+              sum[1] = f2_add(sum[1], f2(w[2], w[3]));
+            }
+          };
+#pragma unroll
+          for (int h = 0; h < C / P; ++h) {
+            const int c0 = group * C + h * P;
+            tmem_ld_parts<P>(lanes + (uint32_t)(a * kCols + h * P), R, hi, lo);
+            if (h == C / P - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&c.sempty[a]));
+            }
+            if (__builtin_expect(flags & 2, 0)) {
+              uint32_t seen = 0u;
 #pragma unroll 1
-            for (int e = 0; live && e < R; ++e)
-              seen |= mass_sees(p, pos, g.first, c.qpos[q][e], c.qrow[q][e]) ? 1u << e : 0u;
-          }
-          const F2 third = f2(kLoScale, kLoScale), key = f2(ks, ks);
-#pragma unroll
-          for (int e0 = 0; e0 < R; e0 += 8) {
-            float hi[8], lo[8];
-            tmem_ld8x2(lanes + (uint32_t)(a * kCols + e0), lanes + (uint32_t)(a * kCols + R + e0), hi, lo);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 f = *reinterpret_cast<const float2*>(&c.qf[q][e0 + e]);
-              const float2 l = *reinterpret_cast<const float2*>(&c.ql[q][e0 + e]);
-              const F2 s = f2_fma(f2(lo[e], lo[e + 1]), third, f2(hi[e], hi[e + 1]));
-              float2 w = f2_parts(f2_fma(s, f2_mul(f2(f.x, f.y), key), f2(l.x, l.y)));
-              w.x = seen >> (e0 + e) & 1 ? ex2(w.x) : 0.f;
-              w.y = seen >> (e0 + e + 1) & 1 ? ex2(w.y) : 0.f;
-              sum[e >> 1 & 1] = f2_add(sum[e >> 1 & 1], f2(w.x, w.y));
+              for (int e = 0; live && e < P; ++e)
+                seen |= mass_sees(p, pos, g.first, c.qpos[q][c0 + e], c.qrow[q][c0 + e]) ? 1u << e : 0u;
+              weigh(std::true_type(), c0, seen);
+            } else {
+              weigh(std::false_type(), c0, 0u);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&c.sempty[a]));
         }
         const float2 s2 = f2_parts(f2_add(sum[0], sum[1]));
-        const float w = s2.x + s2.y;
-        if (!mp.part && g.r0 > 0) {  // more rows than the batch's max_new says
-          if (tid == 0) report_error(p.err, kErrIndex);
+        float w = s2.x + s2.y;
+        if constexpr (Sh::kGroups > 1) {
+          if (group > 0) c.sum[group][tok] = w;
+          __syncwarp();
+          named_bar_sync(2, 32 * kWeigh);
+          if (group == 0) w += c.sum[1][tok];
+        }
+        if (!live) w = 0.f;
+        if (group > 0 || stray) {
         } else if (mp.part) {
           mp.part[mass_part<NT>(mp, g.b, g.row0, g.r0 / NT, g.h) + pos] = w;
         } else if (live) {
@@ -397,7 +460,7 @@ __global__ void __launch_bounds__(kMassThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kWeigh + 1) {
     tc_fence_after();
     tmem_dealloc(tmem, Sh::kTmemCols);
   }
