@@ -513,7 +513,7 @@ Join join_kernel(int nt) {
     case 16: return {sgr::kv_attn_join_kernel<D, 16>, sgr::JoinShape<16>::kRows};
     case 24: return {sgr::kv_attn_join_kernel<D, 24>, sgr::JoinShape<24>::kRows};
     case 32: return {sgr::kv_attn_join_kernel<D, 32>, sgr::JoinShape<32>::kRows};
-    default: return {sgr::kv_attn_join_kernel<D, sgr::kRowsNT>, sgr::JoinShape<sgr::kRowsNT>::kRows};
+    default: return {sgr::kv_attn_rows_join_kernel<D>, 32 * (sgr::kRowsJoinThreads / 32 / (D / 16))};
   }
 }
 

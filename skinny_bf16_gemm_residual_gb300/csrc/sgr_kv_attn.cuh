@@ -67,7 +67,7 @@ struct AttnParams {
   int tree_words;
   float* lse;  // [rows][query heads], or NULL
   unsigned* err;
-  float* part_o;      // [2 grid][NT][D]
+  float* part_o;      // [2 grid][NT][D]; row tiles of 256: [2 grid][D / 4][NT][4]
   float2* part_ml;    // [2 grid][NT]  maximum, sum
   AttnPiece* pieces;  // [grid]
 };
@@ -342,11 +342,49 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
   struct Tile {
     int h, flags;
     int live0, live1;  // its tokens that some row sees
-    int page;  // this lane's table entry, -1 = none
+    int page;          // this lane's table entry, -1 = none
+    int src;           // the lane that has its scales (kBatch)
     float ks, vs;
   };
+  // For row tiles of many rows pages and scales come for all the tiles at once
+  // that 32 lanes have pages of (lane = one page), and those of the next batch
+  // while this one is used.  For few rows they come a tile ahead, across the ends
+  // of sequences, of which there is one every few tiles there (32 sequences of up
+  // to 4096: 19.8 us so, 20.8 in batches).
+  constexpr bool kBatch = NT >= 128;
+  struct Pages {
+    int page;
+    float ks, vs;
+  };
+  const int per_tile = kAttnTile >> ps, batch = 32 / per_tile;  // pages a tile, tiles a batch
+  Pages here{}, ahead{};
+  int first_tile = 0;
+  bool fresh = true;  // whether no batch of the segment has been asked for
   AttnItem cur{};
   int cur_h = 0, cur_b = 0, cur_p0 = 0, cur_p1 = 0;
+  // This lane's page of the batch from tile t0 on, -1 where there is none.
+  auto ask_pages = [&](int t0, Pages& g) {
+    const bool there = t0 + lane / per_tile < t_end;
+    const int tile = there ? t0 + lane / per_tile : t_end - 1;
+    const int x0 = (kMasked ? TileMap(cur.tlo, p.sinks).at(tile) : tile) * kAttnTile;
+    const int block = (x0 >> ps) + lane % per_tile, at = block << ps;
+    if (there && at < cur.thi && (at + (1 << ps) > cur.tlo || (kMasked && at < p.sinks)))
+      g.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
+    else
+      g.page = -2;  // (not asked for)
+  };
+  auto ask_scales = [&](Pages& g) {
+    if (g.page != -2 && (g.page < 0 || g.page >= p.cache.num_pages)) {
+      report_error(p.err, kErrIndex);
+      g.page = -1;
+    }
+    g.ks = g.vs = 1.f;
+    if (g.page >= 0) {
+      const long long at = (long long)g.page * p.cache.scale_stride + cur_h;
+      g.ks = p.cache.k_scale[at];
+      if (kValues) g.vs = p.cache.v_scale[at];
+    }
+  };
   // The next tile of this CTA's share; hands out the segments it enters.
   auto next_tile = [&](Tile& x) -> bool {
     while (t == t_end) {
@@ -396,6 +434,7 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       if (kValues && g.kind == kSegStart) piece = {cta_of(u + units - skip - take - 1), h, s.row0, it.r0, it.nrows, {0, 0, 0}};
       t = g.ta;
       t_end = g.tb;
+      fresh = true;
       cur = it;
       cur_h = h;
       cur_b = b;
@@ -423,18 +462,36 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
         x.flags |= 2;
       }
     }
-    // This lane's page of the tile, where some row sees a position of it.
-    const int block = (x0 >> ps) + lane, at = block << ps;
-    x.page = -1;
-    if (lane < (kAttnTile >> ps) && at < cur.thi && (at + (1 << ps) > cur.tlo || (kMasked && at < p.sinks))) {
-      x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
-      x.flags |= 4;
+    // Its pages, where some row sees a position of them.
+    if constexpr (!kBatch) {
+      const int block = (x0 >> ps) + lane, at = block << ps;
+      x.page = -2;
+      if (lane < per_tile && at < cur.thi && (at + (1 << ps) > cur.tlo || (kMasked && at < p.sinks)))
+        x.page = p.batch.table[(long long)cur_b * p.batch.table_stride + block];
+      return true;
     }
+    int k = t - 1 - first_tile;
+    if (fresh) {
+      first_tile = t - 1;
+      k = 0;
+      ask_pages(first_tile, here);
+      ask_scales(here);
+      fresh = false;
+    } else if (k == batch) {
+      here = ahead;
+      first_tile += batch;
+      k = 0;
+    }
+    if (k == 0) ask_pages(first_tile + batch, ahead);
+    if (k == 2) ask_scales(ahead);
+    x.src = (k * per_tile + lane) & 31;
+    x.page = __shfl_sync(0xffffffffu, here.page, x.src);
+    if (lane >= per_tile) x.page = -1;
     return true;
   };
-  // Checks the entry and asks for the page's scales.
+  // Checks this lane's page and asks for its scales (few rows).
   auto load_scales = [&](Tile& x) {
-    if ((x.flags & 4) && (x.page < 0 || x.page >= p.cache.num_pages)) {
+    if (x.page != -2 && (x.page < 0 || x.page >= p.cache.num_pages)) {
       report_error(p.err, kErrIndex);
       x.page = -1;
     }
@@ -445,14 +502,13 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       if (kValues) x.vs = p.cache.v_scale[at];
     }
   };
-  // One tile ahead of the copies: its table entries are asked for before
-  // this tile's scales arrive, which reach the stage behind its copies.
+  // One tile ahead of the copies: its table entries are asked for before this
+  // tile's scales arrive, which reach the stage behind its copies.
   Tile a{}, next{};
   bool has = next_tile(a);
-  if (has) load_scales(a);
+  if (!kBatch && has) load_scales(a);
   int i = 0, slot = 0;
   uint32_t par = 0;
-  const int per_tile = kAttnTile >> ps;
   const uint32_t page_bytes = (uint32_t)D << ps;
   while (has && ok) {
     if (i >= S) wait(&c.empty[slot], par ^ 1u);
@@ -469,8 +525,13 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       tma_load_4d(dst + kStage - kTile, &tmK, 0, 0, a.h, a.page, kb, policy);
       if constexpr (kValues) tma_load_4d(dst, &tmV, 0, 0, a.h, a.page, smem_u32(&c.vfull[slot]), policy);
     }
-    has = next_tile(next);
     const int meta = i % M;
+    if constexpr (kBatch) {
+      a.ks = __shfl_sync(0xffffffffu, here.ks, a.src);
+      a.vs = __shfl_sync(0xffffffffu, here.vs, a.src);
+    } else {
+      has = next_tile(next);
+    }
     if (lane < per_tile) {
       c.kscale[meta][lane] = a.ks;
       // (an exponent of -inf marks a page that is not there)
@@ -491,8 +552,12 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
       slot = 0;
       par ^= 1u;
     }
-    a = next;
-    if (has) load_scales(a);
+    if constexpr (kBatch) {
+      has = next_tile(a);
+    } else {
+      a = next;
+      if (has) load_scales(a);
+    }
   }
   bool stopped = false;
   if constexpr (Ctl::kStopStage) if (ok) {  // a stage that ends the sequence
@@ -535,6 +600,42 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// Pairs of FP32 values, one instruction for both.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_parts(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Eight elements (of a BF16 row held by kLanes neighbouring lanes) as hi and lo
 // codes, b = hi + lo / lo_scale, b = x * sign / factor with the row's largest
 // |b| in [128, 256).  A row with an infinity or NaN gets a NaN factor.
@@ -542,6 +643,23 @@ struct QuerySplit {
   uint2 hi, lo;
   float factor;
 };
+
+// Two values as hi and lo codes, a pair of bytes each.
+__device__ __forceinline__ void split_pair(float a, float b, float lo_scale, uint32_t& hi, uint32_t& lo) {
+  asm("{\n\t.reg .b16 h, l, z;\n\t.reg .b32 x, y, f;\n\t"
+      "cvt.rn.f16x2.f32 x, %3, %2;\n\t"
+      "cvt.rn.f16x2.f32 f, %4, %4;\n\t"
+      "mov.b16 z, 0;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 h, x;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, h;\n\t"
+      "sub.rn.f16x2 x, x, y;\n\t"
+      "mul.rn.f16x2 x, x, f;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l, x;\n\t"
+      "mov.b32 %0, {h, z};\n\t"
+      "mov.b32 %1, {l, z};\n\t}"
+      : "=r"(hi), "=r"(lo)
+      : "f"(a), "f"(b), "f"(lo_scale));
+}
 
 template <int kLanes>
 __device__ __forceinline__ QuerySplit split_query(const uint4& v, float sign, float lo_scale) {
@@ -555,17 +673,16 @@ __device__ __forceinline__ QuerySplit split_query(const uint4& v, float sign, fl
   int k = ex == 0 ? 126 : 134 - ex;
   k = min(max(k, -120), 126);
   const float sc = kv_exp2i(k) * sign;
-  float x[8], h[8];
+  float x[8];
   unpack8(v, x);
+  // In FP16 on the way: its 11 bits hold b (8 bits) down to 2^-17, far below what
+  // E4M3 rounds to zero, and the rest times lo_scale exactly.
+  uint32_t part[2][4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= sc;
+  for (int e = 0; e < 4; ++e) split_pair(x[2 * e] * sc, x[2 * e + 1] * sc, lo_scale, part[0][e], part[1][e]);
   QuerySplit s;
-  s.hi = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
-  from_e4m3x4(s.hi.x, h[0], h[1], h[2], h[3]);
-  from_e4m3x4(s.hi.y, h[4], h[5], h[6], h[7]);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = (x[e] - h[e]) * lo_scale;  // exact
-  s.lo = make_uint2(to_e4m3x4(x[0], x[1], x[2], x[3]), to_e4m3x4(x[4], x[5], x[6], x[7]));
+  s.hi = make_uint2(part[0][0] | part[0][1] << 16, part[0][2] | part[0][3] << 16);
+  s.lo = make_uint2(part[1][0] | part[1][1] << 16, part[1][2] | part[1][3] << 16);
   s.factor = ex == 255 ? __int_as_float(0x7fffffff) : kv_exp2i(-k);
   return s;
 }
@@ -620,9 +737,7 @@ template <int NT>
 struct JoinShape {
   static constexpr int kParts = NT <= 16 ? 4 : 1;  // warps a row
   static constexpr int kRows = kJoinThreads / 32 / kParts;
-  // Pieces read at once: many rows fill the GPU and have two or three pieces
-  // each (a chunk of a prompt: 120.3 us with runs of 8, 118.0 with 2).
-  static constexpr int kRun = NT <= 32 ? 8 : 2;
+  static constexpr int kRun = 8;  // pieces read at once
 };
 
 template <int D, int NT>

@@ -47,7 +47,8 @@ constexpr int kRowsNT = 256, kRowsThreads = 704;
 
 template <int D>
 struct RowsCtl {
-  static constexpr int kStages = 2, kMeta = 4, S = kStages, M = kMeta;
+  // (the softmax warps may be two tiles behind the copies)
+  static constexpr int kStages = D == 128 ? 2 : 4, kMeta = kStages + 2, S = kStages, M = kMeta;
   static constexpr bool kStopStage = true, kValues = true;
   uint64_t kfull[S], vfull[S], empty[S];
   uint64_t sfull[2], pfull[2], pvdone[2], wfull[2], wempty[2], qfull[2], drain;
@@ -56,7 +57,6 @@ struct RowsCtl {
   int abort;
   int go[2][2];
   AttnSeg seg[kAttnQueue];
-  // of a tile (the softmax warps may be two tiles behind the copies)
   float kscale[M][8], vexp[M][8];
   int flags[M], live[M][2];
   float qf[kRowsNT];
@@ -121,6 +121,51 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// Joins the partial sums of row tiles of 256 rows, as kv_attn_join_kernel: thread
+// = a row and 16 of its elements, a warp 32 rows.
+constexpr int kRowsJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kRowsJoinThreads) kv_attn_rows_join_kernel(const AttnParams p) {
+  constexpr int NT = kRowsNT, kParts = D / 16, kRows = 32 * (kRowsJoinThreads / 32 / kParts);  // warps a row, rows a block
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = blockIdx.y * kRows + warp / kParts * 32 + lane, e0 = warp % kParts * 4;  // row, group of four elements
+  const AttnPiece own = p.pieces[c0];
+  if (own.last <= c0 || q >= own.nrows) return;
+  const int n = own.last - c0 + 1;
+  auto slot = [&](int k) { return (long long)(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)); };
+  float m = -3.0e38f, sum = 0.f, o[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    const float2 ml = p.part_ml[slot(k) * NT + q];
+    float4 v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float4*>(p.part_o + ((slot(k) * (D / 4) + e0 + e) * NT + q) * 4);
+    const float now = fmaxf(m, ml.x), old = exp2_whole(m - now), f = exp2_whole(ml.x - now);
+    m = now;
+    sum = fmaf(ml.y, f, sum * old);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[4 * e] = fmaf(v[e].x, f, o[4 * e] * old);
+      o[4 * e + 1] = fmaf(v[e].y, f, o[4 * e + 1] * old);
+      o[4 * e + 2] = fmaf(v[e].z, f, o[4 * e + 2] * old);
+      o[4 * e + 3] = fmaf(v[e].w, f, o[4 * e + 3] * old);
+    }
+  }
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  const int r = own.r0 + q, tok = div_group(p, r), head = own.h * p.group + r - tok * p.group;
+  if (p.lse && e0 == 0) p.lse[(long long)(own.row0 + tok) * p.q.heads + head] = log_sum_exp(m, sum);
+  __nv_bfloat16* out = p.out.p + (long long)(own.row0 + tok) * p.out.ts + (long long)head * p.out.hs + 4 * e0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8)
+    *reinterpret_cast<uint4*>(out + e) = make_uint4(pack_bf16(o[e] * f, o[e + 1] * f), pack_bf16(o[e + 2] * f, o[e + 3] * f),
+                                                    pack_bf16(o[e + 4] * f, o[e + 5] * f), pack_bf16(o[e + 6] * f, o[e + 7] * f));
 }
 
 template <int D, bool kMasked>
@@ -344,9 +389,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         continue;
       }
       // ------------------------------------------------------- query operand
-      // D / 8 lanes a row, D / 16 passes, two rows of a thread under way.
+      // D / 8 lanes a row, D / 16 passes, four rows of a thread under way.
       {
-        constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+        constexpr int kLanes = D / 8, kRows = 256 / kLanes, kPass = 128 / kRows, kBatch = 4;
         const int l = ht % kLanes;
         auto load_row = [&](int pass) {
           const int q = 128 * half + pass * kRows + ht / kLanes;
@@ -354,19 +399,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
           return *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         };
-        uint4 v0 = load_row(0), v1 = load_row(1);
+        uint4 v[kBatch];
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) v[m] = load_row(m);
 #pragma unroll 1
-        for (int pass = 0; pass < kLanes / 2; ++pass) {
-          const uint4 v = v0;
-          v0 = v1;
-          if (pass + 2 < kLanes / 2) v1 = load_row(pass + 2);
-          const int q = pass * kRows + ht / kLanes;
-          // (a negative scale turns the queries' signs: the factor is positive)
-          const QuerySplit s = split_query<kLanes>(v, p.scale_log2 < 0.f ? -1.f : 1.f, 1.f);
-          const uint32_t at = qbuf + (uint32_t)(half * kHalf + (l & 1) * 8) + swizzled<D>(q, l >> 1);
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(s.hi.x), "r"(s.hi.y) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 128 * D), "r"(s.lo.x), "r"(s.lo.y) : "memory");
-          if (l == 0) c.qf[128 * half + q] = s.factor * fabsf(p.scale_log2);
+        for (int pass = 0; pass < kPass; pass += kBatch) {
+          uint4 now[kBatch];
+#pragma unroll
+          for (int m = 0; m < kBatch; ++m) now[m] = v[m];
+          if (pass + kBatch < kPass) {
+#pragma unroll
+            for (int m = 0; m < kBatch; ++m) v[m] = load_row(pass + kBatch + m);
+          }
+#pragma unroll
+          for (int m = 0; m < kBatch; ++m) {
+            const int q = (pass + m) * kRows + ht / kLanes;
+            // (a negative scale turns the queries' signs: the factor is positive)
+            const QuerySplit s = split_query<kLanes>(now[m], p.scale_log2 < 0.f ? -1.f : 1.f, 1.f);
+            const uint32_t at = qbuf + (uint32_t)(half * kHalf + (l & 1) * 8) + swizzled<D>(q, l >> 1);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(s.hi.x), "r"(s.hi.y) : "memory");
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + 128 * D), "r"(s.lo.x), "r"(s.lo.y) : "memory");
+            if (l == 0) c.qf[128 * half + q] = s.factor * fabsf(p.scale_log2);
+          }
         }
         fence_proxy_async_smem();
         meet();  // (the factors, too)
@@ -439,9 +493,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int pi = (32 * k + 16 * h) >> ps;
-            float m[2] = {__uint_as_float(x[16 * h]), __uint_as_float(x[16 * h + 1])};
+            float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 2; e < 16; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(x[16 * h + e]));
+            for (int e = 0; e < 16; e += 2)
+              m[e >> 1 & 1] = max3(m[e >> 1 & 1], __uint_as_float(x[16 * h + e]), __uint_as_float(x[16 * h + e + 1]));
             top = fmaxf(top, fmaf(fmaxf(m[0], m[1]), score_factor(c.kscale[meta][pi]), c.vexp[meta][pi]));
           }
         }
@@ -479,15 +534,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int pi = (64 * sub + 32 * k + 16 * h) >> ps;
             const float ve = c.vexp[meta][pi], kq = score_factor(c.kscale[meta][pi]), add = (ve + 8.f) - R;
-            float sum[2] = {0.f, 0.f};
+            const F2 kq2 = f2(kq, kq), add2 = f2(add, add);
+            F2 sum = f2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float z0 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e]), kq, add));
-              const float z1 = ex2(fmaf(__uint_as_float(x[16 * h + 2 * e + 1]), kq, add));
-              sum[0] += z0, sum[1] += z1;
-              w[8 * h + e] = pack_f16(z0, z1);
+              float2 z = f2_parts(f2_fma(f2(__uint_as_float(x[16 * h + 2 * e]), __uint_as_float(x[16 * h + 2 * e + 1])), kq2, add2));
+              z.x = ex2(z.x);
+              z.y = ex2(z.y);
+              sum = f2_add(sum, f2(z.x, z.y));
+              w[8 * h + e] = pack_f16(z.x, z.y);
             }
-            l = fmaf(sum[0] + sum[1], ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f, l);  // without the value scale
+            l = fmaf(f2_parts(sum).x + f2_parts(sum).y, ve > -INFINITY ? kv_exp2i(-(int)ve) : 0.f, l);  // without the value scale
           }
           tmem_st16(s_cols + 64 * sub + 16 * k, w);
         }
@@ -516,7 +573,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int head = g.h * p.group + r - rtok * p.group;
       __nv_bfloat16* out = p.out.p + (long long)(g.row0 + rtok) * p.out.ts + (long long)head * p.out.hs;
-      float* part = p.part_o + ((long long)g.slot * NT + q) * D;
+      // (four elements of 32 rows side by side: a warp's stores are whole lines)
+      float* part = p.part_o + ((long long)g.slot * (D / 4) * NT + q) * 4;
 #pragma unroll 1
       for (int k = sub * (D / 64); k < (sub + 1) * (D / 64); ++k) {  // this thread's half of the row
         uint32_t x[32];
@@ -540,7 +598,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         } else if (real) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(part + 32 * k + 4 * e) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            *reinterpret_cast<uint4*>(part + (long long)(8 * k + e) * NT * 4) = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         }
       }
       if (kMasked && p.lse && real && whole && sub == 0) p.lse[(long long)(g.row0 + rtok) * p.q.heads + head] = log_sum_exp(R, l);
