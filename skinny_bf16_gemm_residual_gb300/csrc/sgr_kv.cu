@@ -526,10 +526,17 @@ struct AttnPlan {
   int64_t bytes;    // workspace
 };
 
-AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags) {
+// mask: NULL for the workspace, which depends on the sizes alone (a window makes
+// the tiles of a sequence fewer, and what is chosen by them never larger).
+AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags,
+                   const sgr_kv_mask* mask) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
-  const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  if (mask && mask->window > 0) {
+    const long long seen = ((long long)mask->window + b.max_new) / sgr::kAttnTile + 2 + (mask->sinks + sgr::kAttnTile - 1LL) / sgr::kAttnTile;
+    if (seen < tiles) tiles = seen;
+  }
   auto row_tiles = [&](int nt) {  // at most
     const long long each = b.batch * ((rows + nt - 1) / nt), all = (long long)b.tokens * group / nt + b.batch;
     return c.heads * (each < all ? each : all);
@@ -539,17 +546,23 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   // (five drafted tokens and four heads a key/value head: 29.1 us in a tile of
   // 24 against 33.9 in one of 32).
   a.nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
-  // The 256-row kernel takes some 1.75 times (D = 64: 2.4 times) a 32-row
-  // unit's time for eight times the rows, but 12 units' time to begin and end.
-  // Measured with 28 heads of 128 over 4, small tiles against 256 rows: 19.1
-  // and 21.4 us (8 sequences of 3000, 35 rows a head each), 122.9 and 109.8 (96
-  // of them), 19.4 and 20.4 (4 of 3000, 126 rows), 51.6 and 32.6 (16 of them),
-  // 24.1 and 30.9 (one, 700 rows), 84 and 47 (one, 4200 rows), 113.0 and 63.4
-  // (one of 30000, 700 rows), 102.8 and 99 (32 of 9000, 63 rows), 166 and 107
-  // (112 rows); 32 heads of 64 over 8: 116 and 146 (32 of 9000, 36 rows), 47.5
-  // and 36.9 (3 of 20000, 96 rows).
-  const double unit = c.head_dim == 64 ? 2.4 : 1.75;
-  const bool gains = (double)tiles * ((double)row_tiles(32) - unit * (double)row_tiles(sgr::kRowsNT)) > 12.0 * sms;
+  // Work that does not fill the GPU even in smaller row tiles takes those: more
+  // CTAs, each with less (7 drafted tokens of 7 heads a key/value head over 700).
+  for (int nt : {8, 16, 24})
+    if (nt < a.nt && row_tiles(nt) * (tiles + 1) <= 2LL * sms) {
+      a.nt = nt;
+      break;
+    }
+  // The 256-row kernel takes some 1.25 times a 32-row unit's time for eight times
+  // the rows, but 8 units' time to begin and end.  Measured, small tiles against
+  // 256 rows, 28 heads of 128 over 4: 19.9 and 23.7 us (8 sequences of 3000, 35
+  // rows a head each), 133 and 104 (96 of them), 21.3 and 24.0 (4 of 3000, 126
+  // rows), 53 and 30 (16 of them), 30.0 and 26.1 (8 of 4000, 112 rows), 25.5 and
+  // 27.4 (one of 2000, 700 rows), 119 and 57 (one of 30000, 448 rows), 192 and 99
+  // (32 of 9000, 112 rows), but also 32.2 and 28.5 (24 of 1500, 63 rows); 32 heads
+  // of 64 over 8: 62.7 and 49.3 (16 of 5000, 48 rows), 180 and 131 (32 of 9000, 36
+  // rows), 22.1 and 19.2 (4 of 1500, 160 rows).
+  const bool gains = (double)tiles * ((double)row_tiles(32) - 1.25 * (double)row_tiles(sgr::kRowsNT)) > 8.0 * sms;
   if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);
@@ -617,7 +630,7 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
-  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads, flags);
+  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads, flags, mask);
   if (!a.fits || workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   // (a cache without pages: the maps are never used)
@@ -835,7 +848,7 @@ int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_
   if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
   if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
   if ((rc = sgr::kv_init_device(device)) != SGR_OK) return rc;
-  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads, flags).bytes;
+  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads, flags, nullptr).bytes;
   return SGR_OK;
 }
 

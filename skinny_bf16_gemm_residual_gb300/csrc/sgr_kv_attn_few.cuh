@@ -380,48 +380,57 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         if (g.kind & kSegStop) break;
       }
       // Row `pass` of this thread's: two are under way while one is converted.
-      auto load_row = [&](int pass, long long& out_at, int& pos, int& row) {
+      auto load_row = [&](int pass, long long& out_at, int& pos) {
         const int q = pass * kRows + qt / kLanes;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         pos = -1;  // a row that is none sees nothing
         out_at = 0;
-        row = 0;
         if (q < g.nrows) {
           const int r = g.r0 + q, tok = div_group(p, r), head = g.h * p.group + r - tok * p.group;
-          pos = kMasked && p.tree ? tree_row(p, g.row0, g.n, g.first, tok).last : row_last(g.first, tok);
-          row = g.row0 + tok;
+          pos = row_last(g.first, tok);
           out_at = (long long)(g.row0 + tok) * p.out.ts + (long long)head * p.out.hs;
           v = *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         }
         return v;
       };
       long long out0, out1 = 0;
-      int pos0, pos1 = -1, row0, row1 = 0;
-      uint4 v0 = load_row(0, out0, pos0, row0), v1 = v0;
-      if (kPass > 1) v1 = load_row(1, out1, pos1, row1);
+      int pos0, pos1 = -1;
+      uint4 v0 = load_row(0, out0, pos0), v1 = v0;
+      if (kPass > 1) v1 = load_row(1, out1, pos1);
+      // (a tree's rows: a thread each, so that their words are read at once)
+      TreeRow tr{-1, false};
+      int tree_at = 0;
+      if (kMasked && p.tree && qt < g.nrows) {
+        const int tok = div_group(p, g.r0 + qt);
+        tr = tree_row(p, g.row0, g.n, g.first, tok);
+        tree_at = g.row0 + tok;
+      }
       if (lane == 0 && !dry) ok = mbar_wait_nap<kNap>(smem_u32(&c.qempty[buf]), par ^ 1u, abort_flag);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
 #pragma unroll 1
       for (int i = 0; i < kPass; ++i) {
-        const int q = i * kRows + qt / kLanes, pos = pos0, row = row0;
+        const int q = i * kRows + qt / kLanes, pos = pos0;
         const long long out_at = out0;
         const uint4 v = v0;
-        v0 = v1, out0 = out1, pos0 = pos1, row0 = row1;
-        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1, row1);
+        v0 = v1, out0 = out1, pos0 = pos1;
+        if (i + 2 < kPass) v1 = load_row(i + 2, out1, pos1);
         const QuerySplit s = split_query<kLanes>(v, 1.f, 32.f);
         const uint32_t qb = qbuf + (uint32_t)(buf * Sh::kQBytes) + (uint32_t)((l & 1) * 8);
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(s.hi.x), "r"(s.hi.y) : "memory");
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(NT + q, l >> 1)), "r"(s.lo.x), "r"(s.lo.y) : "memory");
         if (l == 0) {
           c.qf[buf][q] = s.factor * p.scale_log2;
-          c.qpos[buf][q] = pos;
+          if (!kMasked || !p.tree) c.qpos[buf][q] = pos;
           c.qout[buf][q] = out_at;
-          if (kMasked) c.qrow[buf][q] = row;
         }
-        if (kMasked && qt == 0 && i == 0) {
-          c.qspan[buf][0] = g.first;
-          c.qspan[buf][1] = g.tlo;
-        }
+      }
+      if (kMasked && p.tree && qt < NT) {
+        c.qpos[buf][qt] = tr.last;
+        c.qrow[buf][qt] = tree_at;
+      }
+      if (kMasked && qt == 0) {
+        c.qspan[buf][0] = g.first;
+        c.qspan[buf][1] = g.tlo;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -524,9 +533,21 @@ __global__ void __launch_bounds__(AttnShape<D, NT>::kThreads, AttnShape<D, NT>::
         if (__builtin_expect(flags & 2, 0)) {
           if constexpr (kMasked) {
             const int pos = tile_at(t) * kAttnTile + tok;
-            unsigned seen = 0;  // (a rolled loop: unrolled it would cost registers)
-#pragma unroll 1
-            for (int q = 0; live && q < C; ++q) seen |= sees(pos, q) ? 1u << q : 0u;
+            unsigned seen = 0;
+            if (p.tree && pos >= c.qspan[buf][0]) {  // bits of a tree: the columns' words at once
+              const int j = pos - c.qspan[buf][0];
+              unsigned long long word[C];
+#pragma unroll
+              for (int q = 0; q < C; ++q)
+                word[q] = live && (j >> 6) < p.tree_words && c.qpos[buf][q0 + q] >= 0
+                              ? p.tree[c.qrow[buf][q0 + q] * p.tree_stride + (j >> 6)] : 0ULL;
+#pragma unroll
+              for (int q = 0; q < C; ++q) seen |= (unsigned)(word[q] >> (j & 63) & 1) << q;
+            } else {
+#pragma unroll
+              for (int q = 0; q < C; ++q)
+                seen |= live && row_sees(pos, c.qpos[buf][q0 + q], p.window, p.sinks) ? 1u << q : 0u;
+            }
 #pragma unroll
             for (int q = 0; q < C; ++q)
               if (!(seen >> q & 1)) x[q] = -INFINITY;

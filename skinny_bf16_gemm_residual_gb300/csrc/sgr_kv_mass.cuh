@@ -29,6 +29,7 @@
 // rows.
 #pragma once
 
+#include <climits>
 #include <type_traits>
 
 #include "sgr_kv_attn_few.cuh"
@@ -141,6 +142,16 @@ __device__ __forceinline__ bool mass_sees(const AttnParams& p, int pos, int firs
     return (p.tree[row * p.tree_stride + (j >> 6)] >> (j & 63) & 1) != 0;
   }
   return row_sees(pos, last, p.window, p.sinks);
+}
+
+// Which of the rows from r on see a position (no tree): rows are in the order
+// of their positions, so they are those from the position's own token on, up to
+// the last whose window it is in.
+__device__ __forceinline__ uint32_t mass_rows(const AttnParams& p, int pos, int first, int r, int rows) {
+  const long long tok = (long long)pos - first;
+  const long long lo = tok * p.group, hi = pos < p.sinks || p.window == INT_MAX ? rows : min((tok + p.window) * p.group, (long long)rows);
+  const int a = (int)min(max(lo - r, 0LL), 32LL), b = (int)min(max(hi - r, 0LL), 32LL);  // columns [a, b)
+  return a >= b ? 0u : (0xffffffffu >> (32 - b)) & (0xffffffffu << a);
 }
 
 template <int D, int NT>
@@ -258,45 +269,43 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
       ++sq;
       if (g.kind & kSegStop) break;
       for (int k = 0; k * R < g.nrows && ok; ++k) {
-        struct Row {
-          uint4 v;
-          float lse;
-          int last, row;
-        };
         // Row `pass` of this thread's: two are under way while one is converted.
         auto load_row = [&](int pass) {
-          Row r{make_uint4(0u, 0u, 0u, 0u), -INFINITY, -1, 0};  // a row that is none sees nothing
           const int q = k * R + pass * kStep + qt / kLanes;
-          if (q < g.nrows) {
-            const int at = g.r0 + q, tok = div_group(p, at), head = g.h * p.group + at - tok * p.group;
-            r.row = g.row0 + tok;
-            r.last = p.tree ? tree_row(p, g.row0, g.n, g.first, tok).last : row_last(g.first, tok);
-            r.v = *reinterpret_cast<const uint4*>(p.q.p + (long long)r.row * p.q.ts + (long long)head * p.q.hs + 8 * l);
-            r.lse = p.lse[(long long)r.row * p.q.heads + head];
-          }
-          return r;
+          if (q >= g.nrows) return make_uint4(0u, 0u, 0u, 0u);
+          const int at = g.r0 + q, tok = div_group(p, at), head = g.h * p.group + at - tok * p.group;
+          return *reinterpret_cast<const uint4*>(p.q.p + (long long)(g.row0 + tok) * p.q.ts + (long long)head * p.q.hs + 8 * l);
         };
-        Row r0 = load_row(0), r1 = r0;
-        if (kPass > 1) r1 = load_row(1);
+        uint4 v0 = load_row(0), v1 = v0;
+        if (kPass > 1) v1 = load_row(1);
+        // What there is one of a row: a thread each.
+        float lse = -INFINITY;
+        int last = -1, row = 0;  // a row that is none sees nothing
+        if (qt < R && k * R + qt < g.nrows) {
+          const int at = g.r0 + k * R + qt, tok = div_group(p, at);
+          row = g.row0 + tok;
+          lse = p.lse[(long long)row * p.q.heads + g.h * p.group + at - tok * p.group];
+          last = p.tree ? tree_row(p, g.row0, g.n, g.first, tok).last : row_last(g.first, tok);
+        }
         if (lane == 0) ok = mbar_wait_nap<kNap>(smem_u32(&c.qempty[slot]), par ^ 1u, abort_flag);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
 #pragma unroll 1
         for (int i = 0; i < kPass; ++i) {
           const int q = i * kStep + qt / kLanes;
-          const Row r = r0;
-          r0 = r1;
-          if (i + 2 < kPass) r1 = load_row(i + 2);
-          const QuerySplit s = split_query<kLanes>(r.v, 1.f, 32.f);
+          const uint4 v = v0;
+          v0 = v1;
+          if (i + 2 < kPass) v1 = load_row(i + 2);
+          const QuerySplit s = split_query<kLanes>(v, 1.f, 32.f);
           const uint32_t qb = qbuf + (uint32_t)(slot * Sh::kSlotBytes) + (uint32_t)((l & 1) * 8);
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(q, l >> 1)), "r"(s.hi.x), "r"(s.hi.y) : "memory");
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qb + swizzled<D>(R + q, l >> 1)), "r"(s.lo.x), "r"(s.lo.y) : "memory");
-          if (l == 0) {
-            c.qf[slot][q] = s.factor * p.scale_log2;
-            c.ql[slot][q] = r.lse == -INFINITY ? -INFINITY : -1.4426950408889634f * r.lse;
-            c.qpos[slot][q] = r.last;
-            c.qrow[slot][q] = r.row;
-          }
+          if (l == 0) c.qf[slot][q] = s.factor * p.scale_log2;
+        }
+        if (qt < R) {
+          c.ql[slot][qt] = lse == -INFINITY ? -INFINITY : -1.4426950408889634f * lse;
+          c.qpos[slot][qt] = last;
+          c.qrow[slot][qt] = row;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -392,9 +401,13 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
             }
             if (__builtin_expect(flags & 2, 0)) {
               uint32_t seen = 0u;
+              if (live && p.tree) {
 #pragma unroll 1
-              for (int e = 0; live && e < P; ++e)
-                seen |= mass_sees(p, pos, g.first, c.qpos[q][c0 + e], c.qrow[q][c0 + e]) ? 1u << e : 0u;
+                for (int e = 0; e < P; ++e)
+                  seen |= mass_sees(p, pos, g.first, c.qpos[q][c0 + e], c.qrow[q][c0 + e]) ? 1u << e : 0u;
+              } else if (live) {
+                seen = mass_rows(p, pos, g.first, g.r0 + k * R + c0, g.r0 + g.nrows);
+              }
               weigh(std::true_type(), c0, seen);
             } else {
               weigh(std::false_type(), c0, 0u);
