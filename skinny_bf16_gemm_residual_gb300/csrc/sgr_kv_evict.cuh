@@ -341,17 +341,52 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
   if (ranks > 1) cluster_wait();  // (until all have read this CTA's counts)
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Largest magnitude of 16 codes, as its code (NaN does not count).
 __device__ __forceinline__ uint32_t largest_code(const uint4& v) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t u[4] = {v.x & 0x7F7F7F7Fu, v.y & 0x7F7F7F7Fu, v.z & 0x7F7F7F7Fu, v.w & 0x7F7F7F7Fu};
+  const uint32_t nan = (u[0] + 0x01010101u) | (u[1] + 0x01010101u) | (u[2] + 0x01010101u) | (u[3] + 0x01010101u);
+  if (__builtin_expect(nan & 0x80808080u, 0)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] &= ~__vcmpeq4(u[j], 0x7F7F7F7Fu);
+  }
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t a = u[j] & 0x7F7F7F7Fu;
-    m = __vmaxu4(m, a & ~__vcmpeq4(a, 0x7F7F7F7Fu));
-  }
-  m = __vmaxu4(m, m >> 16);
-  return max(m & 0xFFu, m >> 8 & 0xFFu);
+  for (int j = 0; j < 4; ++j) m = max_u16x2(max_u16x2(m, u[j] & 0x00FF00FFu), u[j] >> 8 & 0x00FF00FFu);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// 2^d as a pair of FP16 numbers, -24 <= d <= 15.
+__device__ __forceinline__ uint32_t f16x2_exp2(int d) {
+  const uint32_t h = d >= -14 ? (uint32_t)(d + 15) << 10 : 1u << (24 + d);
+  return h | h << 16;
+}
+
+// Four codes times 2^d, rounded to codes.  In FP16 a code times a power of two
+// is exact down to multiples of 2^-24, far below what E4M3 rounds to zero; below
+// 2^-24 times the largest code, and above 2^15 (which a code other than zero
+// grows by at most twice more), it takes the bounds' factors.
+__device__ __forceinline__ uint32_t scale_codes(uint32_t v, uint32_t f, uint32_t more) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x, y;\n\t"
+      "mov.b32 {lo, hi}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 x, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 y, hi;\n\t"
+      "mul.rn.f16x2 x, x, %2;\n\t"
+      "mul.rn.f16x2 y, y, %2;\n\t"
+      "mul.rn.f16x2 x, x, %3;\n\t"
+      "mul.rn.f16x2 y, y, %3;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 lo, x;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, y;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "r"(v), "r"(f), "r"(more));
+  return r;
 }
 
 constexpr int kMoveThreads = 256;
@@ -440,14 +475,10 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 2 ? 6 : 4) kv_move_kerne
       const int e = __shfl_sync(0xffffffffu, e_old[x], tok);
       uint32_t u[4] = {v[x][i].x, v[x][i].y, v[x][i].z, v[x][i].w};
       if (e != e_new[x]) {
-        // (a page of zeros has the least scale: zeros times 2^127 stay zeros)
-        const float f = kv_exp2i(min(e - e_new[x], 127));
+        const int d = e - e_new[x];
+        const uint32_t f = f16x2_exp2(max(min(d, 15), -24)), more = f16x2_exp2(max(min(d - 15, 15), 0));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float a0, a1, a2, a3;
-          from_e4m3x4(u[j], a0, a1, a2, a3);
-          u[j] = to_e4m3x4(a0 * f, a1 * f, a2 * f, a3 * f);
-        }
+        for (int j = 0; j < 4; ++j) u[j] = scale_codes(u[j], f, more);
       }
       if (t < count) *reinterpret_cast<uint4*>((x ? p.cache.v : p.cache.k) + at) = make_uint4(u[0], u[1], u[2], u[3]);
     }

@@ -25,7 +25,7 @@
 //
 // Roles: four warps weigh (thread = key; eight for products of 32 rows or more,
 // half of the columns each), one walks the work and loads pages, one issues the
-// MMAs, two (four for 128 rows) bring queries into the operand, a ring of products' worth of
+// MMAs, two bring queries into the operand, a ring of products' worth of
 // rows.
 #pragma once
 
@@ -54,7 +54,7 @@ struct MassShape {
   static constexpr int kCols = 2 * kRows;
   static constexpr int kAcc = kRows == 64 ? 2 : 4;  // accumulators
   static constexpr int kGroups = kRows >= 32 ? 2 : 1;  // of 4 weighing warps, each a part of a product's columns
-  static constexpr int kWeigh = 4 * kGroups, kQuery = NT > 32 ? 4 : 2;  // warps
+  static constexpr int kWeigh = 4 * kGroups, kQuery = 2;  // warps
   static constexpr int kThreads = 32 * (kWeigh + 2 + kQuery);
   static constexpr int kTileBytes = kAttnTile * D;
   static constexpr int kSlotBytes = kCols * D;
@@ -370,13 +370,12 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
             live = page >= 0 && tok >= c.live[slot][0] && tok < c.live[slot][1];
           }
           const F2 third = f2(kLoScale, kLoScale);
-          // P columns at a time, from c0 on.
-          constexpr int P = C < 16 ? C : 16;
-          float hi[P], lo[P];
-          auto weigh = [&](auto masked, int c0, uint32_t seen) {
+          // Adds the weights of N columns from c0 on; seen: which count (kHide).
+          auto weigh = [&](auto masked, const auto& hi, const auto& lo, int c0, uint32_t seen) {
             constexpr bool kHide = decltype(masked)::value;
+            constexpr int N = sizeof(hi) / sizeof(float);
 #pragma unroll
-            for (int e = 0; e < P; e += 4) {
+            for (int e = 0; e < N; e += 4) {
               const float4 f = *reinterpret_cast<const float4*>(&c.qf[q][c0 + e]);
               const float4 l = *reinterpret_cast<const float4*>(&c.ql[q][c0 + e]);
               const F2 s0 = f2_fma(f2(lo[e], lo[e + 1]), third, f2(hi[e], hi[e + 1]));
@@ -390,29 +389,35 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
               sum[1] = f2_add(sum[1], f2(w[2], w[3]));
             }
           };
-#pragma unroll
-          for (int h = 0; h < C / P; ++h) {
-            const int c0 = group * C + h * P;
-            tmem_ld_parts<P>(lanes + (uint32_t)(a * kCols + h * P), R, hi, lo);
-            if (h == C / P - 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&c.sempty[a]));
-            }
-            if (__builtin_expect(flags & 2, 0)) {
+          const uint32_t cols = lanes + (uint32_t)(a * kCols);
+          if (__builtin_expect(flags & 2, 0)) {  // (seldom: eight columns at a time, in as little code as that takes)
+#pragma unroll 1
+            for (int c0 = 0; c0 < C; c0 += 8) {
+              float hi[8], lo[8];
+              tmem_ld8x2(cols + (uint32_t)c0, cols + (uint32_t)(R + c0), hi, lo);
+              const int at = group * C + c0;
               uint32_t seen = 0u;
               if (live && p.tree) {
 #pragma unroll 1
-                for (int e = 0; e < P; ++e)
-                  seen |= mass_sees(p, pos, g.first, c.qpos[q][c0 + e], c.qrow[q][c0 + e]) ? 1u << e : 0u;
+                for (int e = 0; e < 8; ++e)
+                  seen |= mass_sees(p, pos, g.first, c.qpos[q][at + e], c.qrow[q][at + e]) ? 1u << e : 0u;
               } else if (live) {
-                seen = mass_rows(p, pos, g.first, g.r0 + k * R + c0, g.r0 + g.nrows);
+                seen = mass_rows(p, pos, g.first, g.r0 + k * R + at, g.r0 + g.nrows);
               }
-              weigh(std::true_type(), c0, seen);
-            } else {
-              weigh(std::false_type(), c0, 0u);
+              weigh(std::true_type(), hi, lo, at, seen);
+            }
+          } else {
+            constexpr int P = C < 16 ? C : 16;  // columns at a time
+#pragma unroll
+            for (int c0 = 0; c0 < C; c0 += P) {
+              float hi[P], lo[P];
+              tmem_ld_parts<P>(cols + (uint32_t)c0, R, hi, lo);
+              weigh(std::false_type(), hi, lo, group * C + c0, 0u);
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&c.sempty[a]));
         }
         const float2 s2 = f2_parts(f2_add(sum[0], sum[1]));
         float w = s2.x + s2.y;
