@@ -526,8 +526,9 @@ struct AttnPlan {
   int64_t bytes;    // workspace
 };
 
-// mask: NULL for the workspace, which depends on the sizes alone (a window makes
-// the tiles of a sequence fewer, and what is chosen by them never larger).
+// mask: NULL for the workspace, which depends on the sizes alone and is enough
+// for any mask (a window makes the tiles of a sequence fewer, and by that perhaps
+// the row tiles smaller, of which more are under way).
 AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags,
                    const sgr_kv_mask* mask) {
   AttnPlan a;
@@ -576,7 +577,13 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   a.fits = units < (1LL << 31) && tiles < (1 << 24);
   a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
-  a.bytes = a.grid * (2LL * a.nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece));
+  auto bytes = [&](long long grid, int nt) { return grid * (2LL * nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece)); };
+  a.bytes = bytes(a.grid, a.nt);
+  for (int nt : {8, 16, 24, 32}) {
+    const long long most = row_tiles(nt) * (tiles + 1), held = nt >= 32 ? sms : 2LL * sms;
+    const int64_t need = bytes(most < held ? most : held, nt);
+    if (!mask && nt < a.nt && need > a.bytes) a.bytes = need;
+  }
   return a;
 }
 

@@ -86,9 +86,9 @@ struct TileMap {
   int tw, gap;
 
   // (sinks = 0: the identity)
-  __device__ __forceinline__ TileMap(int tlo, int sinks)
+  __host__ __device__ __forceinline__ TileMap(int tlo, int sinks)
       : tw(tlo / kAttnTile), gap(tw - min((int)(((unsigned)sinks + kAttnTile - 1) / kAttnTile), tw)) {}
-  __device__ __forceinline__ int at(int t) const { return t < tw ? t - gap : t; }
+  __host__ __device__ __forceinline__ int at(int t) const { return t < tw ? t - gap : t; }
 };
 
 // r / group for 0 <= r < 2^31: the product is at most one too small.
@@ -123,7 +123,7 @@ __host__ __device__ __forceinline__ bool row_sees(int pos, int last, int window,
 // ------------------------------------------------------------ drafted trees
 // A row's bits from the j-th new token on, 32 of them (bits past the last word
 // are zeros).
-__device__ __forceinline__ uint32_t tree_bits(const unsigned long long* row, int words, int j) {
+__host__ __device__ __forceinline__ uint32_t tree_bits(const unsigned long long* row, int words, int j) {
   const int w = j >> 6, s = j & 63;
   const unsigned long long lo = w < words ? row[w] : 0ULL, hi = s > 32 && w + 1 < words ? row[w + 1] : 0ULL;
   return (uint32_t)(lo >> s) | (s > 32 ? (uint32_t)(hi << (64 - s)) : 0u);
@@ -137,7 +137,7 @@ struct TreeRow {
   bool drafts;
 };
 
-__device__ __forceinline__ TreeRow tree_row(const AttnParams& p, int row0, int n, int first, int tok) {
+__host__ __device__ __forceinline__ TreeRow tree_row(const AttnParams& p, int row0, int n, int first, int tok) {
   if (first + tok < 0) return {-1, false};
   const unsigned long long* bits = p.tree + (long long)(row0 + tok) * p.tree_stride;
   const int j0 = first < 0 ? -first : 0;  // new tokens before the first position are not there
@@ -146,20 +146,24 @@ __device__ __forceinline__ TreeRow tree_row(const AttnParams& p, int row0, int n
     unsigned long long x = bits[w];
     if (n - 64 * w < 64) x &= (1ULL << (n - 64 * w)) - 1;
     if (j0 > 64 * w) x = j0 - 64 * w < 64 ? x >> (j0 - 64 * w) << (j0 - 64 * w) : 0ULL;
+#ifdef __CUDA_ARCH__
     count += __popcll(x);
+#else
+    count += __builtin_popcountll(x);
+#endif
   }
   return {max(first, 0) + max(count - 1, 0), count > 0};
 }
 
 // Bits of the positions x .. x + 31 that lie in [lo, hi].
-__device__ __forceinline__ uint32_t span_bits(int x, int lo, int hi) {
+__host__ __device__ __forceinline__ uint32_t span_bits(int x, int lo, int hi) {
   const int a = max(lo - x, 0), b = min(hi - x, 31);
   return a > b ? 0u : (0xffffffffu >> (31 - b)) & (0xffffffffu << a);
 }
 
 // Bits of the positions x .. x + 31 (x >= 0) that a row with this `last` sees;
 // thi: behind the sequence's last position, first: its first new one.
-__device__ __forceinline__ uint32_t row_bits(const AttnParams& p, int x, int last, int thi, int first, int row) {
+__host__ __device__ __forceinline__ uint32_t row_bits(const AttnParams& p, int x, int last, int thi, int first, int row) {
   uint32_t m = span_bits(x, max(last - p.window + 1, 0), last) | span_bits(x, 0, min(last, p.sinks - 1));
   if (p.tree && x + 31 >= first) {
     m &= span_bits(x, 0, first - 1);

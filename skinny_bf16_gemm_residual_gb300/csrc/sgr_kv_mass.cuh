@@ -147,7 +147,7 @@ __device__ __forceinline__ bool mass_sees(const AttnParams& p, int pos, int firs
 // Which of the rows from r on see a position (no tree): rows are in the order
 // of their positions, so they are those from the position's own token on, up to
 // the last whose window it is in.
-__device__ __forceinline__ uint32_t mass_rows(const AttnParams& p, int pos, int first, int r, int rows) {
+__host__ __device__ __forceinline__ uint32_t mass_rows(const AttnParams& p, int pos, int first, int r, int rows) {
   const long long tok = (long long)pos - first;
   const long long lo = tok * p.group, hi = pos < p.sinks || p.window == INT_MAX ? rows : min((tok + p.window) * p.group, (long long)rows);
   const int a = (int)min(max(lo - r, 0LL), 32LL), b = (int)min(max(hi - r, 0LL), 32LL);  // columns [a, b)

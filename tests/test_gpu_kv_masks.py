@@ -241,6 +241,24 @@ def test_log_sum_exp_rows_of_no_sequence_are_left():
         assert (lse[4:] == 7).all() and not (lse[:4] == 7).any()
 
 
+@pytest.mark.parametrize("dim,page,heads,hk,lens,new", [
+    (128, 32, 4, 2, [13, 319], [2, 107]), (64, 16, 24, 2, [2000] * 5, [30] * 5), (128, 64, 28, 4, [9000], [7]),
+    (128, 128, 8, 1, [5000, 70], [200, 3]), (64, 64, 8, 8, [4000] * 40, [5] * 40)])
+def test_workspace_is_enough_for_any_window(dim, page, heads, hk, lens, new):
+    """The workspace depends on the sizes alone; a window may change the row tiles."""
+    pr = ref.Problem(dim, page, hk, [1] * len(lens), [1] * len(lens), extra_pages=4)  # (no position is looked at)
+    cache = pr.cache(sgr)
+    table = torch.zeros(len(lens), -(-max(lens) // page), dtype=torch.int32, device="cuda")
+    start = torch.zeros(len(lens) + 1, dtype=torch.int32, device="cuda")  # no rows
+    batch = sgr.KvBatch(table, torch.zeros(len(lens), dtype=torch.int32, device="cuda"), start, tokens=sum(new), max_new=max(new))
+    q = torch.zeros(sum(new), heads, dim, dtype=torch.bfloat16, device="cuda")
+    for flags in (0, FEW, MANY):
+        work = sgr.kv_attention_workspace(cache, batch, heads, flags)
+        for window in (0, 1, 30, 100, 300, 700, 1000, 2000, 4000, 100000):
+            for sinks in (0, 4, 600):
+                sgr.sgr_kv_attention(cache, batch, q, window=window, sinks=sinks, workspace=work, flags=flags)
+
+
 # ------------------------------------------------------------------------- append
 @pytest.mark.parametrize("dim,interleaved", [(64, True), (128, False)])
 def test_append_to_given_positions(dim, interleaved):

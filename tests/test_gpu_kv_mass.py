@@ -212,7 +212,7 @@ def grown(pr, more):
     pr.pages += more
 
 
-def evict(pr, keeps, first, recent, mass=None, flags=0):
+def evict(pr, keeps, first, recent, mass=None, flags=0, odd=False):
     new_table, more = fresh_table(pr, keeps)
     grown(pr, more)
     if mass is None:
@@ -222,6 +222,10 @@ def evict(pr, keeps, first, recent, mass=None, flags=0):
     cache, batch = pr.cache(sgr), pr.batch(sgr)
     kept = torch.full((len(pr.lens), pr.hk, new_table.shape[1] * pr.page), -7, dtype=torch.int32, device="cuda")
     got = mass.cuda()
+    if odd:  # masses whose rows are not aligned to 16 bytes
+        wide = torch.zeros(pr.pages, pr.hk, pr.page + 1, device="cuda")
+        wide[:, :, 1:] = got
+        got = wide[:, :, 1:]
     new_len, back = sgr.sgr_kv_evict(cache, batch, got, torch.tensor(keeps, dtype=torch.int32).cuda(), new_table.cuda(),
                                      first=first, recent=recent, kept=kept, flags=flags)
     assert back is kept
@@ -277,6 +281,11 @@ EVICT = [
 def test_evict(dim, page, hk, lens, keep, first, recent):
     pr = ref.Problem(dim, page, hk, lens, [min(1, l) for l in lens], seed=sum(lens), heads_inside=hk == 2)
     evict(pr, keep, first, recent)
+
+
+@pytest.mark.parametrize("lens,keep", [([700, 33], [100, 20]), ([40000], [7000])])
+def test_evict_masses_of_odd_strides(lens, keep):
+    evict(ref.Problem(64, 16, 1, lens, [1] * len(lens), seed=len(lens)), keep, 3, 9, odd=True)
 
 
 @pytest.mark.parametrize("kind", ["equal", "few", "signs", "tiny"])
