@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParam
   const long long at = mass_part<NT>(mp, b, s.row0, 0, h) + pos, step = (long long)p.cache.heads * mp.tiles * kAttnTile;
   float w = 0.f;
   bool any = false;
+#pragma unroll 4
   for (int j = 0; j * NT < s.n * p.group; ++j) {
     const AttnItem it = attn_item<NT, true>(p, s, j);
     const TileMap tm(it.tlo, p.sinks);
