@@ -736,7 +736,7 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
   const int runs = c->page_size * c->head_dim / 16, vec = runs / 32 < 4 ? 2 : 4, warps = runs / (32 * vec);
   const int per_block = sgr::kMoveThreads / 32 / warps;
   const long long moves = (items * ev->max_pages + per_block - 1) / per_block;
-  if (items * cluster > 0x7fffffffLL || moves > 0x7fffffffLL || items > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
+  if (items * cluster > 0x7fffffffLL || items * (long long)ev->max_pages > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
   sgr::EvictParams p;
   p.cache = cache_of(*c);
   p.batch = batch_of(*b);
@@ -754,6 +754,8 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
   p.new_len = ev->new_len;
   const long long run = ((longest + cluster - 1) / cluster + 3) & ~3LL;  // of a CTA, at most
   p.cached = (int)(run < sgr::kSelectCached ? run : sgr::kSelectCached);
+  p.pages_inv = ev->max_pages > 1 ? (unsigned)((1ULL << 32) / ev->max_pages) : 0xffffffffu;
+  p.heads_inv = c->heads > 1 ? (unsigned)((1ULL << 32) / c->heads) : 0xffffffffu;
   p.wide = aligned(mass->data, 16) && mass->page_stride % 4 == 0 && mass->head_stride % 4 == 0;
   p.err = dev->err;
   cudaLaunchConfig_t lc = {};

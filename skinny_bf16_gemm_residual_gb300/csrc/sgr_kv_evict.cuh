@@ -40,6 +40,7 @@ struct EvictParams {
   int* new_len;
   int cached;  // keys that a CTA of the selection holds in shared memory
   int wide;    // whether 16-byte reads of the mass are aligned
+  unsigned pages_inv, heads_inv;  // floor(2^32 / new_pages) and of the heads, at most 2^32 - 1
   unsigned* err;
 };
 
@@ -53,6 +54,12 @@ struct EvictPlan {
   int len, first, recent, chosen;
   __device__ __forceinline__ int total() const { return first + chosen + recent; }
 };
+
+// n / d for 0 <= n < 2^31 by d's inverse: the product is at most one too small.
+__device__ __forceinline__ int div_by(int n, int d, unsigned inv) {
+  const int q = (int)__umulhi((unsigned)n, inv);
+  return q + (n - q * d >= d ? 1 : 0);
+}
 
 __device__ __forceinline__ EvictPlan evict_plan(const EvictParams& p, int b, unsigned* err) {
   EvictPlan e;
@@ -367,11 +374,10 @@ __device__ __forceinline__ uint32_t f16x2_exp2(int d) {
   return h | h << 16;
 }
 
-// Four codes times 2^d, rounded to codes.  In FP16 a code times a power of two
-// is exact down to multiples of 2^-24, far below what E4M3 rounds to zero; below
-// 2^-24 times the largest code, and above 2^15 (which a code other than zero
-// grows by at most twice more), it takes the bounds' factors.
-__device__ __forceinline__ uint32_t scale_codes(uint32_t v, uint32_t f, uint32_t more) {
+// Four codes times 2^d as f = f16x2_exp2(d), rounded to codes.  In FP16 a code
+// times a power of two is exact down to multiples of 2^-24, far below what E4M3
+// rounds to zero, and the factor 2^-24 rounds all codes to zero, as lesser ones do.
+__device__ __forceinline__ uint32_t scale_codes(uint32_t v, uint32_t f) {
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 x, y;\n\t"
       "mov.b32 {lo, hi}, %1;\n\t"
@@ -379,13 +385,11 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t v, uint32_t f, uint32_t
       "cvt.rn.f16x2.e4m3x2 y, hi;\n\t"
       "mul.rn.f16x2 x, x, %2;\n\t"
       "mul.rn.f16x2 y, y, %2;\n\t"
-      "mul.rn.f16x2 x, x, %3;\n\t"
-      "mul.rn.f16x2 y, y, %3;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 lo, x;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 hi, y;\n\t"
       "mov.b32 %0, {lo, hi};\n\t}"
       : "=r"(r)
-      : "r"(v), "r"(f), "r"(more));
+      : "r"(v), "r"(f));
   return r;
 }
 
@@ -403,13 +407,13 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 2 ? 6 : 4) kv_move_kerne
   pdl_wait();
   const int ps = p.cache.page_shift, heads = p.cache.heads;
   const int warps = max((1 << ps) / kTok, 1), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * (kMoveThreads / 32 / warps) + warp / warps;
-  const long long units = (long long)p.batch.batch * heads * p.new_pages;
-  const int block = (int)(unit % p.new_pages), item = (int)(min(unit, units - 1) / p.new_pages);
-  const int h = item % heads, b = item / heads, slot0 = block << ps, t0 = warp % warps * kTok;
+  const int shift = __ffs(warps) - 1;  // (a power of two)
+  const int units = p.batch.batch * heads * p.new_pages, all = (int)blockIdx.x * (kMoveThreads / 32 >> shift) + (warp >> shift);
+  const int unit = min(all, units - 1), item = div_by(unit, p.new_pages, p.pages_inv), block = unit - item * p.new_pages;
+  const int b = div_by(item, heads, p.heads_inv), h = item - b * heads, slot0 = block << ps, t0 = (warp & (warps - 1)) * kTok;
   // (three round trips: the number of positions, which, and the new page; their
   // pages; what they hold.  Positions past the number may be read, not followed.)
-  int count = unit < units ? min(p.new_len[b] - slot0, 1 << ps) : 0;
+  int count = all < units ? min(p.new_len[b] - slot0, 1 << ps) : 0;
   const int to = p.new_table[(long long)b * p.new_stride + block];
   const int mine = t0 + min(lane, kTok - 1);  // this lane's position of the new page
   int from = p.kept[(long long)item * ((long long)p.new_pages << ps) + slot0 + mine];
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 2 ? 6 : 4) kv_move_kerne
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-      for (int w = warp / warps * warps; w < (warp / warps + 1) * warps; ++w) top[x] = fmaxf(top[x], part[x][w]);
+      for (int w = warp & ~(warps - 1); w < (warp & ~(warps - 1)) + warps; ++w) top[x] = fmaxf(top[x], part[x][w]);
   }
 #pragma unroll
   for (int x = 0; x < 2; ++x) e_new[x] = kv_scale_exp(top[x]);
@@ -476,9 +480,13 @@ __global__ void __launch_bounds__(kMoveThreads, kVec == 2 ? 6 : 4) kv_move_kerne
       uint32_t u[4] = {v[x][i].x, v[x][i].y, v[x][i].z, v[x][i].w};
       if (e != e_new[x]) {
         const int d = e - e_new[x];
-        const uint32_t f = f16x2_exp2(max(min(d, 15), -24)), more = f16x2_exp2(max(min(d - 15, 15), 0));
+        const uint32_t f = f16x2_exp2(max(min(d, 15), -24));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = scale_codes(u[j], f, more);
+        for (int j = 0; j < 4; ++j) u[j] = scale_codes(u[j], f);
+        if (__builtin_expect(d > 15, 0)) {  // (2^17 at most for codes other than zero)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) u[j] = scale_codes(u[j], f16x2_exp2(min(d - 15, 15)));
+        }
       }
       if (t < count) *reinterpret_cast<uint4*>((x ? p.cache.v : p.cache.k) + at) = make_uint4(u[0], u[1], u[2], u[3]);
     }
