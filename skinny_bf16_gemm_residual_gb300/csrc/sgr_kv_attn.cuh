@@ -734,7 +734,7 @@ __device__ __forceinline__ float log_sum_exp(float R, float sum) {
 //     o = sum_k 2^(R_k - m) o_k / sum_k 2^(R_k - m) l_k,   m = max_k R_k
 //
 // Bound: the latency of its launch and of those two round trips, some 3 us of
-// a call (two chunks of prompts, 33 MB of partial sums: 12 us from a cold L2).
+// a call.
 constexpr int kJoinThreads = 256;
 
 template <int NT>

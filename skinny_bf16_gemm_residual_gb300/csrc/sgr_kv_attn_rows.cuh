@@ -29,10 +29,14 @@
 // product, its completion and the next scores (2100; the scores' columns are
 // the weights', so these products cannot overlap), with the other half half a
 // turn behind.  Tensor memory is full (two halves of scores and outputs, 128
-// columns each): a third chain would take scores of fewer tokens at a time.  Measured for two chunks of some
-// 600 tokens over 6007 (28 heads over 4, 74 GFLOP): 118 us, 625 TFLOP/s,
-// tensor pipe 31% and issue slots 58% of active cycles; with one softmax
-// thread a row instead of two 129 us.
+// columns each).  Measured for two chunks of some 600 tokens over 6007 (28 heads
+// over 4, 74 GFLOP): 103 us, 717 TFLOP/s; with one softmax thread a row instead of
+// two 129 us.  Trees of 129 tokens over windows of 16384 (8 heads a key/value
+// head, 287 GFLOP): 386 us, 744 TFLOP/s, tensor pipe 40% and issue slots 62% of
+// active cycles.  Scores of 64 tokens at a time in two buffers a half, a thread
+// that issues for each half, and halves that take the tiles of few rows in turns
+// were all slower (447 to 521, 443, and 389 us for the trees): the products'
+// issue then sets the pace.
 //
 // Roles (704 threads, one CTA an SM): warps 0-7 and 8-15 softmax of the halves
 // (and their query operands), 16-19 widen V, warp 20 walks the work and loads

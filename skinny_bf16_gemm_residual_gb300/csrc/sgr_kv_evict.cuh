@@ -2,6 +2,12 @@
 // weight (sgr_attention.h): which positions of a head stay, and their move to
 // new pages.
 //
+// Bound: few positions: the chain of reads and cluster barriers (1100 positions:
+// 10 us, of which the selection 6); one sequence of 130001: 40 us (selection 20,
+// on 64 CTAs; the move 16, 67 MB); 48 of up to 8000 in pages of 16 by 64 codes, 417
+// MB: 125 us (selection 25: additions to shared memory and issue; the move 78, 5.3
+// TB/s under the profiler, issue slots 72% taken).
+//
 // Selection.  Of the positions between the protected ends the m with the
 // largest mass stay, of equal ones the first.  Their masses as 32-bit keys in
 // the order of the numbers, the m-th largest is found digit by digit (10, 11
