@@ -736,7 +736,8 @@ int run_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_masses*
   const int runs = c->page_size * c->head_dim / 16, vec = runs / 32 < 4 ? 2 : 4, warps = runs / (32 * vec);
   const int per_block = sgr::kMoveThreads / 32 / warps;
   const long long moves = (items * ev->max_pages + per_block - 1) / per_block;
-  if (items * cluster > 0x7fffffffLL || items * (long long)ev->max_pages > 0x7fffffffLL) return SGR_ERR_UNSUPPORTED;
+  if (items * cluster > 0x7fffffffLL || items * (long long)ev->max_pages > 0x7fffff00LL)
+    return SGR_ERR_UNSUPPORTED;  // (31 bits hold a block's pages, too)
   sgr::EvictParams p;
   p.cache = cache_of(*c);
   p.batch = batch_of(*b);
