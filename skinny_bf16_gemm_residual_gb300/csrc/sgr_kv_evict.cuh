@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_select_kernel(const EvictPa
   // Finds the bin in which, from the highest down, the wanted number is reached.
   auto find = [&](auto log_bins_of, const unsigned* sum) {
     constexpr int kLog = decltype(log_bins_of)::value, kMine = (1 << kLog) / kSelectThreads;
+    static_assert(kMine == 2 || kMine == 4, "a thread reads its bins at once, on their own alignment");
     meet();  // (every CTA's counts)
     const int top = (1 << kLog) - kMine * (tid + 1);  // this thread's bins, from the highest ones down
     unsigned c[4] = {0u, 0u, 0u, 0u};
