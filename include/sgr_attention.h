@@ -272,7 +272,7 @@ int sgr_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch
  * keep their mass.  Scores as in sgr_kv_attention for few rows (queries to
  * 2^-22 of the row's largest), sums in FP32 in a fixed order.  batch->max_new has
  * to be an upper bound (a sequence with more rows is recorded, code 7, and its
- * later rows may be missing).  No two sequences of a call may share a page.
+ * later rows may be missing).  No page may occur twice in a call's tables.
  * workspace: sgr_kv_mass_workspace() bytes, 16-byte aligned, without initial
  * contents, one for each call that may overlap; NULL where 0 bytes are needed.
  */

@@ -390,6 +390,52 @@ def test_evict_stream_and_replay():
                 assert kept[b, h, :len(want)].tolist() == want
 
 
+def test_calls_on_two_streams_at_once():
+    """Attention, masses and evictions of two caches on two streams, many times
+    over, give the bits that they give one after the other."""
+    jobs = []
+    for k in range(2):
+        pr = ref.Problem(128, 64, 2, [1500, 700], [60 + k, 3], seed=50 + k)
+        keeps = [400, 300]
+        new_table, more = fresh_table(pr, keeps)
+        grown(pr, more)
+        q = (1.5 * pr.randn(pr.tokens, 8, 128)).bfloat16().cuda()
+        mass = torch.rand(pr.pages, 2, 64, generator=pr.g).cuda()
+        jobs.append((pr, q, mass, torch.tensor(keeps, dtype=torch.int32).cuda(), new_table.cuda(), torch.cuda.Stream()))
+
+    def run(job, stream):
+        pr, q, mass, keep, table, _ = job
+        cache, batch, mass = pr.cache(sgr), pr.batch(sgr), mass.clone()
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        work = [sgr.kv_attention_workspace(cache, batch, 8), sgr.kv_mass_workspace(cache, batch, 8)]
+        new_len = torch.empty(2, dtype=torch.int32, device="cuda")
+        kept = torch.full((2, 2, table.shape[1] * 64), -1, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+
+        def go():
+            sgr.sgr_kv_attention(cache, batch, q, out=out, lse=lse, window=900, sinks=4, workspace=work[0], stream=stream)
+            sgr.sgr_kv_mass(cache, batch, q, lse, mass, window=900, sinks=4, workspace=work[1], stream=stream)
+            sgr.sgr_kv_evict(cache, batch, mass, keep, table, first=4, recent=70, new_len=new_len, kept=kept, stream=stream)
+
+        return go, (out, lse, mass, kept, cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale.nan_to_num())
+
+    want = []
+    for job in jobs:
+        go, outs = run(job, None)
+        for _ in range(5):
+            go()
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs])
+    both = [run(job, job[5]) for job in jobs]
+    for _ in range(5):
+        for go, _ in both:
+            go()
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(both, want):
+        for x, y in zip(outs, w):
+            assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------- all together
 def test_server_steps_of_trees_masses_and_evictions():
     """A prompt, its mass, an eviction, a tree of drafted tokens over what stayed,
