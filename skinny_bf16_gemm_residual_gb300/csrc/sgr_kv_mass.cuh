@@ -5,16 +5,18 @@
 //     s = scale log2(e) q.k,   L = log2(e) lse
 //
 // With the rows' log-sum-exp known a position's sum needs its own key alone:
-// one pass over K, no maxima, and every sum within one thread.  As in the
-// attention kernel (sgr_kv_attn_few.cuh) the codes of 128 keys are the 128-row
-// operand of the FP8 tensor core as they are,
+// one pass over K and no maxima.  As in the attention kernel
+// (sgr_kv_attn_few.cuh) the codes of 128 keys are the 128-row operand of the FP8
+// tensor core as they are,
 //
 //     S^T [128 keys, 2 rows] = K Q^T
 //
 // with the rows' queries in two E4M3 parts b = hi + lo / 32 side by side (8
 // significant bits, all of a BF16 query, down to 2^-14 of its row's largest
 // and an absolute 2^-22 of it below).  Thread = key: it reads its lane of the
-// accumulator, adds the parts in FP32, and sums 2^(s - L) over the columns.
+// accumulator, adds the parts in FP32, and sums 2^(s - L) over the columns: in one
+// thread for products of 8 or 16 rows, in two for larger ones, a half of the
+// columns each, whose halves meet in shared memory once a tile.
 //
 // Bound: for few rows the keys' bytes, each read once (64 sequences of up to
 // 16384, 64 heads of 128 over 8, 607 MB: 97 us, 6.3 TB/s); one request's of 333
@@ -86,7 +88,7 @@ struct MassCtl {
   float kscale[S][8];  // of a stage's pages
   int page[S][8];      // (-1: not there)
   int flags[S], live[S][2];
-  float sum[Sh::kGroups][kAttnTile];  // of the groups but the first
+  float sum[Sh::kGroups > 1 ? 2 : 1][kAttnTile];  // of the second group, two tiles
   alignas(16) float qf[Q][Sh::kRows];  // a row's score factor
   alignas(16) float ql[Q][Sh::kRows];  // and -L (-inf: a row that counts for nothing)
   int qpos[Q][Sh::kRows];              // the last position that it sees, by itself
@@ -429,10 +431,14 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
         const float2 s2 = f2_parts(f2_add(sum[0], sum[1]));
         float w = s2.x + s2.y;
         if constexpr (Sh::kGroups > 1) {
-          if (group > 0) c.sum[group][tok] = w;
+          // Two buffers by the tile's parity: the second group, past the barrier of
+          // tile i, may be at its sums of tile i + 1 while a warp of the first still
+          // reads those of tile i; the barrier of tile i + 1, to which that warp comes
+          // after its read, stands before the sums of tile i + 2.
+          if (group > 0) c.sum[i & 1][tok] = w;
           __syncwarp();
           named_bar_sync(2, 32 * kWeigh);
-          if (group == 0) w += c.sum[1][tok];
+          if (group == 0) w += c.sum[i & 1][tok];
         }
         if (!live) w = 0.f;
         if (group > 0 || stray) {
