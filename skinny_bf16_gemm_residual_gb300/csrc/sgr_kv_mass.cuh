@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParam
   const AttnParams& p = mp.a;
   pdl_launch_dependents();
   pdl_wait();
-  const int t = blockIdx.x, h = blockIdx.y, b = blockIdx.z, pos = t * kAttnTile + threadIdx.x;
+  const int h = blockIdx.y, b = blockIdx.z, pos = (int)blockIdx.x * kAttnTile + (int)threadIdx.x;
   const KvSeq s = kv_seq(p.batch, p.cache.page_shift, b, nullptr);
   if (s.n == 0 || pos >= s.len) return;
   const long long at = mass_part<NT>(mp, b, s.row0, 0, h) + pos, step = (long long)p.cache.heads * mp.tiles * kAttnTile;
@@ -483,8 +483,9 @@ __global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParam
 #pragma unroll 4
   for (int j = 0; j * NT < s.n * p.group; ++j) {
     const AttnItem it = attn_item<NT, true>(p, s, j);
-    const TileMap tm(it.tlo, p.sinks);
-    if (t >= it.tb || (t < tm.tw && t >= tm.tw - tm.gap)) continue;  // a tile that its rows do not see
+    // (Position by position: a tile that the rows see a part of may hold pages that
+    // none of them sees, whose table entries may be anything.)
+    if (pos >= it.thi || (pos < it.tlo && pos >= p.sinks)) continue;
     w += mp.part[at + j * step];
     any = true;
   }

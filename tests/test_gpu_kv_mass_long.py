@@ -73,3 +73,37 @@ def test_mass_of_many_tiles_a_cta(dim, new, window, sinks, tree):
     assert lse.isfinite().all() and math.isfinite(float(got.sum()))
     mref.check_mass(got, *mref.mass(before.double(), q, pr.values(0), lse.cpu(), pr.block_table, pr.seq_len, pr.q_start, page,
                                     dim ** -0.5, window, sinks, trees))
+
+
+@pytest.mark.parametrize("page,window,sinks", [(16, 70, 5), (32, 1, 33), (64, 300, 0)])
+@pytest.mark.parametrize("entry", ["another page", "none"])
+def test_mass_follows_no_entry_of_a_page_that_no_row_sees(page, window, sinks, entry):
+    """Several row tiles under a window: entries between the sinks and the first
+    window name a page that is another's (its masses are -0.0, which an addition of
+    zero would make +0.0), or none (which would be recorded)."""
+    new = 180
+    pr = ref.Problem(64, page, 2, [1000, 700], [new, new - 1], seed=window, extra_pages=3)
+    other = pr.pages - 1
+    while other in pr.block_table.tolist()[0] or other in pr.block_table.tolist()[1]:
+        other -= 1
+    table = pr.block_table.clone()
+    hidden = 0
+    for b in range(2):
+        first = pr.lens[b] - pr.new[b]
+        for block in range(pr.max_pages):
+            if block * page >= sinks and (block + 1) * page <= first - window + 1:
+                table[b, block] = other if entry == "another page" else -1
+                hidden += 1
+    assert hidden > 4
+    q = (1.5 * pr.randn(pr.tokens, 4, 64)).bfloat16()
+    batch = sgr.KvBatch(table.cuda(), pr.seq_len.cuda(), pr.q_start.cuda(), tokens=pr.tokens, max_new=new)
+    cache = pr.cache(sgr)
+    lse = torch.empty(pr.tokens, 4, device="cuda")
+    sgr.sgr_kv_attention(cache, batch, q.cuda(), lse=lse, window=window, sinks=sinks)
+    assert sgr.kv_mass_workspace(cache, batch, 4).numel() > 0
+    before = torch.rand(pr.pages, 2, page, generator=pr.g)
+    before[other] = -0.0
+    got = sgr.sgr_kv_mass(cache, batch, q.cuda(), lse, before.cuda(), window=window, sinks=sinks)
+    assert (got[other].signbit() & (got[other] == 0)).all()
+    mref.check_mass(got, *mref.mass(before.double(), q, pr.values(0), lse.cpu(), pr.block_table, pr.seq_len, pr.q_start, page,
+                                    0.125, window, sinks))
