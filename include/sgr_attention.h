@@ -270,9 +270,12 @@ int sgr_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch
  * are set, not added to: a page needs no clearing before it is used.  Masked
  * weights have no part, whatever the position holds; positions that no row sees
  * keep their mass.  Scores as in sgr_kv_attention for few rows (queries to
- * 2^-22 of the row's largest), sums in FP32 in a fixed order.  batch->max_new has
- * to be an upper bound (a sequence with more rows is recorded, code 7, and its
- * later rows may be missing).  No page may occur twice in a call's tables.
+ * 2^-22 of the row's largest), sums in FP32, of a sequence in a fixed order.
+ * batch->max_new has to be an upper bound (a sequence with more rows is
+ * recorded, code 7, and its later rows may be missing).  Sequences may share
+ * pages of older positions (a common prompt): such a position gets the weights
+ * of all of them, added in any order (its last bits may differ from run to
+ * run).  A page of new positions may occur once in a call's tables.
  * workspace: sgr_kv_mass_workspace() bytes, 16-byte aligned, without initial
  * contents, one for each call that may overlap; NULL where 0 bytes are needed.
  */

@@ -388,7 +388,9 @@ def sgr_kv_mass(cache: KvCache, batch: KvBatch, q, lse, mass, scale: float | Non
     the new tokens' queries [tokens, q_heads, head_dim] give each cached
     position, summed over the heads of its key/value head; the new tokens' own
     positions are set.  lse: what sgr_kv_attention wrote for the same queries,
-    scale and masks.  Returns mass."""
+    scale and masks.  Older positions of pages that sequences share get the
+    weights of all of them, added in any order; a page of new positions may
+    occur once in the block table.  Returns mass."""
     index = cache.index
     shape = (batch.tokens, _shape3(q, "q")[1], cache.head_dim)
     hq = _heads(q, "q", shape, index)

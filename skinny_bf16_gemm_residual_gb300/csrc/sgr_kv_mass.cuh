@@ -28,9 +28,10 @@
 // Rows that share a key/value head go in products of up to 64.  Up to 128 of
 // them, their queries all in shared memory, meet a tile of keys while it is
 // there (it is read once); more are several row tiles, whose sums go to the
-// workspace and are added in order by a second kernel: no atomics on one
-// address from two places, the same bits on every run.  Every CTA takes the
-// same number of (row tile, key tile) units (attn_walk).
+// workspace and are added in order by a second kernel.  A sequence adds once to
+// each of its positions: the same bits on every run, but for positions of pages
+// that several sequences share, whose sums are added in any order.  Every CTA
+// takes the same number of (row tile, key tile) units (attn_walk).
 //
 // Roles: four warps weigh (thread = key; eight for products of 32 rows or more,
 // half of the columns each), one walks the work and loads pages, one issues the
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(MassShape<D, NT>::kThreads, 2)
           if (pos >= g.first)
             *at = w;
           else
-            atomicAdd(at, w);  // (the only one to this address: no read to wait for)
+            atomicAdd(at, w);  // (no read to wait for; the only one to this address but for pages that sequences share)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&c.empty[slot]));
@@ -492,7 +493,10 @@ __global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParam
   const int page = any ? p.batch.table[(long long)b * p.batch.table_stride + (pos >> p.cache.page_shift)] : -1;
   if (page < 0 || page >= p.cache.num_pages) return;  // (recorded by the kernel before)
   float* to = mp.mass + (long long)page * mp.page_stride + (long long)h * mp.head_stride + (pos & ((1 << p.cache.page_shift) - 1));
-  *to = pos >= s.len - s.n ? w : *to + w;
+  if (pos >= s.len - s.n)
+    *to = w;
+  else
+    atomicAdd(to, w);  // (other sequences may share the page; otherwise the only one to this address)
 }
 
 }  // namespace sgr

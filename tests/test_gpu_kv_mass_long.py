@@ -107,3 +107,28 @@ def test_mass_follows_no_entry_of_a_page_that_no_row_sees(page, window, sinks, e
     assert (got[other].signbit() & (got[other] == 0)).all()
     mref.check_mass(got, *mref.mass(before.double(), q, pr.values(0), lse.cpu(), pr.block_table, pr.seq_len, pr.q_start, page,
                                     0.125, window, sinks))
+
+
+@pytest.mark.parametrize("new", [1, 9, 100])  # rows a head: 4, 36, 400 (the last: several row tiles, joined)
+def test_mass_of_shared_pages(new):
+    """Twelve sequences with a common prompt, and pages of their own behind it: a
+    shared position gets the weights of all.  The error allowed is the sum of the
+    sequences' own."""
+    page, heads, hk, shared, count = 32, 8, 2, 20, 12
+    lens = [shared * page + r for r in range(new, new + 7 * count, 7)]
+    pr = ref.Problem(128, page, hk, lens, [new] * count, seed=new)
+    pr.block_table[:, :shared] = pr.block_table[0, :shared]
+    q = (1.5 * pr.randn(pr.tokens, heads, 128)).bfloat16()
+    cache, batch = pr.cache(sgr), pr.batch(sgr)
+    lse = torch.empty(pr.tokens, heads, device="cuda")
+    sgr.sgr_kv_attention(cache, batch, q.cuda(), lse=lse)
+    before = torch.rand(pr.pages, hk, page, generator=pr.g)
+    want, tol = before.double(), torch.zeros_like(before, dtype=torch.float64)
+    for b in range(count):
+        rows = slice(new * b, new * (b + 1))
+        want, more = mref.mass(want, q[rows], pr.values(0), lse[rows].cpu(), pr.block_table[b:b + 1], pr.seq_len[b:b + 1],
+                               torch.tensor([0, new]), page, 128 ** -0.5)
+        tol += more
+    for _ in range(5):
+        got = sgr.sgr_kv_mass(cache, batch, q.cuda(), lse, before.cuda())
+        mref.check_mass(got, want, tol)
