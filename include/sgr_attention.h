@@ -223,8 +223,9 @@ int sgr_kv_append(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sg
  * The same, with row r's query and key rotated to positions[r] instead of its
  * place in the cache: drafted tokens of a tree stand at their depth, and new
  * tokens of a sequence that has lost positions (sgr_kv_evict) behind all that
- * it ever had.  A negative position counts as 0 and records code 7.  positions
- * NULL: as sgr_kv_append.
+ * it ever had.  A negative position counts as 0 and records code 7; without a
+ * rotation table positions are not looked at.  They may share no memory with
+ * q_out or the cache (SGR_ERR_ALIAS).  positions NULL: as sgr_kv_append.
  */
 int sgr_kv_append_at(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_heads* q, const sgr_heads* k,
                      const sgr_heads* v, const sgr_heads* q_out, const sgr_norm_rope* nr, const int* positions,

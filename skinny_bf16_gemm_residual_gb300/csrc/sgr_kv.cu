@@ -182,6 +182,12 @@ int check_batch(const sgr_kv_batch* b) {
 
 bool empty(const sgr_kv_batch& b) { return b.batch == 0 || b.tokens == 0; }
 
+// n numbers of 4 bytes.
+Extent words_extent(const void* p, long long n) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + 4 * (uintptr_t)(n > 0 ? n : 0)};
+}
+
 // Whether memory and the cache (codes or scales) share bytes.
 bool touches_cache(Extent e, const sgr_kv_cache& c) {
   if (c.num_pages == 0) return false;
@@ -213,12 +219,16 @@ int validate_append(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_head
   if ((rc = check_heads(k, c->heads, dim, false)) != SGR_OK) return rc;
   if ((rc = check_heads(v, c->heads, dim, false)) != SGR_OK) return rc;
   if (touches_cache(*k, *c, b->tokens) || touches_cache(*v, *c, b->tokens)) return SGR_ERR_ALIAS;
+  // (blocks write while others still read positions)
+  const Extent at = words_extent(positions, positions ? b->tokens : 0);
+  if (touches_cache(at, *c)) return SGR_ERR_ALIAS;
   if (q) {
     if ((rc = check_heads(q, q->heads, dim, false)) != SGR_OK) return rc;
     if ((rc = check_heads(qo, q->heads, dim, true)) != SGR_OK) return rc;
     if ((rc = check_rows(*qo, b->tokens, dim)) != SGR_OK) return rc;
     if (!same_rows(*q, *qo) && heads_overlap(*q, *qo, b->tokens, dim)) return SGR_ERR_ALIAS;
     if (heads_overlap(*k, *qo, b->tokens, dim) || heads_overlap(*v, *qo, b->tokens, dim)) return SGR_ERR_ALIAS;
+    if (overlap(at, heads_extent(*qo, b->tokens, dim))) return SGR_ERR_ALIAS;
     if (touches_cache(*q, *c, b->tokens) || touches_cache(*qo, *c, b->tokens)) return SGR_ERR_ALIAS;
   }
   return SGR_OK;
@@ -329,16 +339,12 @@ int validate_evict(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_kv_ma
   if (ev->table_stride > kMaxStride) return SGR_ERR_UNSUPPORTED;
   Extent e[3];  // what is written: masses, positions, lengths
   if ((rc = check_masses(mass, *c, &e[0])) != SGR_OK) return rc;
-  auto of = [](const void* p, long long n) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Extent{lo, lo + 4 * (uintptr_t)(n > 0 ? n : 0)};
-  };
   const long long rows = b->batch - 1;
-  e[1] = of(ev->kept, (long long)b->batch * c->heads * ev->max_pages * c->page_size);
-  e[2] = of(ev->new_len, b->batch);
-  const Extent in[4] = {of(b->seq_len, b->batch), of(ev->keep, b->batch),
-                        of(b->block_table, b->max_pages > 0 ? rows * b->table_stride + b->max_pages : 0),
-                        of(ev->table, ev->max_pages > 0 ? rows * ev->table_stride + ev->max_pages : 0)};
+  e[1] = words_extent(ev->kept, (long long)b->batch * c->heads * ev->max_pages * c->page_size);
+  e[2] = words_extent(ev->new_len, b->batch);
+  const Extent in[4] = {words_extent(b->seq_len, b->batch), words_extent(ev->keep, b->batch),
+                        words_extent(b->block_table, b->max_pages > 0 ? rows * b->table_stride + b->max_pages : 0),
+                        words_extent(ev->table, ev->max_pages > 0 ? rows * ev->table_stride + ev->max_pages : 0)};
   for (int i = 0; i < 3; ++i) {
     for (const Extent& x : in)
       if (overlap(e[i], x)) return SGR_ERR_ALIAS;
