@@ -152,7 +152,8 @@ typedef struct {
  *           seq_len - n + (bits set) - 1 sees.  Bits from n on are not looked
  *           at.  NULL: not a tree.  tree_words: words of a row, at least
  *           max_new / 64 rounded up.
- * A padding row (its place negative) sees nothing, and no row sees one.
+ * A padding row (its place negative) sees nothing, and no row sees one.  The
+ * words of tree may share no memory with what a call writes (SGR_ERR_ALIAS).
  */
 typedef struct {
   const uint64_t* tree; /* [tokens, tree_words], 8-byte aligned */

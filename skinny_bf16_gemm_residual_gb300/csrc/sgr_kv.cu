@@ -246,6 +246,12 @@ int check_mask(const sgr_kv_mask* m, const sgr_kv_batch& b) {
   return SGR_OK;
 }
 
+// The words of a mask's trees, which are read while outputs are written.
+Extent tree_extent(const sgr_kv_mask* m, const sgr_kv_batch& b) {
+  if (!m || !m->tree) return {0, 0};
+  return words_extent(m->tree, 2 * ((b.tokens - 1) * m->tree_stride + m->tree_words));
+}
+
 int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, const sgr_heads* out,
                        const float* lse, float scale, const sgr_kv_mask* mask) {
   int rc;
@@ -261,12 +267,14 @@ int validate_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_h
   if ((rc = check_rows(*out, b->tokens, c->head_dim)) != SGR_OK) return rc;
   if (heads_overlap(*q, *out, b->tokens, c->head_dim)) return SGR_ERR_ALIAS;
   if (touches_cache(*out, *c, b->tokens)) return SGR_ERR_ALIAS;
+  const Extent tree = tree_extent(mask, *b);
+  if (overlap(tree, heads_extent(*out, b->tokens, c->head_dim))) return SGR_ERR_ALIAS;
   if (lse) {
     if (!aligned(lse, 4)) return SGR_ERR_ALIGN;
     const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
     const Extent e{lo, lo + 4 * (uintptr_t)b->tokens * q->heads};
     if (overlap(e, heads_extent(*q, b->tokens, c->head_dim)) || overlap(e, heads_extent(*out, b->tokens, c->head_dim)) ||
-        touches_cache(e, *c))
+        overlap(e, tree) || touches_cache(e, *c))
       return SGR_ERR_ALIAS;
   }
   return SGR_OK;
@@ -314,7 +322,8 @@ int validate_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   Extent e;
   if ((rc = check_masses(mass, *c, &e)) != SGR_OK) return rc;
   const uintptr_t lo = reinterpret_cast<uintptr_t>(lse);
-  if (overlap(e, heads_extent(*q, b->tokens, c->head_dim)) || overlap(e, {lo, lo + 4 * (uintptr_t)b->tokens * q->heads}))
+  if (overlap(e, heads_extent(*q, b->tokens, c->head_dim)) || overlap(e, {lo, lo + 4 * (uintptr_t)b->tokens * q->heads}) ||
+      overlap(e, tree_extent(mask, *b)))
     return SGR_ERR_ALIAS;
   return SGR_OK;
 }
