@@ -149,9 +149,10 @@ typedef struct {
  *           tree[row * tree_stride + j / 64] for the j-th (itself among them
  *           only if set; a window does not count between them), and of the
  *           positions before the new ones those that a row at position
- *           seq_len - n + (bits set) - 1 sees.  Bits from n on are not looked
- *           at.  NULL: not a tree.  tree_words: words of a row, at least
- *           max_new / 64 rounded up.
+ *           max(seq_len - n, 0) + max(bits set, 1) - 1 sees: a row without any
+ *           stands where the first new token does.  Bits from n on are not
+ *           looked at, nor those of padding rows.  NULL: not a tree.
+ *           tree_words: words of a row, at least max_new / 64 rounded up.
  * A padding row (its place negative) sees nothing, and no row sees one.  The
  * words of tree may share no memory with what a call writes (SGR_ERR_ALIAS).
  */
