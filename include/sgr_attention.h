@@ -270,7 +270,10 @@ int sgr_kv_attention_masked(const sgr_kv_cache* cache, const sgr_kv_batch* batch
  *
  * over the rows that see t (mask: as sgr_kv_attention_masked; lse: what that
  * call wrote for the same q, scale and mask).  The new tokens' own positions
- * are set, not added to: a page needs no clearing before it is used.  Masked
+ * are set, not added to: a page needs no clearing before it is used where this
+ * call follows every append.  A position appended without it has the mass that
+ * its place had, of the page's last user or of a draft (NaN or large, perhaps,
+ * and then sgr_kv_evict keeps it): set it to zero at the append.  Masked
  * weights have no part, whatever the position holds; positions that no row sees
  * keep their mass.  Scores as in sgr_kv_attention for few rows (queries to
  * 2^-22 of the row's largest), sums in FP32, of a sequence in a fixed order.

@@ -387,7 +387,8 @@ def sgr_kv_mass(cache: KvCache, batch: KvBatch, q, lse, mass, scale: float | Non
     """Add to mass [pages, heads, page_size] (float32) the attention weight that
     the new tokens' queries [tokens, q_heads, head_dim] give each cached
     position, summed over the heads of its key/value head; the new tokens' own
-    positions are set.  lse: what sgr_kv_attention wrote for the same queries,
+    positions are set.  A position that is appended without this call keeps what
+    its place had: set it to zero, an eviction would go by it.  lse: what sgr_kv_attention wrote for the same queries,
     scale and masks.  Older positions of pages that sequences share get the
     weights of all of them, added in any order; a page of new positions may
     occur once in the block table.  Returns mass."""

@@ -1,8 +1,11 @@
 """What the header says of the attention operators' arguments where no other test
 looks, on the GPU against the header's own formulas."""
+import random
+
 import pytest
 import torch
 
+import kv_mask_ref as mref
 import kv_ref as ref
 import skinny_bf16_gemm_residual_gb300 as sgr
 
@@ -91,3 +94,77 @@ def test_tree_rows_without_bits_under_windows(window, sinks, flags):
         assert torch.equal(got[:, 0] != 0, see.any(0)) and torch.equal(got[:, 1] != 0, see.any(0))
         row += n
     ref.check_attention(out, want, mag)
+
+
+def test_masses_where_only_some_steps_are_weighed():
+    """Pages that hold NaN masses of their last user; a prompt in two chunks of which
+    the second is weighed, a weighed tree, its accepted branch and a decode step that
+    are not, a weighed decode step, and an eviction: with the new positions of the
+    steps that are not weighed set to zero, all masses are the definition's."""
+    heads, hk, dim, page, lens = 8, 2, 64, 16, [150, 70]
+    g = torch.Generator().manual_seed(2)
+    cache = sgr.KvCache.empty(60, hk, page, dim)
+    mass = cache.zero_mass()
+    mass.fill_(float("nan"))
+    rope = sgr.RopeNorm(ref.rope_table(400, dim).cuda())
+    order = torch.randperm(60, generator=g).int()
+    table, host = order[:24].view(2, 12).cuda(), order[:24].view(2, 12).long()
+    want = torch.zeros(mass.shape, dtype=torch.float64)
+    tol = torch.zeros_like(want)
+
+    def step(length, new, weighed, trees=None, positions=None, rows=None):
+        """Appends `new` tokens up to `length` positions; weighs them or clears their masses."""
+        nonlocal want, tol
+        n = sum(new)
+        start = torch.tensor([0, new[0], n], dtype=torch.int32)
+        batch = sgr.KvBatch(table, torch.tensor(length, dtype=torch.int32).cuda(), start.cuda(), tokens=n, max_new=max(new))
+        q, k, v = torch.randn(n, heads + 2 * hk, dim, generator=g).bfloat16().cuda().split((heads, hk, hk), 1)
+        if rows is not None:
+            k, v = rows[0][rows[2]], rows[1][rows[2]]
+        q = sgr.sgr_kv_append(cache, batch, k, v, rope, q=q, positions=positions)
+        lse = torch.empty(n, heads, device="cuda")
+        words = torch.cat([mref.tree_words(t, 1) for t in trees]).cuda() if trees else None
+        sgr.sgr_kv_attention(cache, batch, q, tree=words, lse=lse)
+        places = [(host[b, t // page], t % page) for b in range(2) for t in range(length[b] - new[b], length[b])]
+        if weighed:
+            sgr.sgr_kv_mass(cache, batch, q, lse, mass, tree=words)
+            kk = (cache.k.float() * cache.k_scale[:, :, None, None]).double().cpu()
+            want, more = mref.mass(want, q.cpu(), kk, lse.cpu(), host, length, start, page, dim ** -0.5, trees=trees)
+            for p, at in places:
+                tol[p, :, at] = 0.0
+            tol += more
+        else:
+            for p, at in places:
+                mass[p, :, at] = 0.0
+                want[p, :, at] = tol[p, :, at] = 0.0
+        return k, v
+
+    step([90, 30], [90, 30], False)
+    step(lens, [60, 40], True)
+    r = random.Random(5)
+    trees = [mref.random_tree(7, r) for _ in range(2)]
+    depth = torch.tensor([lens[b] + len(path) - 1 for b in range(2) for path in trees[b]], dtype=torch.int32).cuda()
+    k, v = step([lens[0] + 7, lens[1] + 7], [7, 7], True, trees, depth)
+    paths = [max(t, key=len) for t in trees]
+    count = [len(p) for p in paths]
+    rows = torch.tensor([7 * b + j for b in range(2) for j in paths[b]]).cuda()
+    lens = [lens[b] + count[b] for b in range(2)]
+    step(lens, count, False, positions=depth[rows], rows=(k, v, rows))
+    lens = [n + 1 for n in lens]
+    step(lens, [1, 1], False)
+    lens = [n + 1 for n in lens]
+    step(lens, [1, 1], True)
+    masses = mass.double().cpu()
+    for b in range(2):
+        t = torch.arange(lens[b])
+        pages = host[b][t // page]
+        got, w, e = masses[pages, :, t % page], want[pages, :, t % page], tol[pages, :, t % page]
+        assert ((got - w).abs() <= e).all() and (w > 0).any()
+    keep = torch.tensor([64, 40], dtype=torch.int32).cuda()
+    batch = sgr.KvBatch(table, torch.tensor(lens, dtype=torch.int32).cuda())
+    new_len, kept = sgr.sgr_kv_evict(cache, batch, mass, keep, order[30:38].view(2, 4).cuda(), first=2, recent=4)
+    for b in range(2):
+        t = torch.arange(lens[b])
+        for h in range(hk):
+            stay = mref.chosen(masses[host[b][t // page], h, t % page].tolist(), int(keep[b]), 2, 4)
+            assert kept[b, h, :int(new_len[b])].tolist() == stay
