@@ -292,7 +292,8 @@ int sgr_kv_mass(const sgr_kv_cache* cache, const sgr_kv_batch* batch, const sgr_
 /* Workspace that sgr_kv_mass needs for this batch and `q_heads` query heads, in
  * bytes: 0 where a key/value head has at most 128 rows of a sequence (max_new
  * times the group), else 4 bytes a position and key/value head for every 128 of
- * them.  Depends on the sizes in the structures alone. */
+ * them.  Depends on the sizes in the structures alone.  SGR_ERR_UNSUPPORTED for
+ * sizes that sgr_kv_mass refuses. */
 int sgr_kv_mass_workspace(const sgr_kv_cache* cache, const sgr_kv_batch* batch, int q_heads, int64_t* bytes);
 
 /*

@@ -692,10 +692,10 @@ MassPlan mass_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   const long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
   const long long row_tiles = m.part ? (long long)b.tokens * group / m.nt + b.batch : b.batch;  // at most
   const long long units = c.heads * row_tiles * (tiles + 1);
-  m.fits = units < (1LL << 31) && tiles < (1 << 24) && c.heads * row_tiles * tiles < (1LL << 31);
+  m.fits = units < (1LL << 31) && tiles < (1 << 24) && (!m.part || b.batch <= 65535);
   m.tiles = (int)tiles;
   m.grid = (int)(units < 2LL * sms ? units : 2LL * sms);
-  m.bytes = m.part ? row_tiles * c.heads * tiles * sgr::kAttnTile * 4LL : 0;
+  m.bytes = m.part && m.fits ? row_tiles * c.heads * tiles * sgr::kAttnTile * 4LL : 0;
   return m;
 }
 
@@ -707,7 +707,7 @@ int run_mass(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads* q, c
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
   const MassPlan m = mass_plan(dev->sms, *c, *b, q->heads);
-  if (!m.fits || (m.part && b->batch > 65535)) return SGR_ERR_UNSUPPORTED;
+  if (!m.fits) return SGR_ERR_UNSUPPORTED;
   if (m.part) {
     if (!workspace) return SGR_ERR_NULL;
     if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
@@ -888,7 +888,11 @@ int sgr_kv_mass_workspace(const sgr_kv_cache* cache, const sgr_kv_batch* batch, 
   int rc;
   if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
   if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
-  *bytes = mass_plan(1, *cache, *batch, q_heads).bytes;
+  // (as the call: what it refuses might not fit 64 bits)
+  if (q_heads > kMaxHeads || q_heads / cache->heads > kMaxGroup) return SGR_ERR_UNSUPPORTED;
+  const MassPlan m = mass_plan(1, *cache, *batch, q_heads);
+  if (!m.fits && !empty(*batch)) return SGR_ERR_UNSUPPORTED;
+  *bytes = m.bytes;
   return SGR_OK;
 }
 
