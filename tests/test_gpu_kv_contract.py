@@ -168,3 +168,19 @@ def test_masses_where_only_some_steps_are_weighed():
         for h in range(hk):
             stay = mref.chosen(masses[host[b][t // page], h, t % page].tolist(), int(keep[b]), 2, 4)
             assert kept[b, h, :int(new_len[b])].tolist() == stay
+
+
+def test_numbers_past_32_bits_are_refused():
+    pr = ref.Problem(64, 16, 1, [20], [1])
+    cache, batch, q = pr.cache(sgr), pr.batch(sgr), pr.randn(1, 2, 64).bfloat16().cuda()
+    lse, mass = torch.zeros(1, 2, device="cuda"), pr.cache(sgr).zero_mass()
+    keep, to = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for big in (1 << 31, (1 << 32) + 5):
+        for call in (lambda: sgr.sgr_kv_attention(cache, batch, q, window=big),
+                     lambda: sgr.sgr_kv_attention(cache, batch, q, window=big, lse=lse),
+                     lambda: sgr.sgr_kv_attention(cache, batch, q, window=4, sinks=big),
+                     lambda: sgr.sgr_kv_mass(cache, batch, q, lse, mass, window=big),
+                     lambda: sgr.sgr_kv_evict(cache, batch, mass, keep, to, first=big),
+                     lambda: sgr.sgr_kv_evict(cache, batch, mass, keep, to, recent=big)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()

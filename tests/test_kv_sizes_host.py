@@ -28,3 +28,14 @@ def test_mass_workspace_refuses_what_the_call_refuses(kw, ckw, q_heads):
 def test_mass_workspace_of_nothing():
     assert mass_workspace(cache(), batch(tokens=0, batch=0), 4) == (sgr.SGR_OK, 0)
     assert mass_workspace(cache(), batch(tokens=70000, max_new=32, batch=70000, q_start=BASE + 112 * GIB), 16) == (sgr.SGR_OK, 0)
+
+
+def test_numbers_past_32_bits_are_value_errors():
+    from skinny_bf16_gemm_residual_gb300 import attention
+
+    for window, sinks in ((1 << 31, 0), (0, 1 << 31), (1 << 70, 4), (-(1 << 31) - 1, 0), (3.5, 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            attention._mask(None, window, sinks, None, 0)
+    assert len(attention._mask(None, (1 << 31) - 1, (1 << 31) - 1, None, 0)) == 32
+    with pytest.raises(ValueError, match="first and recent"):
+        attention._pack(attention._pack_eviction, "first and recent", 0, 0, 0, 0, 1, 1, 1 << 31, 0, 0)
