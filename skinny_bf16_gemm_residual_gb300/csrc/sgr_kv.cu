@@ -539,18 +539,16 @@ struct AttnPlan {
   bool reuse;       // whether a sequence may have several row tiles
   bool fits;        // 31 bits hold the number of units
   int64_t bytes;    // workspace
+  int64_t any_window;  // workspace for the same sizes under any window
 };
 
-// mask: NULL for the workspace, which depends on the sizes alone and is enough
-// for any mask (a window makes the tiles of a sequence fewer, and by that perhaps
-// the row tiles smaller, of which more are under way).
 AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags,
-                   const sgr_kv_mask* mask) {
+                   const sgr_kv_mask& mask) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
   long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
-  if (mask && mask->window > 0) {
-    const long long seen = ((long long)mask->window + b.max_new) / sgr::kAttnTile + 2 + (mask->sinks + sgr::kAttnTile - 1LL) / sgr::kAttnTile;
+  if (mask.window > 0) {
+    const long long seen = ((long long)mask.window + b.max_new) / sgr::kAttnTile + 2 + (mask.sinks + sgr::kAttnTile - 1LL) / sgr::kAttnTile;
     if (seen < tiles) tiles = seen;
   }
   auto row_tiles = [&](int nt) {  // at most
@@ -571,14 +569,22 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
     }
   // The 256-row kernel takes some 1.25 times a 32-row unit's time for eight times
   // the rows, but 8 units' time to begin and end.  Measured, small tiles against
-  // 256 rows, 28 heads of 128 over 4: 19.9 and 23.7 us (8 sequences of 3000, 35
-  // rows a head each), 133 and 104 (96 of them), 21.3 and 24.0 (4 of 3000, 126
-  // rows), 53 and 30 (16 of them), 30.0 and 26.1 (8 of 4000, 112 rows), 25.5 and
-  // 27.4 (one of 2000, 700 rows), 119 and 57 (one of 30000, 448 rows), 192 and 99
-  // (32 of 9000, 112 rows), but also 32.2 and 28.5 (24 of 1500, 63 rows); 32 heads
-  // of 64 over 8: 62.7 and 49.3 (16 of 5000, 48 rows), 180 and 131 (32 of 9000, 36
-  // rows), 22.1 and 19.2 (4 of 1500, 160 rows).
-  const bool gains = (double)tiles * ((double)row_tiles(32) - 1.25 * (double)row_tiles(sgr::kRowsNT)) > 8.0 * sms;
+  // 256 rows, one sequence of the length and the others of 1 to it, 28 heads of 128
+  // over 4: 118 and 96 us (96 of 3000, 35 rows a head each), 22.4 and 23.7 (4 of
+  // 3000, 126 rows), 57 and 31 (16 of 3000, 126 rows), 34 and 26 (8 of 4000, 112
+  // rows), 25.2 and 27.7 (one of 2000, 700 rows), 117 and 57 (one of 30000, 448
+  // rows), 211 and 92 (32 of 9000, 112 rows; 306 and 133 where all are 9000 long),
+  // 64 and 52 (64 of 1500, 63 rows), but also 30.8 and 28.8 (24 of 1500, 63 rows);
+  // 32 heads of 64 over 8: 57 and 41 (16 of 5000, 48 rows), 178 and 134 (32 of 9000,
+  // 36 rows; 285 and 220 where all are 9000 long), 24.3 and 19.9 (4 of 1500, 160
+  // rows), 54 and 37 (3 of 20000, 96 rows).
+  // It also sees a query's small elements in fewer bits (sgr_attention.h).  Calls
+  // over all positions up to a row's own, or the last of them, keep the few-row
+  // kernel's longer, where it gives up to a third of its speed: rows of 36 to 64 in
+  // the figures above, and the 160 rows.  (So a log-sum-exp changes no output.)
+  const bool plain = !mask.tree && !(mask.window > 0 && mask.sinks > 0);
+  const double unit = !plain ? 1.25 : c.head_dim == 64 ? 2.4 : 1.75, begin = plain ? 12.0 : 8.0;
+  const bool gains = (double)tiles * ((double)row_tiles(32) - unit * (double)row_tiles(sgr::kRowsNT)) > begin * sms;
   if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);
@@ -593,13 +599,25 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   a.grid = (int)(units < ctas ? units : ctas);
   a.reuse = rows > a.nt;
   auto bytes = [&](long long grid, int nt) { return grid * (2LL * nt * (c.head_dim * 4LL + 8) + (long long)sizeof(sgr::AttnPiece)); };
-  a.bytes = bytes(a.grid, a.nt);
+  a.bytes = a.any_window = bytes(a.grid, a.nt);
   for (int nt : {8, 16, 24, 32}) {
     const long long most = row_tiles(nt) * (tiles + 1), held = nt >= 32 ? sms : 2LL * sms;
     const int64_t need = bytes(most < held ? most : held, nt);
-    if (!mask && nt < a.nt && need > a.bytes) a.bytes = need;
+    if (nt < a.nt && need > a.any_window) a.any_window = need;
   }
   return a;
+}
+
+// The workspace depends on the sizes alone and is enough for any mask: with a
+// tree or without, and with windows, which make the tiles of a sequence fewer,
+// and by that perhaps the row tiles smaller, of which more are under way.
+int64_t attn_workspace(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_heads, unsigned flags) {
+  sgr_kv_mask mask = {};
+  const int64_t plain = attn_plan(sms, c, b, q_heads, flags, mask).any_window;
+  const uint64_t some = 0;
+  mask.tree = &some;  // (not looked at)
+  const int64_t tree = attn_plan(sms, c, b, q_heads, flags, mask).any_window;
+  return plain > tree ? plain : tree;
 }
 
 // Cache codes as a 4-D tensor (element, position in the page, head, page).
@@ -652,7 +670,7 @@ int run_attention(const sgr_kv_cache* c, const sgr_kv_batch* b, const sgr_heads*
   if (!aligned(workspace, 16)) return SGR_ERR_ALIGN;
   KvDevice* dev;
   if ((rc = current_kv_device(&dev)) != SGR_OK) return rc;
-  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads, flags, mask);
+  const AttnPlan a = attn_plan(dev->sms, *c, *b, q->heads, flags, mask ? *mask : sgr_kv_mask{});
   if (!a.fits || workspace_bytes < a.bytes) return SGR_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   // (a cache without pages: the maps are never used)
@@ -873,7 +891,7 @@ int sgr_kv_attention_workspace(int device, const sgr_kv_cache* cache, const sgr_
   if ((rc = check_cache(cache)) != SGR_OK || (rc = check_batch(batch)) != SGR_OK) return rc;
   if (q_heads < 1 || q_heads % cache->heads) return SGR_ERR_SHAPE;
   if ((rc = sgr::kv_init_device(device)) != SGR_OK) return rc;
-  *bytes = attn_plan(g_kv[device].sms, *cache, *batch, q_heads, flags, nullptr).bytes;
+  *bytes = attn_workspace(g_kv[device].sms, *cache, *batch, q_heads, flags);
   return SGR_OK;
 }
 

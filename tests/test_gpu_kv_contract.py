@@ -184,3 +184,38 @@ def test_numbers_past_32_bits_are_refused():
                      lambda: sgr.sgr_kv_evict(cache, batch, mass, keep, to, recent=big)):
             with pytest.raises(ValueError, match="32 bits"):
                 call()
+
+
+def test_plain_calls_of_medium_row_counts_keep_small_elements():
+    """A query's elements far below its largest keep their 8 bits (multiples of
+    2^-20 from 2^-14 to 2^-12, beside a 1 that meets zeros), where all scores come
+    from them, in a plain call with 160 rows a head; with or without a log-sum-exp.
+    Scores are then good to the 32-bit sums' 2^-20 of them, far below the allowed
+    2^-7 of sum p |v|; steps of 2^-18 would move scores of some 4 by a tenth."""
+    pr = ref.Problem(64, 64, 8, [1500] * 4, [40] * 4, seed=2)
+    for b in pr.block_table:
+        pr.codes[0][b.long(), :, :, 0] = 0
+    small = torch.randint(64, 256, (160, 32, 64), generator=pr.g) * (2 * torch.randint(0, 2, (160, 32, 64), generator=pr.g) - 1)
+    q = (small * 2.0 ** -20).bfloat16()
+    q[:, :, 0] = 1.0
+    assert (q[:, :, 1:].float() == small[:, :, 1:] * 2.0 ** -20).all()
+    cache, batch = pr.cache(sgr), pr.batch(sgr)
+    scale = 2.0 ** 11
+    out = sgr.sgr_kv_attention(cache, batch, q.cuda(), scale=scale)
+    lse = torch.empty(160, 32, device="cuda")
+    assert torch.equal(sgr.sgr_kv_attention(cache, batch, q.cuda(), scale=scale, lse=lse), out)
+    k, v = pr.values(0), pr.values(1)
+    want, mag = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
+    t = torch.arange(1500)
+    for b in range(4):
+        pages, rows = pr.block_table[b].long()[t // 64], slice(40 * b, 40 * b + 40)
+        hidden = t > torch.arange(1460, 1500)[:, None]
+        for h in range(32):
+            s = (q[rows, h].double() @ k[pages, h // 4, t % 64].T * scale).masked_fill(hidden, -torch.inf)
+            assert 1 < float(s[:, :1460].std()) < 64
+            p = torch.softmax(s, -1)
+            want[rows, h] = p @ v[pages, h // 4, t % 64]
+            mag[rows, h] = p @ v[pages, h // 4, t % 64].abs()
+    ref.check_attention(out, want, mag)
+    with pytest.raises(AssertionError):  # (the call's choice is what this is about)
+        ref.check_attention(sgr.sgr_kv_attention(cache, batch, q.cuda(), scale=scale, flags=sgr.SGR_FLAG_KV_MANY_ROWS), want, mag)
