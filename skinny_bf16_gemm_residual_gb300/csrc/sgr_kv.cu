@@ -546,7 +546,8 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
                    const sgr_kv_mask& mask) {
   AttnPlan a;
   const long long group = q_heads / c.heads, rows = (b.max_new > 0 ? b.max_new : 1) * group;
-  long long tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  const long long table_tiles = ((long long)b.max_pages * c.page_size + sgr::kAttnTile - 1) / sgr::kAttnTile;
+  long long tiles = table_tiles;
   if (mask.window > 0) {
     const long long seen = ((long long)mask.window + b.max_new) / sgr::kAttnTile + 2 + (mask.sinks + sgr::kAttnTile - 1LL) / sgr::kAttnTile;
     if (seen < tiles) tiles = seen;
@@ -568,7 +569,7 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
       break;
     }
   // The 256-row kernel takes some 1.25 times a 32-row unit's time for eight times
-  // the rows, but 8 units' time to begin and end.  Measured, small tiles against
+  // the rows, but some 8 units' time to begin and end.  Measured, small tiles against
   // 256 rows, one sequence of the length and the others of 1 to it, 28 heads of 128
   // over 4: 118 and 96 us (96 of 3000, 35 rows a head each), 22.4 and 23.7 (4 of
   // 3000, 126 rows), 57 and 31 (16 of 3000, 126 rows), 34 and 26 (8 of 4000, 112
@@ -580,11 +581,19 @@ AttnPlan attn_plan(int sms, const sgr_kv_cache& c, const sgr_kv_batch& b, int q_
   // rows), 54 and 37 (3 of 20000, 96 rows).
   // It also sees a query's small elements in fewer bits (sgr_attention.h).  Calls
   // over all positions up to a row's own, or the last of them, keep the few-row
-  // kernel's longer, where it gives up to a third of its speed: rows of 36 to 64 in
-  // the figures above, and the 160 rows.  (So a log-sum-exp changes no output.)
+  // kernel's longer, whatever their window, at up to a third of the speed: rows of
+  // 36 to 64 in the figures above, and the 160 rows.  (So a log-sum-exp changes no
+  // output.)  Of those that do not, short windows take the few-row kernel: 15.4 and
+  // 15.7 us (8 of 4000, 112 rows, window 256: gain 2.3), 19.4 and 21.1 (one of 30000,
+  // 448 rows, 1024: 3.0), but 23.3 and 18.9 (8 of 4000, 1024: 5.8), 32 and 24 (16 of
+  // 3000, 126 rows, 512: 6.9), 31 and 33 (one of 30000, 4096: 10), 50 and 24 (32 of
+  // 9000, 112 rows, 512: 14).
   const bool plain = !mask.tree && !(mask.window > 0 && mask.sinks > 0);
-  const double unit = !plain ? 1.25 : c.head_dim == 64 ? 2.4 : 1.75, begin = plain ? 12.0 : 8.0;
-  const bool gains = (double)tiles * ((double)row_tiles(32) - unit * (double)row_tiles(sgr::kRowsNT)) > begin * sms;
+  auto gain = [&](long long t, double unit) {  // 32-row units that an SM saves
+    return (double)t * ((double)row_tiles(32) - unit * (double)row_tiles(sgr::kRowsNT)) / sms;
+  };
+  const bool gains = plain ? gain(table_tiles, c.head_dim == 64 ? 2.4 : 1.75) > 12.0 && gain(tiles, 1.25) > 5.0
+                           : gain(tiles, 1.25) > 8.0;
   if ((flags & SGR_FLAG_KV_MANY_ROWS) || (gains && !(flags & SGR_FLAG_KV_FEW_ROWS))) a.nt = sgr::kRowsNT;
   // (resident CTAs)
   const long long ctas = a.nt >= 32 ? sms : 2LL * sms, items = row_tiles(a.nt);

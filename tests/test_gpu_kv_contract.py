@@ -219,3 +219,17 @@ def test_plain_calls_of_medium_row_counts_keep_small_elements():
     ref.check_attention(out, want, mag)
     with pytest.raises(AssertionError):  # (the call's choice is what this is about)
         ref.check_attention(sgr.sgr_kv_attention(cache, batch, q.cuda(), scale=scale, flags=sgr.SGR_FLAG_KV_MANY_ROWS), want, mag)
+
+
+@pytest.mark.parametrize("window,many", [(0, True), (4000, True), (512, True), (64, False)])
+def test_choice_of_plain_calls_under_windows(window, many):
+    """A window takes no call that has many rows away from the kernel for them,
+    unless it is so short that there is next to nothing to do."""
+    pr = ref.Problem(64, 64, 4, [3000] * 3 + [700] * 13, [18] * 16, seed=1)
+    q = pr.randn(pr.tokens, 28, 64).bfloat16().cuda()
+    cache, batch = pr.cache(sgr), pr.batch(sgr)
+    out, forced = (sgr.sgr_kv_attention(cache, batch, q, window=window, flags=f)
+                   for f in (0, sgr.SGR_FLAG_KV_MANY_ROWS if many else sgr.SGR_FLAG_KV_FEW_ROWS))
+    assert torch.equal(out, forced)
+    other = sgr.sgr_kv_attention(cache, batch, q, window=window, flags=sgr.SGR_FLAG_KV_FEW_ROWS if many else sgr.SGR_FLAG_KV_MANY_ROWS)
+    assert not torch.equal(out, other)
