@@ -481,14 +481,23 @@ __global__ void __launch_bounds__(kAttnTile) kv_mass_join_kernel(const MassParam
   const long long at = mass_part<NT>(mp, b, s.row0, 0, h) + pos, step = (long long)p.cache.heads * mp.tiles * kAttnTile;
   float w = 0.f;
   bool any = false;
-#pragma unroll 4
-  for (int j = 0; j * NT < s.n * p.group; ++j) {
-    const AttnItem it = attn_item<NT, true>(p, s, j);
-    // (Position by position: a tile that the rows see a part of may hold pages that
-    // none of them sees, whose table entries may be anything.)
-    if (pos >= it.thi || (pos < it.tlo && pos >= p.sinks)) continue;
-    w += mp.part[at + j * step];
-    any = true;
+  // Eight sums are read at once, those that are not there from the last row tile's
+  // place.  (Position by position: a tile that the rows see a part of may hold pages
+  // that none of them sees, whose table entries may be anything.)
+  constexpr int kRun = 8;
+  const int count = (s.n * p.group + NT - 1) / NT;
+  for (int j0 = 0; j0 < count; j0 += kRun) {
+    float x[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) x[k] = mp.part[at + min(j0 + k, count - 1) * step];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const AttnItem it = attn_item<NT, true>(p, s, j0 + k);
+      if (j0 + k < count && pos < it.thi && (pos >= it.tlo || pos < p.sinks)) {
+        w += x[k];
+        any = true;
+      }
+    }
   }
   const int page = any ? p.batch.table[(long long)b * p.batch.table_stride + (pos >> p.cache.page_shift)] : -1;
   if (page < 0 || page >= p.cache.num_pages) return;  // (recorded by the kernel before)
