@@ -54,6 +54,7 @@ _pack_masses = struct.Struct("@Pqq").pack
 assert struct.calcsize("@Pqq") == ctypes.sizeof(sgr_kv_masses)
 _pack_eviction = struct.Struct("@PPPPqiiii").pack
 assert struct.calcsize("@PPPPqiiii") == ctypes.sizeof(sgr_kv_eviction)
+_NOT_32 = "window, sinks, first and recent must be whole numbers of 32 bits"
 
 
 def _check(rc: int, what: str) -> None:
@@ -271,17 +272,13 @@ def sgr_qk_norm_rope(q, k, positions, rope: RopeNorm, q_out=None, k_out=None, fl
     return q_out, k_out
 
 
-def _pack(pack, what: str, *fields) -> bytes:
-    try:
-        return pack(*fields)
-    except struct.error:
-        raise ValueError(f"{what} must be whole numbers of 32 bits") from None
-
-
 def _mask(batch, window: int, sinks: int, tree, index: int) -> bytes:
     """The sgr_kv_mask of these arguments."""
     if tree is None:
-        return _pack(_pack_mask, "window and sinks", 0, 0, 0, window, sinks, 0)
+        try:
+            return _pack_mask(0, 0, 0, window, sinks, 0)
+        except struct.error:
+            raise ValueError(_NOT_32) from None
     if tree.dtype is not torch.int64 or tree.dim() != 2 or (tree.shape[1] > 1 and tree.stride(1) != 1):
         raise ValueError("tree must be a 2-D int64 tensor [tokens, words] with unit inner stride")
     if tree.get_device() != index:
@@ -289,8 +286,10 @@ def _mask(batch, window: int, sinks: int, tree, index: int) -> bytes:
     tokens, words = tree.shape
     if tokens != batch.tokens or 64 * words < batch.max_new:
         raise ValueError(f"tree must be [{batch.tokens}, at least {-(-batch.max_new // 64)}], got {list(tree.shape)}")
-    return _pack(_pack_mask, "window and sinks", tree.data_ptr(), tree.stride(0) if tokens > 1 else words, words, window,
-                 sinks, 0)
+    try:
+        return _pack_mask(tree.data_ptr(), tree.stride(0) if tokens > 1 else words, words, window, sinks, 0)
+    except struct.error:
+        raise ValueError(_NOT_32) from None
 
 
 def sgr_kv_append(cache: KvCache, batch: KvBatch, k, v, rope: RopeNorm, q=None, q_out=None, flags: int = 0,
@@ -365,7 +364,7 @@ def sgr_kv_attention(cache: KvCache, batch: KvBatch, q, out=None, scale: float |
         scale = shape[2] ** -0.5
     if sinks == 0 and tree is None and lse is None:
         if window > 0x7fffffff:  # (ctypes would take its lower bits)
-            raise ValueError("window and sinks must be whole numbers of 32 bits")
+            raise ValueError(_NOT_32)
         _launch(index, stream, "sgr_kv_attention", load().sgr_kv_attention, cache.ref, batch.ref, hq, ho, scale, window,
                 workspace.data_ptr(), workspace.nbytes, flags)
         return out
@@ -446,8 +445,11 @@ def sgr_kv_evict(cache: KvCache, batch: KvBatch, mass, keep, new_table, first: i
             raise ValueError(f"{name} must be a contiguous int32 tensor {list(shapes[name])} on cuda:{index}")
     new_len, kept = given["new_len"], given["kept"]
     _on(index, batch.index, "sgr_kv_evict")
-    ev = _pack(_pack_eviction, "first and recent", keep.data_ptr(), new_table.data_ptr(), kept.data_ptr(),
-               new_len.data_ptr(), new_table.stride(0) if batch.batch > 1 else pages, pages, first, recent, 0)
+    try:
+        ev = _pack_eviction(keep.data_ptr(), new_table.data_ptr(), kept.data_ptr(), new_len.data_ptr(),
+                            new_table.stride(0) if batch.batch > 1 else pages, pages, first, recent, 0)
+    except struct.error:
+        raise ValueError(_NOT_32) from None
     _launch(index, stream, "sgr_kv_evict", load().sgr_kv_evict, cache.ref, batch.ref, _masses(mass, cache), ev, flags)
     return new_len, kept
 

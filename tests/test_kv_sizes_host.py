@@ -37,5 +37,3 @@ def test_numbers_past_32_bits_are_value_errors():
         with pytest.raises(ValueError, match="32 bits"):
             attention._mask(None, window, sinks, None, 0)
     assert len(attention._mask(None, (1 << 31) - 1, (1 << 31) - 1, None, 0)) == 32
-    with pytest.raises(ValueError, match="first and recent"):
-        attention._pack(attention._pack_eviction, "first and recent", 0, 0, 0, 0, 1, 1, 1 << 31, 0, 0)
