@@ -225,7 +225,10 @@ __device__ __forceinline__ void attn_walk(Ctl& c, const AttnParams& p, const CUt
     const int b_last = min(b_first + per_lane, p.batch.batch);
     int mine = 0, units = 0;
     int tiles = 0;  // row tiles of a sequence, the most of any
-    constexpr bool kSeveral = NT >= 32;  // (rows that fit a smaller tile are in one)
+    // (Tiles of fewer rows are one a sequence, or a few where the work does not fill
+    // the GPU: the plan takes them while row tiles times tiles are at most two for
+    // each SM.)
+    constexpr bool kSeveral = NT >= 32;
     if (kSeveral && p.reuse && per_lane == 1) {
       if (b_first < b_last) s = kv_seq(p.batch, ps, b_first, p.err);
       tiles = __reduce_max_sync(0xffffffffu, (s.n * p.group + NT - 1) / NT);

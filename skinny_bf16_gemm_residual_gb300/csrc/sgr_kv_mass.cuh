@@ -23,7 +23,11 @@
 // positions 5.4 us in a graph (launch, walk, first page).  For many rows a chain
 // of product, its sums and the next product in each of two CTAs an SM, issue slots
 // 55% taken (chunks of up to 500 tokens over 4001, 32 heads of 64 over 8, 87
-// million weights: 60 us; the exponentials alone would take some 19).
+// million weights: 59 us; the exponentials alone would take some 19).  In between
+// 32 sequences of up to 8000 with 20 rows a head 42 us (32 heads of 128 over 8,
+// 145 MB: 22 us at the copy peak), 8 of 5000 with 128 rows 35 (32 MB).  Registers
+// bound the two-group kernels: 80 for two CTAs an SM, 16 bytes of spills with 32
+// rows and 40 with 64.
 //
 // Rows that share a key/value head go in products of up to 64.  Up to 128 of
 // them, their queries all in shared memory, meet a tile of keys while it is
