@@ -233,3 +233,27 @@ def test_choice_of_plain_calls_under_windows(window, many):
     assert torch.equal(out, forced)
     other = sgr.sgr_kv_attention(cache, batch, q, window=window, flags=sgr.SGR_FLAG_KV_FEW_ROWS if many else sgr.SGR_FLAG_KV_MANY_ROWS)
     assert not torch.equal(out, other)
+
+
+@pytest.mark.parametrize("dim,page,heads,hk,lens,new", [
+    (128, 32, 4, 2, [13, 319], [2, 107]), (64, 16, 24, 2, [2000] * 5, [30] * 5), (128, 64, 28, 4, [9000], [7]),
+    (64, 64, 32, 8, [1500] * 4, [40] * 4), (64, 64, 8, 8, [4000] * 40, [5] * 40)])
+def test_workspace_is_enough_for_trees_and_windows(dim, page, heads, hk, lens, new):
+    """One workspace for calls with and without trees, windows, sinks and a
+    log-sum-exp, which may take different kernels and row tiles."""
+    pr = ref.Problem(dim, page, hk, [1] * len(lens), [1] * len(lens), extra_pages=4)  # (no position is looked at)
+    cache = pr.cache(sgr)
+    table = torch.zeros(len(lens), -(-max(lens) // page), dtype=torch.int32, device="cuda")
+    start = torch.zeros(len(lens) + 1, dtype=torch.int32, device="cuda")  # no rows
+    batch = sgr.KvBatch(table, torch.zeros(len(lens), dtype=torch.int32, device="cuda"), start, tokens=sum(new), max_new=max(new))
+    q = torch.zeros(sum(new), heads, dim, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(sum(new), heads, device="cuda")
+    words = torch.zeros(sum(new), -(-max(new) // 64), dtype=torch.int64, device="cuda")
+    for flags in (0, sgr.SGR_FLAG_KV_FEW_ROWS, sgr.SGR_FLAG_KV_MANY_ROWS):
+        work = sgr.kv_attention_workspace(cache, batch, heads, flags)
+        for window in (0, 1, 30, 300, 1000, 4000, 100000):
+            for sinks in (0, 4, 600):
+                for tree in (None, words):
+                    for stat in (None, lse):
+                        sgr.sgr_kv_attention(cache, batch, q, window=window, sinks=sinks, tree=tree, lse=stat, workspace=work,
+                                             flags=flags)
